@@ -469,8 +469,9 @@ def _own(s, kind):
     if kind == "extend":
         return K.gqa_extend(cache, s["table"], s["seq_lens"],
                             s["max_seq_len"], s["q"], s["row_start"],
-                            window=case["window"])
-    return K.gqa_decode(cache, s["table"], s["seq_lens"], s["max_seq_len"],
+                            s["max_rows"], window=case["window"])
+    # one new token a sequence: row b belongs to sequence b
+    return K.gqa_extend(cache, s["table"], s["seq_lens"], s["max_seq_len"],
                         s["q"], window=case["window"])
 
 
