@@ -11,6 +11,7 @@ Cache layout (per layer): K and V tensors [num_blocks][n_kv][block_size]
 [num_blocks][n_kv][block_size][head_dim/2 + head_dim/16] bytes of MXFP4 rows
 (torch.uint8; include/kvd.h gives the row format).
 """
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import Optional
@@ -22,6 +23,8 @@ __all__ = ["PagedCache", "kv_append", "gqa_decode", "mla_decode",
            "indexer_topk", "indexer_pool", "indexer_topk_pool",
            "BlockPool", "copy_blocks",
            "sparse_decode", "workspace_size",
+           "RopePlan", "rope_plan", "rope", "kv_write", "kv_read",
+           "gqa_extend", "extend_workspace_size",
            "bytes_per_token", "device_error", "launch_count", "set_tuning",
            "KvdError",
            "OP_GQA_DECODE", "OP_MLA_DECODE", "OP_INDEXER_TOPK",
@@ -338,6 +341,318 @@ def sparse_decode(cache, block_table, seq_lens, max_seq_len, indices, q,
                                   _ptr(indices), k, _ptr(q), n_h,
                                   float(scale or 0.0), _ptr(out), _ptr(lse),
                                   _ptr(ws), ws.numel(), _stream(stream)))
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# the prompt path (include/kvd_prompt.h)
+# ---------------------------------------------------------------------------
+def _one_device(first, *tensors):
+    """The device of a call, all of whose tensors must lie on it."""
+    for t in tensors:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device} in "
+                             "one call")
+    return first.device
+
+
+@contextlib.contextmanager
+def _launching(device, stream):
+    """The stream of a call on `device` (made current for the call, as is
+    the stream, so that what the call allocates belongs to that stream)."""
+    import torch
+    if stream is not None and stream.device != device:
+        raise ValueError(f"a stream of {stream.device} for tensors on "
+                         f"{device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield _stream(None)
+        else:
+            with torch.cuda.stream(stream):
+                yield _stream(stream)
+
+
+def _rows3(t, name, heads=None, width=None):
+    """bf16 [rows][heads][width] with any strides but a unit innermost one."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [rows][heads][width] with "
+                         "contiguous vectors")
+    if heads is not None and t.shape[1] != heads:
+        raise ValueError(f"{name} must have {heads} heads, got {t.shape[1]}")
+    if width is not None and t.shape[2] != width:
+        raise ValueError(f"{name} must be {width} wide, got {t.shape[2]}")
+    return _native.KvdRows(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0),
+                           t.stride(1))
+
+
+def _new_rows(t):
+    import torch
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+@dataclass
+class RopePlan:
+    """Frequencies and axes of rotary positions, on the device (rope_plan
+    makes one; a model keeps it)."""
+    turns: "torch.Tensor"            # int64 [d_rot / 2]: 64-bit turn fractions
+    axis: Optional["torch.Tensor"]   # uint8 [d_rot / 2], or None: one axis
+    d_rot: int
+    n_axes: int
+    pairing: str                     # "half" | "adjacent"
+
+    def struct(self, inverse=False):
+        import torch
+        _need(self.turns, "plan.turns", torch.int64, self.d_rot // 2)
+        if self.axis is not None:
+            _need(self.axis, "plan.axis", torch.uint8, self.d_rot // 2)
+        return _native.KvdRopePlan(
+            _ptr(self.turns), _ptr(self.axis), self.d_rot, self.n_axes,
+            _PAIRINGS[self.pairing], int(bool(inverse)))
+
+
+_PAIRINGS = {"half": 0, "adjacent": 1}
+
+
+def rope_axes(d_rot, sections, interleave=False):
+    """Axis of each of the d_rot / 2 pairs. ``sections``: pairs per axis,
+    summing to d_rot / 2. In order of the axes, or (interleave) the axes in
+    turn, each while pairs of its section are left."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 4 or min(sections) < 0:
+        raise ValueError("sections: 1 to 4 counts of pairs")
+    if sum(sections) * 2 != d_rot:
+        raise ValueError(f"sections {sections} do not sum to d_rot / 2 = "
+                         f"{d_rot / 2}")
+    if not interleave:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, axes = list(sections), []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                left[a] -= 1
+                axes.append(a)
+    return axes
+
+
+def rope_plan(d_rot, theta=10000.0, sections=None, interleave=False,
+              pairing="half", freqs=None, device=None):
+    """A RopePlan: pair i turns by theta^(-2 i / d_rot) radians a position,
+    or by ``freqs[i]`` (d_rot / 2 Python floats or a float64 tensor; scaled
+    frequencies for long contexts go in here). ``sections`` and
+    ``interleave`` give the pairs' axes (rope_axes); None: one axis.
+    ``pairing``: "half" (channels i and i + d_rot / 2) or "adjacent"
+    (channels 2 i and 2 i + 1)."""
+    import numpy as np
+    import torch
+    d_rot = int(d_rot)
+    if d_rot < 2 or d_rot % 2:
+        raise ValueError(f"d_rot must be even and positive, got {d_rot}")
+    if pairing not in _PAIRINGS:
+        raise ValueError(f"pairing must be one of {sorted(_PAIRINGS)}")
+    if freqs is None:
+        f = [float(theta) ** (-2.0 * i / d_rot) for i in range(d_rot // 2)]
+    else:
+        f = [float(x) for x in freqs]
+        if len(f) != d_rot // 2:
+            raise ValueError(f"freqs must have {d_rot // 2} entries")
+    f = np.array(f, dtype=np.float64)
+    turns = np.empty(d_rot // 2, dtype=np.uint64)
+    check(lib().kvd_rope_turns(f.ctypes.data, f.size, turns.ctypes.data))
+    device = torch.device("cuda" if device is None else device)
+    axis = None
+    n_axes = 1
+    if sections is not None:
+        axes = rope_axes(d_rot, sections, interleave)
+        n_axes = len(sections)
+        axis = torch.tensor(axes, dtype=torch.uint8, device=device)
+    return RopePlan(torch.from_numpy(turns.view(np.int64)).to(device), axis,
+                    d_rot, n_axes, pairing)
+
+
+def _positions(plan, positions, rows):
+    """positions int32 [n_axes][rows] ([rows] for one axis), contiguous."""
+    import torch
+    _need(positions, "positions", torch.int32, plan.n_axes * rows)
+    if positions.dim() > 2 or positions.shape[-1] != rows:
+        raise ValueError(f"positions must be [{plan.n_axes}][{rows}]")
+    return positions
+
+
+def rope(plan, positions, q, k=None, q_out=None, k_out=None, inverse=False,
+         stream=None):
+    """Rotate q [rows][n_h][d] (and k [rows][n_kv][d]) bf16 to positions
+    int32 [n_axes][rows]: returns (q_out, k_out). Any strides with
+    contiguous vectors; q_out=q rotates in place. ``inverse`` turns back
+    (also the gradient of a rotation)."""
+    qs = _rows3(q, "q")
+    ks = None if k is None else _rows3(k, "k", width=q.shape[2])
+    if k_out is not None and k is None:
+        raise ValueError("k_out without k")
+    r = plan.struct(inverse)
+    _positions(plan, positions, q.shape[0])
+    dev = _one_device(q, k, q_out, k_out, positions, plan.turns, plan.axis)
+    with _launching(dev, stream) as s:
+        if q_out is None:
+            q_out = _new_rows(q)
+        if k is not None and k_out is None:
+            k_out = _new_rows(k)
+        qo = _rows3(q_out, "q_out", q.shape[1], q.shape[2])
+        ko = None if k is None else _rows3(k_out, "k_out", k.shape[1],
+                                           k.shape[2])
+        check(lib().kvd_rope(ctypes.byref(r), _ptr(positions), q.shape[0],
+                             q.shape[2], ctypes.byref(qs), ctypes.byref(qo),
+                             ks and ctypes.byref(ks), ko and ctypes.byref(ko),
+                             s))
+    return q_out, k_out
+
+
+def _ragged(cache, block_table, start, row_start):
+    import torch
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][max_blocks_per_seq]")
+    B = block_table.shape[0]
+    _need(start, "start", torch.int32, B)
+    _need(row_start, "row_start", torch.int32, B + 1)
+    return B
+
+
+def kv_write(cache, block_table, start, row_start, k_new, v_new=None,
+             rope=None, positions=None, q=None, q_out=None, stream=None):
+    """Write ragged new rows k_new (and v_new) [rows][n_kv][head_dim] bf16
+    into the cache: rows row_start[b] .. row_start[b + 1] - 1 go to positions
+    start[b] .. of sequence b. With ``rope`` (a RopePlan) and ``positions``
+    the keys are rotated on the way, and so is q [rows][n_h][head_dim] if
+    given: returns q_out (None without q; q_out=q rotates in place)."""
+    c = cache.struct()
+    B = _ragged(cache, block_table, start, row_start)
+    ks = _rows3(k_new, "k_new", cache.n_kv, cache.head_dim)
+    vs = None
+    if v_new is not None:
+        vs = _rows3(v_new, "v_new", cache.n_kv, cache.head_dim)
+    qs = qo = r = None
+    if rope is not None:
+        r = rope.struct()
+        _positions(rope, positions, k_new.shape[0])
+    elif q is not None or q_out is not None or positions is not None:
+        raise ValueError("q and positions need rope")
+    if q is not None:
+        qs = _rows3(q, "q", width=cache.head_dim)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    dev = _one_device(cache.k, cache.v, block_table, start, row_start, k_new,
+                      v_new, positions, q, q_out,
+                      rope and rope.turns, rope and rope.axis,
+                      cache.k_inv_scale, cache.v_inv_scale)
+    with _launching(dev, stream) as s:
+        if q is not None:
+            if q_out is None:
+                q_out = _new_rows(q)
+            qo = _rows3(q_out, "q_out", q.shape[1], q.shape[2])
+        check(lib().kvd_kv_write(
+            ctypes.byref(c), _ptr(block_table), block_table.shape[1],
+            _ptr(start), _ptr(row_start), B, ctypes.byref(ks),
+            vs and ctypes.byref(vs), r and ctypes.byref(r), _ptr(positions),
+            k_new.shape[0], qs and ctypes.byref(qs), qo and ctypes.byref(qo),
+            s))
+    return q_out
+
+
+def kv_read(cache, block_table, start, row_start, rows, k_out=None,
+            v_out=None, stream=None):
+    """Read positions start[b] .. of every sequence back as bf16 rows
+    row_start[b] .. row_start[b + 1] - 1: returns (k, v) [rows][n_kv]
+    [head_dim] (v None for a K-only cache). ``rows``: rows of the outputs;
+    outputs passed in may have any strides with contiguous vectors. Rows of
+    new outputs that no sequence owns are not initialised."""
+    import torch
+    c = cache.struct()
+    B = _ragged(cache, block_table, start, row_start)
+    dev = _one_device(cache.k, cache.v, block_table, start, row_start, k_out,
+                      v_out, cache.k_scale, cache.v_scale)
+    shape = (int(rows), cache.n_kv, cache.head_dim)
+    with _launching(dev, stream) as s:
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if cache.v is None:
+            if v_out is not None:
+                raise ValueError("v_out for a K-only cache")
+        elif v_out is None:
+            v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        ks = _rows3(k_out, "k_out", *shape[1:])
+        vs = None if v_out is None else _rows3(v_out, "v_out", *shape[1:])
+        if ks.rows != shape[0] or (vs is not None and vs.rows != shape[0]):
+            raise ValueError(f"outputs must have {shape[0]} rows")
+        check(lib().kvd_kv_read(
+            ctypes.byref(c), _ptr(block_table), block_table.shape[1],
+            _ptr(start), _ptr(row_start), B, ctypes.byref(ks),
+            vs and ctypes.byref(vs), s))
+    return k_out, v_out
+
+
+def extend_workspace_size(cache, block_table, seq_lens, max_seq_len, rows,
+                          n_h, max_rows=1, window=0):
+    """Workspace bytes of a gqa_extend call (kvd_extend_workspace_size)."""
+    import torch
+    c = cache.struct()
+    s = _seqs(block_table, seq_lens, max_seq_len, window=window)
+    out = ctypes.c_size_t(0)
+    with torch.cuda.device(block_table.device):
+        check(lib().kvd_extend_workspace_size(
+            ctypes.byref(c), ctypes.byref(s), int(rows), int(max_rows), n_h,
+            ctypes.byref(out)))
+    return out.value
+
+
+def gqa_extend(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
+               max_rows=1, scale=None, out=None, lse=None, workspace=None,
+               want_lse=True, stream=None, window=0, window_start=None):
+    """Attention of new tokens over an MXFP4 cache that holds them: q
+    [rows][n_h][head_dim] bf16 (contiguous vectors) -> (out [rows][n_h]
+    [head_dim] bf16, lse [rows][n_h] fp32). Rows row_start[b] ..
+    row_start[b + 1] - 1 (int32 [batch + 1]) are the last positions of
+    sequence b, at most ``max_rows`` of them; without row_start row b is
+    sequence b's one new token. Each row attends to the positions up to its
+    own, within ``window`` and from ``window_start`` if given."""
+    import torch
+    qs = _rows3(q, "q", width=cache.head_dim)
+    c = cache.struct()
+    s = _seqs(block_table, seq_lens, max_seq_len, 0, window, window_start)
+    rows, n_h = q.shape[0], q.shape[1]
+    if row_start is not None:
+        _need(row_start, "row_start", torch.int32, seq_lens.numel() + 1)
+    dev = _one_device(q, cache.k, cache.v, block_table, seq_lens, row_start,
+                      window_start, out, lse, workspace)
+    with _launching(dev, stream) as st:
+        if out is None:
+            out = torch.empty((rows, n_h, cache.head_dim),
+                              dtype=torch.bfloat16, device=dev)
+        _need(out, "out", torch.bfloat16, rows * n_h * cache.head_dim)
+        if lse is None and want_lse:
+            lse = torch.empty((rows, n_h), dtype=torch.float32, device=dev)
+        if lse is not None:
+            _need(lse, "lse", torch.float32, rows * n_h)
+        nbytes = 0
+        if workspace is not None:
+            _need(workspace, "workspace", torch.uint8)
+            nbytes = workspace.numel()
+        else:
+            need = ctypes.c_size_t(0)
+            check(lib().kvd_extend_workspace_size(
+                ctypes.byref(c), ctypes.byref(s), rows, int(max_rows), n_h,
+                ctypes.byref(need)))
+            nbytes = need.value
+            if nbytes:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        check(lib().kvd_gqa_extend(
+            ctypes.byref(c), ctypes.byref(s), _ptr(row_start), int(max_rows),
+            ctypes.byref(qs), float(scale or 0.0), _ptr(out), _ptr(lse),
+            _ptr(workspace), nbytes, st))
     return out, lse
 
 

@@ -14,6 +14,7 @@ ROOT = os.path.dirname(PKG)
 LIB_PATH = os.path.join(PKG, "libkvd.so")
 INPUTS_LIB_PATH = os.path.join(PKG, "libkvd_inputs.so")
 HEADER = os.path.join(ROOT, "include", "kvd.h")
+PROMPT_HEADER = os.path.join(ROOT, "include", "kvd_prompt.h")
 
 c_void_p = ctypes.c_void_p
 c_int32 = ctypes.c_int32
@@ -37,12 +38,26 @@ class KvdSeqs(ctypes.Structure):
                 ("window", c_int32), ("window_start", c_void_p)]
 
 
+class KvdRows(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("rows", c_int32), ("heads", c_int32),
+                ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class KvdRopePlan(ctypes.Structure):
+    _fields_ = [("turns", c_void_p), ("axis", c_void_p), ("d_rot", c_int32),
+                ("n_axes", c_int32), ("pairing", c_int32),
+                ("inverse", c_int32)]
+
+
 STATUS = {0: "KVD_OK", 1: "KVD_ERR_NULL", 2: "KVD_ERR_SHAPE",
           3: "KVD_ERR_UNSUPPORTED", 4: "KVD_ERR_CAPACITY",
           5: "KVD_ERR_WORKSPACE", 6: "KVD_ERR_CUDA"}
 
 _PCACHE = ctypes.POINTER(KvdCache)
 _PSEQS = ctypes.POINTER(KvdSeqs)
+_PROWS = ctypes.POINTER(KvdRows)
+_PROPE = ctypes.POINTER(KvdRopePlan)
 
 _SIGS = {
     "kvd_version": (c_int32, []),
@@ -92,6 +107,20 @@ _SIGS = {
                                                 ctypes.POINTER(c_int32)]),
     "kvd_copy_blocks": (c_int32, [_PCACHE, c_void_p, c_void_p, c_int32,
                                   c_void_p]),
+    "kvd_rope_turns": (c_int32, [c_void_p, c_int32, c_void_p]),
+    "kvd_rope": (c_int32, [_PROPE, c_void_p, ctypes.c_int64, c_int32, _PROWS,
+                           _PROWS, _PROWS, _PROWS, c_void_p]),
+    "kvd_kv_write": (c_int32, [_PCACHE, c_void_p, c_int32, c_void_p, c_void_p,
+                               c_int32, _PROWS, _PROWS, _PROPE, c_void_p,
+                               ctypes.c_int64, _PROWS, _PROWS, c_void_p]),
+    "kvd_kv_read": (c_int32, [_PCACHE, c_void_p, c_int32, c_void_p, c_void_p,
+                              c_int32, _PROWS, _PROWS, c_void_p]),
+    "kvd_gqa_extend": (c_int32, [_PCACHE, _PSEQS, c_void_p, c_int32, _PROWS,
+                                 c_float, c_void_p, c_void_p, c_void_p,
+                                 c_size_t, c_void_p]),
+    "kvd_extend_workspace_size": (c_int32, [_PCACHE, _PSEQS, c_int32, c_int32,
+                                            c_int32,
+                                            ctypes.POINTER(c_size_t)]),
     "kvd_workspace_size": (c_int32, [c_int32, _PCACHE, _PSEQS, c_int32,
                                      c_int32, ctypes.POINTER(c_size_t)]),
 }
@@ -147,9 +176,9 @@ def check(status):
         raise KvdError(status, msg)
 
 
-def header_functions():
-    """Names of the functions include/kvd.h declares."""
-    with open(HEADER) as f:
+def header_functions(header=HEADER):
+    """Names of the functions a header (include/kvd.h) declares."""
+    with open(header) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(kvd_[a-z_0-9]+)\s*\(", text)))

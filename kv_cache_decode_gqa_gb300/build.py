@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_SOURCES = ["api.cu", "append.cu", "decode_simt.cu", "noalloc.cu",
                "decode_mma.cu", "decode_wide.cu", "decode_latent_tc.cu",
                "decode_gather_tc.cu",
-               "indexer.cu", "block_pool.cu"]
+               "indexer.cu", "block_pool.cu", "rows.cu", "extend_few.cu",
+               "extend_tc.cu"]
 INPUTS_SOURCES = ["inputs_fill.cu"]
 LIB = os.path.join(PKG, "libkvd.so")
 INPUTS_LIB = os.path.join(PKG, "libkvd_inputs.so")
@@ -54,8 +55,9 @@ def _stamp(sources):
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode())
             h.update(f.read())
-    with open(os.path.join(INCLUDE, "kvd.h"), "rb") as f:
-        h.update(f.read())
+    for name in sorted(os.listdir(INCLUDE)):
+        with open(os.path.join(INCLUDE, name), "rb") as f:
+            h.update(f.read())
     return h.hexdigest()
 
 

@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "kvd.h"
+#include "kvd_prompt.h"
 #include "kvd_internal.h"
 
 namespace {
@@ -917,6 +918,516 @@ kvd_status kvd_indexer_pool(const kvd_seqs *seqs, const int32_t *indices,
   return launched(kvd::launch_indexer_pool(
                       p, reinterpret_cast<cudaStream_t>(stream)),
                   "indexer_pool");
+}
+
+}  // extern "C"
+
+// ===========================================================================
+// the prompt path (kvd_prompt.h)
+// ===========================================================================
+namespace {
+
+// Rows of a ragged tensor: `out` ones may not overlap one another.
+kvd_status check_rows(const kvd_rows *r, int d, bool out, const char *what,
+                      const char *name) {
+  if (r->rows < 0 || r->heads < 1)
+    return fail(KVD_ERR_SHAPE, "%s: %s needs rows >= 0 and heads >= 1", what,
+                name);
+  if (r->rows > 0 && !r->data)
+    return fail(KVD_ERR_NULL, "%s: %s->data is NULL", what, name);
+  if (!aligned(r->data, 2))
+    return fail(KVD_ERR_SHAPE, "%s: %s->data is not 2-byte aligned", what,
+                name);
+  const int64_t lim = int64_t(1) << 40;
+  if (r->row_stride < 0 || r->head_stride < 0 || r->row_stride > lim ||
+      r->head_stride > lim)
+    return fail(KVD_ERR_SHAPE, "%s: %s strides must be in [0, 2^40]", what,
+                name);
+  if (!out) return KVD_OK;
+  const int64_t rs = r->row_stride, hs = r->head_stride;
+  const bool heads_fit = r->heads == 1 || hs >= d;
+  const bool rows_fit = r->rows <= 1 || rs >= d;
+  const bool apart = r->heads == 1 || r->rows <= 1 ||
+                     rs >= (int64_t)(r->heads - 1) * hs + d ||
+                     hs >= (int64_t)(r->rows - 1) * rs + d;
+  if (!heads_fit || !rows_fit || !apart)
+    return fail(KVD_ERR_SHAPE, "%s: rows of %s overlap one another", what,
+                name);
+  return KVD_OK;
+}
+
+bool rows_aligned16(const kvd_rows *r) {
+  return aligned(r->data, 16) && r->row_stride % 8 == 0 &&
+         r->head_stride % 8 == 0;
+}
+
+// A rotation's input and output pair.
+kvd_status check_rotated(const kvd_rows *in, const kvd_rows *out, int d,
+                         const char *what, const char *name) {
+  if (!in || !out)
+    return fail(KVD_ERR_NULL, "%s: %s and %s_out go together", what, name,
+                name);
+  kvd_status st = check_rows(in, d, false, what, name);
+  if (st != KVD_OK) return st;
+  st = check_rows(out, d, true, what, name);
+  if (st != KVD_OK) return st;
+  if (in->rows != out->rows || in->heads != out->heads)
+    return fail(KVD_ERR_SHAPE, "%s: %s and %s_out have different shapes", what,
+                name, name);
+  if (in->rows > 0 && in->data == out->data &&
+      (in->row_stride != out->row_stride ||
+       in->head_stride != out->head_stride))
+    return fail(KVD_ERR_SHAPE, "%s: %s_out in place needs the strides of %s",
+                what, name, name);
+  return KVD_OK;
+}
+
+kvd_status check_rope(const kvd_rope_plan *r, const int32_t *positions,
+                      int64_t axis_stride, int d, int rows,
+                      const char *what) {
+  if (r->d_rot < 2 || r->d_rot % 2 != 0 || r->d_rot > d)
+    return fail(KVD_ERR_SHAPE, "%s: d_rot (%d) must be even, at least 2 and "
+                "at most the head width %d", what, r->d_rot, d);
+  if (r->d_rot > 1024 || r->n_axes < 1 || r->n_axes > 4)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: d_rot up to 1024 and 1 to 4 axes",
+                what);
+  if (r->pairing != KVD_PAIR_HALF && r->pairing != KVD_PAIR_ADJACENT)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: unknown pairing %d", what,
+                r->pairing);
+  if (r->inverse != 0 && r->inverse != 1)
+    return fail(KVD_ERR_SHAPE, "%s: inverse must be 0 or 1", what);
+  if (!r->turns || (rows > 0 && !positions))
+    return fail(KVD_ERR_NULL, "%s: turns and positions required", what);
+  if (!aligned(r->turns, 8) || !aligned(positions, 4))
+    return fail(KVD_ERR_SHAPE, "%s: turns or positions misaligned", what);
+  if (r->n_axes > 1 && axis_stride < rows)
+    return fail(KVD_ERR_SHAPE, "%s: axis_stride below the number of rows",
+                what);
+  return KVD_OK;
+}
+
+void set_rope(kvd::RowsParams &p, const kvd_rope_plan *r,
+              const int32_t *positions, int64_t axis_stride) {
+  p.rope.turns = r->turns;
+  p.rope.axis = r->axis;
+  p.rope.pos = positions;
+  p.rope.axis_stride = axis_stride;
+  p.rope.half = r->d_rot / 2;
+  p.rope.n_axes = r->n_axes;
+  p.rope.adjacent = r->pairing == KVD_PAIR_ADJACENT;
+  p.rope.inverse = r->inverse;
+  p.rope.on = 1;
+}
+
+void set_q(kvd::RowsParams &p, const kvd_rows *q, const kvd_rows *q_out) {
+  p.q = static_cast<const uint16_t *>(q->data);
+  p.q_rs = q->row_stride;
+  p.q_hs = q->head_stride;
+  p.q_out = static_cast<uint16_t *>(q_out->data);
+  p.qo_rs = q_out->row_stride;
+  p.qo_hs = q_out->head_stride;
+  p.n_h = q->heads;
+}
+
+// What kvd_kv_write and kvd_kv_read check alike.
+kvd_status check_paged_rows(const kvd_cache *c, int32_t max_blocks,
+                            const int32_t *block_table, const int32_t *start,
+                            const int32_t *row_start, int32_t batch,
+                            const char *what) {
+  if (batch < 0 || batch > 65535 || max_blocks < 1)
+    return fail(KVD_ERR_SHAPE, "%s: 0 <= batch <= 65535 and "
+                "max_blocks_per_seq >= 1 required", what);
+  if (c->head_dim % 8 != 0)
+    return fail(KVD_ERR_SHAPE, "%s: head_dim must be a multiple of 8", what);
+  if (batch > 0 && (!block_table || !start || !row_start))
+    return fail(KVD_ERR_NULL, "%s: block_table, start and row_start required",
+                what);
+  return KVD_OK;
+}
+
+kvd_status check_kv_rows(const kvd_cache *c, const kvd_rows *r, int rows,
+                         bool out, const char *what, const char *name) {
+  const kvd_status st = check_rows(r, c->head_dim, out, what, name);
+  if (st != KVD_OK) return st;
+  if (r->heads != c->n_kv || r->rows != rows)
+    return fail(KVD_ERR_SHAPE, "%s: %s must have %d rows of %d heads", what,
+                name, rows, c->n_kv);
+  if (!rows_aligned16(r))
+    return fail(KVD_ERR_SHAPE, "%s: %s must be 16-byte aligned with strides "
+                "that are multiples of 8", what, name);
+  return KVD_OK;
+}
+
+void set_paged(kvd::RowsParams &p, const kvd_cache *c, int32_t max_blocks,
+               const int32_t *block_table, const int32_t *start,
+               const int32_t *row_start, int32_t batch, int *err) {
+  p.k_cache = static_cast<uint8_t *>(c->k);
+  p.v_cache = static_cast<uint8_t *>(c->v);
+  p.k_inv = c->k_inv_scale;
+  p.v_inv = c->v_inv_scale;
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.block_table = block_table;
+  p.start = start;
+  p.row_start = row_start;
+  p.n_kv = c->n_kv;
+  p.d = c->head_dim;
+  p.dtype = c->dtype;
+  p.batch = batch;
+  p.max_blocks = max_blocks;
+  p.block_size = c->block_size;
+  p.num_blocks = c->num_blocks;
+  p.err = err;
+}
+
+struct ExtendPlan {
+  bool few = false;
+  kvd::ExtendParams p{};  // hp, n_splits, whole_units, chunks_per_split
+  int blocks = 0, splits = 1;
+  size_t ws_o_bytes = 0, ws_bytes = 0;
+};
+
+// Few (row, head) pairs a kv head: the stream-K kernel with one CTA per SM.
+// Else row blocks of 256 pairs: enough of them fill the SMs by themselves
+// (two waves and more); fewer are split over the positions into about four
+// waves of equal shares, so that ragged lengths level out.
+ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
+                       int max_rows, int n_h, int sms) {
+  ExtendPlan pl;
+  const int g = n_h / c->n_kv;
+  const int forced = g_decode_ctas.load(std::memory_order_relaxed);
+  if ((long)max_rows * g <= kvd::kFewRows) {
+    pl.few = true;
+    const int hp = kvd::extend_few_heads(c->n_kv, c->block_size);
+    const int ch = kvd::extend_few_chunk(hp);
+    const long units = (long)s->batch * (c->n_kv / hp);
+    long unit_chunks = (s->max_seq_len + ch - 1) / ch;
+    const long chunks = units * unit_chunks;
+    if (s->window > 0)
+      unit_chunks = std::min<long>(
+          unit_chunks, ((long)s->window + max_rows + ch - 2) / ch + 1);
+    pl.p.hp = hp;
+    long ctas = forced > 0 ? forced : sms;
+    if (forced <= 0 && units <= ctas &&
+        unit_chunks * ch <= kWholeUnitChunks * kvd::kStageRows) {
+      pl.p.whole_units = 1;
+      pl.p.n_splits = (int)std::max(units, 1L);
+      return pl;
+    }
+    ctas = std::max(1L, std::min(ctas, std::max(chunks, 1L)));
+    pl.p.n_splits = (int)ctas;
+    const size_t slots = (size_t)ctas * 2 * hp * kvd::kFewRows;
+    pl.ws_o_bytes = round_up(slots * 128 * 4, 256);
+    pl.ws_bytes = pl.ws_o_bytes + round_up(slots * 4, 256);
+    return pl;
+  }
+  const long pairs = (long)rows * g;
+  pl.blocks = (int)(pairs / kvd::kExtendRows + std::min(s->batch, rows));
+  const int ch = kvd::kExtendChunk;
+  long chunks = (s->max_seq_len + ch - 1) / ch;
+  if (s->window > 0)
+    chunks = std::min<long>(
+        chunks, ((long)s->window + kvd::kExtendRows / g + ch) / ch + 2);
+  const long ctas = (long)pl.blocks * c->n_kv;
+  const long want = forced > 0 ? forced : 4L * sms;
+  if (forced > 0 || ctas < 2L * sms) {
+    const long per = std::max(4L, (ctas * chunks + want - 1) / want);
+    if (per < chunks) {
+      pl.p.chunks_per_split = (int)per;
+      pl.splits = (int)((chunks + per - 1) / per);
+      const size_t n = (size_t)pl.splits * rows * n_h;
+      pl.ws_o_bytes = round_up(n * 128 * 4, 256);
+      pl.ws_bytes = pl.ws_o_bytes + round_up(n * 4, 256);
+    }
+  }
+  return pl;
+}
+
+kvd_status check_extend(const kvd_cache *c, const kvd_seqs *s, int rows,
+                        int max_rows, int n_h, bool lists,
+                        const char *what) {
+  kvd_status st = check_cache(c, true, what);
+  if (st != KVD_OK) return st;
+  st = check_seqs(s, c, what);
+  if (st != KVD_OK) return st;
+  if (c->dtype != KVD_MXFP4)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: an MXFP4 cache is required", what);
+  if (n_h < 1 || n_h % c->n_kv != 0)
+    return fail(KVD_ERR_SHAPE, "%s: n_h (%d) must be a positive multiple of "
+                "n_kv (%d)", what, n_h, c->n_kv);
+  if (n_h / c->n_kv > 128)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: group size %d above 128", what,
+                n_h / c->n_kv);
+  if (s->batch > 1024)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: at most 1024 sequences per call "
+                "(got %d)", what, s->batch);
+  if (rows < 0 || max_rows < 0)
+    return fail(KVD_ERR_SHAPE, "%s: rows and max_rows must be >= 0", what);
+  if (!lists && (rows != s->batch || max_rows != 1))
+    return fail(KVD_ERR_SHAPE, "%s: without row_start there is one row a "
+                "sequence (rows = batch, max_rows = 1)", what);
+  if ((long)rows * n_h >= (1L << 31) || (long)max_rows * n_h >= (1L << 31))
+    return fail(KVD_ERR_SHAPE, "%s: rows x n_h must be below 2^31", what);
+  return KVD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvd_status kvd_rope_turns(const double *freq, int32_t n, uint64_t *turns) {
+  if (n < 0) return fail(KVD_ERR_SHAPE, "rope_turns: n must be >= 0");
+  if (n > 0 && (!freq || !turns))
+    return fail(KVD_ERR_NULL, "rope_turns: freq and turns required");
+  for (int32_t i = 0; i < n; ++i)
+    if (!(std::fabs(freq[i]) < 2147483648.0))
+      return fail(KVD_ERR_SHAPE, "rope_turns: frequency %d is not finite and "
+                  "below 2^31 in magnitude", i);
+  // 1 / (2 pi) as the sum of two doubles
+  const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  for (int32_t i = 0; i < n; ++i) {
+    const double f = std::fabs(freq[i]);
+    const double a = f * hi;  // a + b turns
+    const double b = std::fma(f, lo, std::fma(f, hi, -a));
+    // fractions of a turn in units of 2^-64, modulo 2^64
+    const double t = std::ldexp(a - std::floor(a), 32);  // exact
+    const double r = std::ldexp(t - std::floor(t), 32) + std::ldexp(b, 64);
+    const uint64_t u = ((uint64_t)std::floor(t) << 32) +
+                       (uint64_t)(int64_t)std::nearbyint(r);
+    turns[i] = freq[i] < 0 ? 0 - u : u;
+  }
+  return ok();
+}
+
+kvd_status kvd_rope(const kvd_rope_plan *plan, const int32_t *positions,
+                    int64_t axis_stride, int32_t head_dim, const kvd_rows *q,
+                    const kvd_rows *q_out, const kvd_rows *k,
+                    const kvd_rows *k_out, kvd_stream stream) {
+  if (!plan) return fail(KVD_ERR_NULL, "rope: plan is NULL");
+  if (head_dim < 1) return fail(KVD_ERR_SHAPE, "rope: head_dim must be >= 1");
+  kvd_status st = check_rotated(q, q_out, head_dim, "rope", "q");
+  if (st != KVD_OK) return st;
+  if (k || k_out) {
+    st = check_rotated(k, k_out, head_dim, "rope", "k");
+    if (st != KVD_OK) return st;
+    if (k->rows != q->rows)
+      return fail(KVD_ERR_SHAPE, "rope: q and k have different rows");
+  }
+  st = check_rope(plan, positions, axis_stride, head_dim, q->rows, "rope");
+  if (st != KVD_OK) return st;
+  if (q->rows == 0) return ok();
+  const DeviceInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != KVD_OK) return st;
+  kvd::RowsParams p{};
+  set_rope(p, plan, positions, axis_stride);
+  set_q(p, q, q_out);
+  if (k) {
+    p.k = static_cast<const uint16_t *>(k->data);
+    p.k_rs = k->row_stride;
+    p.k_hs = k->head_stride;
+    p.k_out = static_cast<uint16_t *>(k_out->data);
+    p.ko_rs = k_out->row_stride;
+    p.ko_hs = k_out->head_stride;
+    p.n_kv = k->heads;
+  }
+  p.rows = q->rows;
+  p.d = head_dim;
+  p.err = d->err;
+  return launched(kvd::launch_rows(p, false, d->sms,
+                                   reinterpret_cast<cudaStream_t>(stream)),
+                  "rope");
+}
+
+kvd_status kvd_kv_write(const kvd_cache *cache, const int32_t *block_table,
+                        int32_t max_blocks_per_seq, const int32_t *start,
+                        const int32_t *row_start, int32_t batch,
+                        const kvd_rows *k_new, const kvd_rows *v_new,
+                        const kvd_rope_plan *rope, const int32_t *positions,
+                        int64_t axis_stride, const kvd_rows *q,
+                        const kvd_rows *q_out, kvd_stream stream) {
+  kvd_status st = check_cache(cache, false, "kv_write");
+  if (st != KVD_OK) return st;
+  st = check_paged_rows(cache, max_blocks_per_seq, block_table, start,
+                        row_start, batch, "kv_write");
+  if (st != KVD_OK) return st;
+  if (!k_new) return fail(KVD_ERR_NULL, "kv_write: k_new required");
+  if (cache->v && !v_new)
+    return fail(KVD_ERR_NULL, "kv_write: v_new required for a K/V cache");
+  st = check_kv_rows(cache, k_new, k_new->rows, false, "kv_write", "k_new");
+  if (st != KVD_OK) return st;
+  if (cache->v) {
+    st = check_kv_rows(cache, v_new, k_new->rows, false, "kv_write", "v_new");
+    if (st != KVD_OK) return st;
+  }
+  if (cache->dtype == KVD_FP8_E4M3 &&
+      (!cache->k_inv_scale || (cache->v && !cache->v_inv_scale)))
+    return fail(KVD_ERR_NULL, "kv_write: fp8 cache needs inverse scales");
+  if (q || q_out) {
+    if (!rope)
+      return fail(KVD_ERR_NULL, "kv_write: q is rotated, so rope is required");
+    st = check_rotated(q, q_out, cache->head_dim, "kv_write", "q");
+    if (st != KVD_OK) return st;
+    if (q->rows != k_new->rows)
+      return fail(KVD_ERR_SHAPE, "kv_write: q and k_new have different rows");
+  }
+  if (rope) {
+    st = check_rope(rope, positions, axis_stride, cache->head_dim, k_new->rows,
+                    "kv_write");
+    if (st != KVD_OK) return st;
+    if (!kvd::rows_fit(cache->head_dim, rope->d_rot / 2))
+      return fail(KVD_ERR_UNSUPPORTED, "kv_write: a rotated head of %d does "
+                  "not fit in shared memory", cache->head_dim);
+  }
+  if (batch == 0 || k_new->rows == 0) return ok();
+  const DeviceInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != KVD_OK) return st;
+  kvd::RowsParams p{};
+  set_paged(p, cache, max_blocks_per_seq, block_table, start, row_start, batch,
+            d->err);
+  p.k = static_cast<const uint16_t *>(k_new->data);
+  p.k_rs = k_new->row_stride;
+  p.k_hs = k_new->head_stride;
+  if (cache->v) {
+    p.v = static_cast<const uint16_t *>(v_new->data);
+    p.v_rs = v_new->row_stride;
+    p.v_hs = v_new->head_stride;
+  }
+  if (rope) set_rope(p, rope, positions, axis_stride);
+  if (q) set_q(p, q, q_out);
+  p.rows = k_new->rows;
+  return launched(kvd::launch_rows(p, true, d->sms,
+                                   reinterpret_cast<cudaStream_t>(stream)),
+                  "kv_write");
+}
+
+kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
+                       int32_t max_blocks_per_seq, const int32_t *start,
+                       const int32_t *row_start, int32_t batch,
+                       const kvd_rows *k_out, const kvd_rows *v_out,
+                       kvd_stream stream) {
+  kvd_status st = check_cache(cache, v_out != nullptr, "kv_read");
+  if (st != KVD_OK) return st;
+  st = check_paged_rows(cache, max_blocks_per_seq, block_table, start,
+                        row_start, batch, "kv_read");
+  if (st != KVD_OK) return st;
+  if (!k_out && !v_out)
+    return fail(KVD_ERR_NULL, "kv_read: k_out or v_out required");
+  const int rows = k_out ? k_out->rows : v_out->rows;
+  if (k_out) {
+    st = check_kv_rows(cache, k_out, rows, true, "kv_read", "k_out");
+    if (st != KVD_OK) return st;
+  }
+  if (v_out) {
+    st = check_kv_rows(cache, v_out, rows, true, "kv_read", "v_out");
+    if (st != KVD_OK) return st;
+  }
+  if (cache->dtype == KVD_FP8_E4M3 &&
+      ((k_out && !cache->k_scale) || (v_out && !cache->v_scale)))
+    return fail(KVD_ERR_NULL, "kv_read: fp8 cache needs scales");
+  if (batch == 0 || rows == 0) return ok();
+  const DeviceInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != KVD_OK) return st;
+  kvd::RowsParams p{};
+  set_paged(p, cache, max_blocks_per_seq, block_table, start, row_start, batch,
+            d->err);
+  if (k_out) {
+    p.k_out = static_cast<uint16_t *>(k_out->data);
+    p.ko_rs = k_out->row_stride;
+    p.ko_hs = k_out->head_stride;
+  }
+  if (v_out) {
+    p.v_out = static_cast<uint16_t *>(v_out->data);
+    p.vo_rs = v_out->row_stride;
+    p.vo_hs = v_out->head_stride;
+  }
+  p.rows = rows;
+  return launched(kvd::launch_read(p, d->sms,
+                                   reinterpret_cast<cudaStream_t>(stream)),
+                  "kv_read");
+}
+
+kvd_status kvd_extend_workspace_size(const kvd_cache *cache,
+                                     const kvd_seqs *seqs, int32_t rows,
+                                     int32_t max_rows, int32_t n_h,
+                                     size_t *bytes) {
+  if (!bytes)
+    return fail(KVD_ERR_NULL, "extend_workspace_size: bytes is NULL");
+  kvd_status st = check_extend(cache, seqs, rows, max_rows, n_h, true,
+                               "extend_workspace_size");
+  if (st != KVD_OK) return st;
+  const DeviceInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != KVD_OK) return st;
+  *bytes = rows == 0 || max_rows == 0 || seqs->batch == 0
+               ? 0
+               : extend_plan(cache, seqs, rows, max_rows, n_h, d->sms)
+                     .ws_bytes;
+  return ok();
+}
+
+kvd_status kvd_gqa_extend(const kvd_cache *cache, const kvd_seqs *seqs,
+                          const int32_t *row_start, int32_t max_rows,
+                          const kvd_rows *q, float scale, void *out,
+                          float *lse, void *workspace, size_t workspace_bytes,
+                          kvd_stream stream) {
+  if (!q) return fail(KVD_ERR_NULL, "gqa_extend: q is NULL");
+  kvd_status st = check_extend(cache, seqs, q->rows, max_rows, q->heads,
+                               row_start != nullptr, "gqa_extend");
+  if (st != KVD_OK) return st;
+  st = check_rows(q, cache->head_dim, false, "gqa_extend", "q");
+  if (st != KVD_OK) return st;
+  if (!rows_aligned16(q) || !aligned(out, 16))
+    return fail(KVD_ERR_SHAPE, "gqa_extend: q and out must be 16-byte aligned, "
+                "q's strides multiples of 8");
+  if (seqs->batch == 0 || q->rows == 0 || max_rows == 0) return ok();
+  if (!out) return fail(KVD_ERR_NULL, "gqa_extend: out required");
+  const DeviceInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != KVD_OK) return st;
+  const int n_h = q->heads;
+  const ExtendPlan pl =
+      extend_plan(cache, seqs, q->rows, max_rows, n_h, d->sms);
+  Plan need;
+  need.ws_bytes = pl.ws_bytes;
+  st = check_ws(need, workspace, workspace_bytes, "gqa_extend");
+  if (st != KVD_OK) return st;
+  kvd::ExtendParams p = pl.p;
+  p.k = static_cast<const uint8_t *>(cache->k);
+  p.v = static_cast<const uint8_t *>(cache->v);
+  p.block_table = seqs->block_table;
+  p.seq_lens = seqs->seq_lens;
+  p.q = static_cast<const uint16_t *>(q->data);
+  p.q_rs = q->row_stride;
+  p.q_hs = q->head_stride;
+  p.out = static_cast<uint16_t *>(out);
+  p.lse = lse;
+  p.ws_o = static_cast<float *>(workspace);
+  p.ws_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                       pl.ws_o_bytes);
+  p.batch = seqs->batch;
+  p.n_h = n_h;
+  p.n_kv = cache->n_kv;
+  p.dk = p.dv = cache->head_dim;
+  p.dtype = cache->dtype;
+  p.block_size = cache->block_size;
+  p.num_blocks = cache->num_blocks;
+  p.max_blocks = seqs->max_blocks_per_seq;
+  p.max_seq_len = seqs->max_seq_len;
+  p.window = seqs->window;
+  p.win_start = seqs->window_start;
+  p.row_start = row_start;
+  p.max_rows = max_rows;
+  p.rows = q->rows;
+  p.scale_log2 = log2_scale(scale, cache->head_dim);
+  p.err = d->err;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launched(pl.few
+                      ? kvd::launch_extend_few(p, s)
+                      : kvd::launch_extend_tc(p, pl.blocks, pl.splits, s),
+                  "gqa_extend");
 }
 
 }  // extern "C"

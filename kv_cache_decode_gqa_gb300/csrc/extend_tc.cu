@@ -1,0 +1,727 @@
+// Attention of several new rows a sequence over an MXFP4 cache on the
+// 5th-generation tensor cores (kvd_gqa_extend with more than 16 (row, query
+// head) pairs a kv head: prompts, chunks of prompts, drafts of wide groups).
+//
+// The (row, head) pairs of a kv head are numbered row-major, pair f = row *
+// G + head, so any group size G fills the MMA's M. A CTA takes a block of up
+// to 256 pairs -- two M = 128 tiles -- against chunks of 128 positions:
+//   S = Q K^T   (A = Q in shared memory, B = K chunk, K-major)
+//   O += P V    (A = P in tensor memory, over S; B = V chunk, MN-major)
+// with S, P and O of each tile in 128 + 128 columns of tensor memory (512 in
+// all) and one softmax thread per pair (tensor-memory lane). The tiles run
+// against each other: while the softmax of one works, the tensor core does
+// PV of the last chunk and QK of the next one for the other tile. A block of
+// at most 128 pairs has one tile only; then both halves work for it, on even
+// and odd chunks, and their states are merged at the end.
+//
+// What bounds it: prompts do 4 * 128 multiply-adds' flops a (pair, position)
+// at the f16 rate (512 cycles an M = N = K = 128 product); a few rows over a
+// long cache read 144 bytes a position. Either way 256 codes of a position
+// are widened once per CTA, by four warps: a row a thread, 8 codes at a
+// time, times the group's E4M3 scale (exact in f16), into the 128-byte-
+// swizzled tiles that both products read. Raw rows come through a ring of
+// bulk copies, so that the widening never waits for HBM.
+//
+// The softmax keeps a reference maximum per pair and moves it only when a
+// chunk exceeds it by more than 2^8 (the accumulator is rescaled then, in
+// tensor memory): P stays below 2^8, exact enough in f16, and the final
+// division by the sum (fp32, of the same exponentials) takes the reference
+// out again. Queries are scaled by a power of two per (row, head) into f16
+// (see extend_few.cu).
+//
+// Warp roles (512 threads, one CTA per SM; registers are moved from the
+// launch's 128 a thread to 176 / 96 / 64 a warpgroup):
+//   warps 0-3, 4-7   softmax of tile 0 and 1, query load, epilogue
+//   warps 8-11       widening
+//   warp 12          bulk copies of cached rows
+//   warp 13          tensor memory, MMA issue
+#include <algorithm>
+#include <cmath>
+
+#include "kvd_common.cuh"
+#include "stream_k.cuh"
+#include "tcgen05.cuh"
+
+namespace kvd {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kRow = 72;             // bytes of a cached row
+constexpr int kM = 128;              // pairs per tile
+constexpr int kN = kExtendChunk;     // positions per chunk
+constexpr int kTile = 128 * 256;     // a 128 x 128 f16 operand tile, 32 KB
+constexpr int kHalf = 128 * 128;     // its 64-column half
+constexpr int kRaw = kN * kRow;      // raw K (or V) rows of a chunk
+constexpr int kThreads = 512;
+constexpr int kWiden0 = 8, kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kSoftBar = 1;
+constexpr float kSlack = 8.f;        // log2 units the reference may lag by
+
+// shared memory: Q tiles, K ring, V ring (2 each), raw ring
+constexpr int Q_OFF = 0;
+constexpr int K_OFF = Q_OFF + 2 * kTile;
+constexpr int V_OFF = K_OFF + 2 * kTile;
+constexpr int RAW_OFF = V_OFF + 2 * kTile;
+constexpr int kRawSlots = 3;         // + 3 more in Q tile 1 when it is unused
+constexpr int F_OFF = RAW_OFF + kRawSlots * kRaw;  // float [4][128]
+constexpr int BAR_OFF = F_OFF + 4 * kM * 4;
+constexpr int kBars = 2 * (2 * kRawSlots) + 8 + 4 + 2;
+constexpr int FLAG_OFF = BAR_OFF + kBars * 8;      // int [8]
+constexpr int SCAN_OFF = FLAG_OFF + 32;            // int [16 + 16]
+constexpr int SMEM = SCAN_OFF + 128;
+static_assert(3 * kRaw <= kTile && SMEM <= 227 * 1024, "shared memory");
+
+constexpr uint32_t kColS = 0, kColO = 256;         // + 128 * tile
+
+// 16-byte piece c (0..7) of row r in a 128-byte-swizzled 64-column half.
+__device__ __forceinline__ uint32_t sw128(int r, int c) {
+  return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A row block of the batch: block `mb` of sequence b, its pairs [f0, f1),
+// and the positions [lo, hi) they see.
+struct Block {
+  int n, T;    // rows and visible length of the sequence
+  int f0, f1;
+  int lo, hi;
+};
+
+__device__ __forceinline__ Block block_at(const ExtendParams &p, int b,
+                                          int mb, int G) {
+  Block k;
+  k.n = seq_rows(p, b);
+  k.T = min(max(p.seq_lens[b], 0), p.max_seq_len);
+  k.f0 = mb * kExtendRows;
+  k.f1 = min(k.f0 + kExtendRows, k.n * G);
+  const int first = k.T - k.n + k.f0 / G, last = k.T - k.n + (k.f1 - 1) / G;
+  int lo = p.win_start ? max(p.win_start[b], 0) : 0;
+  if (p.window > 0) lo = max(lo, first + 1 - p.window);
+  k.lo = lo;
+  k.hi = max(last + 1, 0);
+  return k;
+}
+
+// Chunks [c0, c1) that a block's positions lie in.
+__device__ __forceinline__ void block_chunks(const Block &k, int &c0,
+                                             int &c1) {
+  c0 = k.lo / kN;
+  c1 = k.lo < k.hi ? (k.hi + kN - 1) / kN : c0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    extend_tc_kernel(const __grid_constant__ ExtendParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float *fs = reinterpret_cast<float *>(smem + F_OFF);
+  uint64_t *rawfull = reinterpret_cast<uint64_t *>(smem + BAR_OFF);
+  uint64_t *rawempty = rawfull + 2 * kRawSlots;
+  uint64_t *kfull = rawempty + 2 * kRawSlots;  // [2] each
+  uint64_t *kempty = kfull + 2;
+  uint64_t *vfull = kempty + 2;
+  uint64_t *vempty = vfull + 2;
+  uint64_t *sfull = vempty + 2;
+  uint64_t *pfull = sfull + 2;
+  uint64_t *qfull = pfull + 2;
+  uint64_t *odone = qfull + 1;
+  int *flags = reinterpret_cast<int *>(smem + FLAG_OFF);
+  volatile int *s_abort = flags;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(flags + 1);
+  int *s_blk = flags + 2;  // sequence and block of this CTA, total blocks
+  int *s_scan = reinterpret_cast<int *>(smem + SCAN_OFF);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.n_h / p.n_kv;
+
+  pdl_wait();
+  pdl_trigger();  // after the wait: the merge launch never overlaps this
+                  // launch's predecessor
+  // ---- which block: a scan of the sequences' block counts --------------
+  // The last blocks come first: under the causal mask they are the longest.
+  const int h = (int)blockIdx.x % p.n_kv;
+  const int want = (int)blockIdx.x / p.n_kv;
+  if (tid == 0) s_blk[0] = -1;
+  {
+    int cnt[2], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int b = 2 * tid + j;
+      cnt[j] = 0;
+      if (b < p.batch) {
+        const int n = seq_rows(p, b);
+        cnt[j] = (int)(((long)n * G + kExtendRows - 1) / kExtendRows);
+        if (blockIdx.x == 0 && blockIdx.y == 0) {
+          if (n == 0 && p.row_start && p.row_start[b] != p.row_start[b + 1])
+            report(p.err, DEVERR_LEN);
+          if (p.seq_lens[b] > p.max_seq_len) report(p.err, DEVERR_LEN);
+        }
+      }
+      sum += cnt[j];
+    }
+    int x = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    int excl = before + x - sum;
+    const int mine = total - 1 - want;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (mine >= excl && mine < excl + cnt[j]) {
+        s_blk[0] = 2 * tid + j;
+        s_blk[1] = mine - excl;
+      }
+      excl += cnt[j];
+    }
+  }
+  __syncthreads();
+  const int b = s_blk[0], mb = s_blk[1];
+  if (b < 0) return;  // past the batch's blocks
+  const Block k = block_at(p, b, mb, G);
+  int c0, c1;
+  block_chunks(k, c0, c1);
+  const int per = p.chunks_per_split > 0 ? p.chunks_per_split
+                                         : max(c1 - c0, 1);
+  const int parts = max((c1 - c0 + per - 1) / per, 1);
+  const int part = blockIdx.y;
+  if (part >= parts) return;
+  c0 += part * per;
+  c1 = min(c1, c0 + per);
+  const int nch = c1 - c0;
+  const int np = k.f1 - k.f0;  // pairs
+  const long row0 = p.row_start ? p.row_start[b] : b;
+  // output row of pair f: query row f / G, head h G + f % G
+  auto out_row = [&](int f) {
+    return (row0 + f / G) * p.n_h + (long)h * G + f % G;
+  };
+  if (nch <= 0) {  // nothing is seen (parts is 1)
+    for (int i = tid; i < np * (kD / 8); i += kThreads)
+      reinterpret_cast<uint4 *>(p.out + out_row(k.f0 + i / (kD / 8)) *
+                                            kD)[i % (kD / 8)] =
+          make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int i = tid; i < np; i += kThreads)
+        p.lse[out_row(k.f0 + i)] = -INFINITY;
+    return;
+  }
+  const bool two = np > kM;
+  const int nraw = two ? kRawSlots : 2 * kRawSlots;
+  // step s: tile s & 1; chunk s / 2 for two tiles, chunk s for one
+  const int nsteps = two ? 2 * nch : nch;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2 * kRawSlots; ++i) {
+      mbar_init(&rawfull[i], 1);
+      mbar_init(&rawempty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kfull[i], 4);
+      mbar_init(&kempty[i], 1);
+      mbar_init(&vfull[i], 4);
+      mbar_init(&vempty[i], 1);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], kM);
+    }
+    mbar_init(qfull, two ? 8 : 4);
+    mbar_init(odone, 1);
+    // the swizzled tiles assume 1 KB atoms (every CTA sees the same layout)
+    *s_abort = (smem_u32(smem) & 1023u) != 0;
+    if (*s_abort) report(p.err, DEVERR_TIMEOUT);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *s_tmem;
+  auto raw_slot = [&](int s) {
+    return smem + (s < kRawSlots ? RAW_OFF + s * kRaw
+                                 : Q_OFF + kTile + (s - kRawSlots) * kRaw);
+  };
+  // Every wait is bounded; a role that gives up flags the abort and leaves
+  // its loop, and the others follow when their own waits run out.
+  auto give_up = [&]() {
+    if (lane == 0) {
+      report(p.err, DEVERR_TIMEOUT);
+      *s_abort = 1;
+    }
+  };
+  auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, !*s_abort && mbar_wait(bar, parity));
+  };
+
+  if (warp < kWiden0) {
+    // ======================= softmax ======================================
+    reg_inc<176>();
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // pair of the tile
+    const int ri = two ? t * kM + r : r;   // pair of the block
+    const bool live = ri < np;
+    const int f = k.f0 + ri;
+    const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+    int vlo = 0, vhi = 0;                  // positions this pair sees
+    if (live) {
+      const int pos = k.T - k.n + f / G;
+      vhi = max(pos + 1, 0);
+      vlo = p.win_start ? max(p.win_start[b], 0) : 0;
+      if (p.window > 0) vlo = max(vlo, pos + 1 - p.window);
+    }
+    // ---- the pair's query, scaled into f16 (tile t, or both halves' one)
+    float sl;
+    {
+      uint4 x[16];
+      uint32_t m = 0;
+      const uint16_t *q = p.q + (row0 + f / G) * p.q_rs +
+                          ((long)h * G + f % G) * p.q_hs;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        x[c] = live ? reinterpret_cast<const uint4 *>(q)[c]
+                    : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        m = __vmaxu2(m, __vmaxu2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu));
+        m = __vmaxu2(m, __vmaxu2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu));
+      }
+      m = max(m & 0xffffu, m >> 16);
+      const int e = row_exponent(m);
+      const float sc = __uint_as_float((uint32_t)e << 23);
+      sl = fmaxf(p.scale_log2 * exp2f((float)(127 - e)), 1.17549435e-38f);
+      if (two || t == 0) {
+        uint8_t *qt = smem + Q_OFF + (two ? t * kTile : 0);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          uint4 w;
+          w.x = pack_f16x2(bf16lo(x[c].x) * sc, bf16hi(x[c].x) * sc);
+          w.y = pack_f16x2(bf16lo(x[c].y) * sc, bf16hi(x[c].y) * sc);
+          w.z = pack_f16x2(bf16lo(x[c].z) * sc, bf16hi(x[c].z) * sc);
+          w.w = pack_f16x2(bf16lo(x[c].w) * sc, bf16hi(x[c].w) * sc);
+          *reinterpret_cast<uint4 *>(qt + (c >> 3) * kHalf +
+                                     sw128(r, c & 7)) = w;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qfull);
+      }
+    }
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    float ref = -INFINITY, l = 0.f;
+    for (int j = 0, s = t; s < nsteps; s += 2, ++j) {
+      const int c = c0 + (two ? j : s);
+      if (!wait_all(&sfull[t], j & 1)) {
+        give_up();
+        break;
+      }
+      tc_fence_after();
+      if (warp_live) {
+        uint32_t x[4][32];
+        const uint32_t ts = tl + kColS + 128 * t;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) tmem_ld32(ts + 32 * g, x[g]);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) tmem_wait_ld(x[g]);
+        // columns [a, z) of the chunk are seen
+        const int a = vlo - c * kN, z = vhi - c * kN;
+        if (__any_sync(0xffffffffu, a > 0 || z < kN)) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * g + i < a || 32 * g + i >= z)
+                x[g][i] = 0xff800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          mx[g] = __uint_as_float(x[g][0]);
+#pragma unroll
+          for (int i = 1; i < 32; ++i)
+            mx[g] = fmaxf(mx[g], __uint_as_float(x[g][i]));
+        }
+        const float top =
+            fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+        const bool grow = top > ref + kSlack;  // from -inf: any score
+        if (__any_sync(0xffffffffu, grow)) {
+          const float al = grow ? ex2(ref - top) : 1.f;
+          if (grow) ref = top;
+          l *= al;
+          if (j > 0) {
+            // sfull of this step followed PV of the tile's last step
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              uint32_t o[16];
+              const uint32_t to = tl + kColO + 128 * t + 16 * g;
+              tmem_ld16(to, o);
+              tmem_wait_ld16(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+              tmem_st16(to, o);
+            }
+          }
+        }
+        const float mu = ref == -INFINITY ? 0.f : ref;
+        float ls[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          ls[g] = 0.f;
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float e0 =
+                ex2(fmaf(__uint_as_float(x[g][2 * i]), sl, -mu));
+            const float e1 =
+                ex2(fmaf(__uint_as_float(x[g][2 * i + 1]), sl, -mu));
+            ls[g] += e0 + e1;
+            pk[i] = pack_f16x2(e0, e1);
+          }
+          tmem_st16(ts + 16 * g, pk);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive(&pfull[t]);
+    }
+    // ---- epilogue --------------------------------------------------------
+    const bool ok = wait_all(odone, 0);
+    if (!ok) give_up();
+    tc_fence_after();
+    float w0 = 1.f, w1 = 0.f, M = ref, L = l;
+    if (!two) {
+      // the halves' states of pair r: this thread's own and the other's
+      fs[t * kM + r] = ref;
+      fs[(2 + t) * kM + r] = l;
+      named_sync(kSoftBar, 2 * kM);
+      const float ra = fs[r], rb = fs[kM + r];
+      M = fmaxf(ra, rb);
+      const float mu = M == -INFINITY ? 0.f : M;
+      w0 = ex2(ra - mu);
+      w1 = ex2(rb - mu);
+      L = fs[2 * kM + r] * w0 + fs[3 * kM + r] * w1;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float lse =
+        L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    const long at = live ? out_row(f) : 0;
+    // two tiles: all 128 columns of the tile's pair; one: the halves write
+    // 64 columns each
+    const int ncol = two ? kD : kD / 2;
+    const int col0 = two ? 0 : t * (kD / 2);
+    const uint32_t ta = tl + kColO + (two ? 128 * t : 0) + col0;
+    const bool second = !two && nsteps > 1;
+    if (warp_live && ok) {
+#pragma unroll 1
+      for (int g = 0; g < ncol; g += 32) {
+        uint32_t o[32];
+        tmem_ld32(ta + g, o);
+        tmem_wait_ld(o);
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          y[i] = __uint_as_float(o[i]) * (two ? inv : w0 * inv);
+        if (second) {
+          tmem_ld32(ta + 128 + g, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            y[i] = fmaf(__uint_as_float(o[i]), w1 * inv, y[i]);
+        }
+        if (live) {
+          if (parts == 1) {
+            uint4 *dst =
+                reinterpret_cast<uint4 *>(p.out + at * kD + col0 + g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]),
+                                  pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                  pack_bf16x2(y[8 * i + 4], y[8 * i + 5]),
+                                  pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(
+                p.ws_o + ((long)part * p.rows * p.n_h + at) * kD + col0 + g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2],
+                                   y[4 * i + 3]);
+          }
+        }
+      }
+      if (live && (two || t == 0)) {
+        if (parts > 1)
+          p.ws_lse[(long)part * p.rows * p.n_h + at] = lse;
+        else if (p.lse)
+          p.lse[at] = lse;
+      }
+    }
+  } else if (warp < kLoadWarp) {
+    // ======================= widening =====================================
+    reg_dec<96>();
+    const int r = tid - kWiden0 * 32;  // row of the chunk
+    int rs = 0, rph = 0;
+    for (int u = 0; u < 2 * nch; ++u) {
+      const int i = u >> 1, st = i & 1, ph = (i >> 1) & 1;
+      const bool is_v = u & 1;
+      if (!wait_all(&rawfull[rs], rph)) {
+        give_up();
+        break;
+      }
+      const uint8_t *src = raw_slot(rs) + r * kRow;
+      uint2 w[9];
+#pragma unroll
+      for (int g = 0; g < 9; ++g)
+        w[g] = *reinterpret_cast<const uint2 *>(src + 8 * g);
+      const int pos = (c0 + i) * kN + r;
+      if (pos < k.lo || pos >= k.hi) {
+        // a row that was not copied, or that no pair sees: zeros, so that 0
+        // times it stays 0
+#pragma unroll
+        for (int g = 0; g < 9; ++g) w[g] = make_uint2(0, 0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rawempty[rs]);
+      if (++rs == nraw) rs = 0, rph ^= 1;
+      // the tile's last reader is done (a fresh barrier passes parity 1)
+      if (!wait_all(is_v ? &vempty[st] : &kempty[st], ph ^ 1)) {
+        give_up();
+        break;
+      }
+      uint8_t *dst = smem + (is_v ? V_OFF : K_OFF) + st * kTile;
+      const uint32_t sc[4] = {e4m3x2_to_f16x2((uint16_t)w[8].x),
+                              e4m3x2_to_f16x2((uint16_t)(w[8].x >> 16)),
+                              e4m3x2_to_f16x2((uint16_t)w[8].y),
+                              e4m3x2_to_f16x2((uint16_t)(w[8].y >> 16))};
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const uint32_t s2 =
+            prmt(sc[g >> 1], 0, (g & 1) ? 0x3232 : 0x1010);
+        const uint32_t cw[2] = {w[g].x, w[g].y};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint4 y;
+          y.x = mul_f16x2(e2m1x2_to_f16x2(cw[q]), s2);
+          y.y = mul_f16x2(e2m1x2_to_f16x2(cw[q] >> 8), s2);
+          y.z = mul_f16x2(e2m1x2_to_f16x2(cw[q] >> 16), s2);
+          y.w = mul_f16x2(e2m1x2_to_f16x2(cw[q] >> 24), s2);
+          const int c = 2 * g + q;
+          *reinterpret_cast<uint4 *>(dst + (c >> 3) * kHalf +
+                                     sw128(r, c & 7)) = y;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(is_v ? &vfull[st] : &kfull[st]);
+    }
+  } else {
+    reg_dec<64>();
+    if (warp == kLoadWarp) {
+      // ===================== bulk copies ==================================
+      // In alternation K and V of a chunk. The attended positions are
+      // widened to even bounds (rows of 72 bytes are copied in pairs; block
+      // sizes are even); blocks are one a lane, looked up a chunk ahead.
+      const int bs = p.block_size;
+      auto bounds = [&](int c, int &t0, int &t1, int &b0, int &nb) {
+        t0 = max(c * kN, k.lo) & ~1;
+        t1 = (min((c + 1) * kN, k.hi) + 1) & ~1;
+        b0 = t0 / bs;
+        nb = (t1 - 1) / bs - b0 + 1;
+      };
+      auto block_of = [&](int lb) {
+        int pb = p.block_table[(long)b * p.max_blocks + lb];
+        if (pb < 0 || pb >= p.num_blocks) {
+          report(p.err, DEVERR_BLOCK);
+          pb = 0;  // read a valid block; the result is flagged as wrong
+        }
+        return pb;
+      };
+      int t0, t1, b0, nb;
+      bounds(c0, t0, t1, b0, nb);
+      int pb = lane < nb ? block_of(b0 + lane) : 0;
+      int s = 0, ph = 1;
+      int last[2 * kRawSlots];  // parity of each slot's last copy, or -1
+#pragma unroll
+      for (int i = 0; i < 2 * kRawSlots; ++i) last[i] = -1;
+      bool go = true;
+      for (int c = c0; go && c < c1; ++c) {
+        int u0 = 0, u1 = 0, v0 = 0, nv = 0, pbn = 0;
+        if (c + 1 < c1) {
+          bounds(c + 1, u0, u1, v0, nv);
+          if (lane < nv) pbn = block_of(v0 + lane);
+        }
+        for (int q = 0; q < 2; ++q) {  // K, V
+          go = wait_all(&rawempty[s], ph);
+          if (!go) {
+            give_up();
+            break;
+          }
+          if (lane == 0)
+            mbar_arrive_expect_tx(&rawfull[s], (uint32_t)(t1 - t0) * kRow);
+          __syncwarp();
+          const uint8_t *base = q ? p.v : p.k;
+          uint8_t *dst = raw_slot(s);
+          for (int j = lane; j < nb; j += 32) {
+            const int blk = j < 32 ? pb : block_of(b0 + j);
+            const int lb = b0 + j;
+            const int a0 = max(t0, lb * bs), a1 = min(t1, (lb + 1) * bs);
+            const long row = ((long)blk * p.n_kv + h) * bs + (a0 - lb * bs);
+            bulk_g2s(dst + (a0 - c * kN) * kRow, base + row * kRow,
+                     (uint32_t)(a1 - a0) * kRow, &rawfull[s]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2 * kRawSlots; ++i)
+            if (i == s) last[i] = ph ^ 1;
+          if (++s == nraw) s = 0, ph ^= 1;
+        }
+        t0 = u0, t1 = u1, b0 = v0, nb = nv, pb = pbn;
+      }
+      if (!go) {
+        // after an abort: every copy that was issued has landed before this
+        // CTA gives its shared memory back
+#pragma unroll
+        for (int i = 0; i < 2 * kRawSlots; ++i)
+          if (last[i] >= 0) mbar_wait(&rawfull[i], last[i]);
+      }
+    } else if (warp == kMmaWarp) {
+      // ===================== MMA issue ====================================
+      constexpr uint32_t idS = umma_idesc_f16(kM, kN, false);
+      constexpr uint32_t idO = umma_idesc_f16(kM, kD, true);
+      const uint32_t q0 = smem_u32(smem + Q_OFF);
+      const uint32_t k0 = smem_u32(smem + K_OFF);
+      const uint32_t v0 = smem_u32(smem + V_OFF);
+      // S of step s (its chunk's K tile is awaited with the chunk's first
+      // step and given back with its last)
+      auto issue_s = [&](int s) -> bool {
+        const int t = s & 1, i = two ? s >> 1 : s, st = i & 1;
+        if ((!two || t == 0) && !wait_all(&kfull[st], (i >> 1) & 1))
+          return false;
+        tc_fence_after();
+        const uint64_t a = umma_desc_sw128(q0 + (two ? t * kTile : 0), 16,
+                                           1024);
+        const uint64_t bk = umma_desc_sw128(k0 + st * kTile, 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < kD / 16; ++ks) {
+          const uint64_t off =
+              (uint64_t)(((ks >> 2) * kHalf + (ks & 3) * 32) >> 4);
+          umma_ss_elect(tbase + kColS + 128 * t, a + off, bk + off, idS,
+                        ks > 0 ? 1u : 0u);
+        }
+        umma_commit_elect(&sfull[t]);
+        if (!two || t == 1) umma_commit_elect(&kempty[st]);
+        return true;
+      };
+      bool ok = wait_all(qfull, 0);
+      ok = ok && issue_s(0);
+      if (ok && nsteps > 1) ok = issue_s(1);
+      for (int s = 0; ok && s < nsteps; ++s) {
+        const int t = s & 1, i = two ? s >> 1 : s, st = i & 1;
+        if (!two || t == 0) ok = wait_all(&vfull[st], (i >> 1) & 1);
+        ok = ok && wait_all(&pfull[t], (s >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t bv = umma_desc_sw128(v0 + st * kTile, kHalf, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kN / 16; ++kk)
+          umma_ts_elect(tbase + kColO + 128 * t,
+                        tbase + kColS + 128 * t + kk * 8,
+                        bv + (uint64_t)((kk * 2048) >> 4), idO,
+                        (s > 1 || kk > 0) ? 1u : 0u);
+        if (!two || t == 1) umma_commit_elect(&vempty[st]);
+        if (s + 2 < nsteps) ok = issue_s(s + 2);
+      }
+      if (!ok) give_up();
+      // every MMA issued has completed before the epilogue and the dealloc
+      umma_commit_elect(odone);
+      mbar_wait(odone, 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();  // every read of tensor memory is done
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Log-sum-exp merge of the blocks that the launch before split over the
+// positions: one warp per output row, a float4 a lane, up to 8 parts'
+// loads in flight.
+constexpr int kRowMergeThreads = 256;
+
+__global__ void __launch_bounds__(kRowMergeThreads)
+    extend_merge_kernel(const __grid_constant__ ExtendParams p) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long at = (long)blockIdx.x * (kRowMergeThreads / 32) + (threadIdx.x >> 5);
+  if (at >= (long)p.rows * p.n_h) return;
+  const int row = (int)(at / p.n_h), hh = (int)(at % p.n_h);
+  const int G = p.n_h / p.n_kv;
+  int b = row, r0 = row;
+  if (p.row_start) {
+    int lo = 0, hi = p.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.row_start[mid] <= row)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    b = lo;
+    r0 = p.row_start[b];
+  }
+  if (row < r0 || row >= r0 + seq_rows(p, b)) return;  // no sequence's row
+  const Block k = block_at(p, b, ((row - r0) * G + hh % G) / kExtendRows, G);
+  int c0, c1;
+  block_chunks(k, c0, c1);
+  const int parts = (c1 - c0 + p.chunks_per_split - 1) / p.chunks_per_split;
+  if (parts <= 1) return;  // written whole
+  const long n = (long)p.rows * p.n_h;
+  float M, W;
+  float4 acc;
+  quad_merge<1>(p.ws_lse, p.ws_o, 1, kD, 0, lane, parts,
+                [&](int i) { return i * n + at; }, M, W, acc);
+  const float iw = W == 0.f ? 0.f : 1.f / W;
+  uint2 packed;
+  packed.x = pack_bf16x2(acc.x * iw, acc.y * iw);
+  packed.y = pack_bf16x2(acc.z * iw, acc.w * iw);
+  reinterpret_cast<uint2 *>(p.out + at * kD)[lane] = packed;
+  if (lane == 0 && p.lse) p.lse[at] = W == 0.f ? -INFINITY : M + logf(W);
+}
+
+}  // namespace
+
+cudaError_t launch_extend_tc(const ExtendParams &p, int blocks, int splits,
+                             cudaStream_t s) {
+  static bool done[64] = {};
+  cudaError_t e = set_smem_once(extend_tc_kernel, SMEM, done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(extend_tc_kernel, dim3(blocks * p.n_kv, splits),
+                 dim3(kThreads), SMEM, s, 1, p);
+  if (e != cudaSuccess || splits <= 1) return e;
+  const long rows = (long)p.rows * p.n_h;
+  const long per = kRowMergeThreads / 32;
+  return launch_pdl(extend_merge_kernel, dim3((unsigned)((rows + per - 1) / per)),
+                    dim3(kRowMergeThreads), 0, s, 1, p);
+}
+
+}  // namespace kvd

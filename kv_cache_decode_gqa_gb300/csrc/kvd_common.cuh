@@ -493,6 +493,21 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t b) {
   return r;
 }
 
+// Product of two f16 pairs, each rounded to nearest even.
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Exponent field of the power of two that takes a query row whose largest
+// bf16 magnitude has bits `amax` into [2^14, 2^15), where f16 holds it (1
+// for a row with an infinity or NaN, which then shows in its outputs).
+__device__ __forceinline__ int row_exponent(uint32_t amax) {
+  const int e = max((int)(amax >> 7), 1);
+  return e == 255 ? 127 : min(268 - e, 254);
+}
+
 // One 16-channel group of a new bf16 row into an MXFP4 row: 8 bytes of
 // codes (channel 2j low nibble) at `codes`, the E4M3 scale byte at
 // `scale`. amax and both divisions in fp32, conversions round to nearest
