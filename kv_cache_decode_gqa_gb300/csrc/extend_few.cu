@@ -378,11 +378,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t s0 = prmt(sp, 0, 0x1010), s1 = prmt(sp, 0, 0x3232);
           const uint32_t w[4] = {c0.x, c0.y, c1.x, c1.y};
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t sh = kk < 4 ? s0 : s1;
-            const uint32_t h16 = w[kk >> 1] >> (16 * (kk & 1));
-            mma_f16(sc[u][t2], qa[kk], mul_f16x2(e2m1x2_to_f16x2(h16), sh),
-                    mul_f16x2(e2m1x2_to_f16x2(h16 >> 8), sh));
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const uint32_t sh = k4 < 2 ? s0 : s1;
+            uint32_t x[4];
+            e2m1x8_to_f16(w[k4], x);
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2)
+              mma_f16(sc[u][t2], qa[2 * k4 + h2], mul_f16x2(x[2 * h2], sh),
+                      mul_f16x2(x[2 * h2 + 1], sh));
           }
         }
       // ---- online softmax over the warp's tokens, rows qr and qr + 8 ----
@@ -465,14 +468,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           d[t][1] = ((x.y >> 4) & 0x0f0f0f0fu) | (y.y & 0xf0f0f0f0u);
         }
 #pragma unroll
-        for (int i8 = 0; i8 < 8; ++i8) {
-          const int w = i8 >> 2, sh = 8 * (i8 & 3);
-          mma_f16(o[2 * i8], pa[u],
-                  mul_f16x2(e2m1x2_to_f16x2(e[0][w] >> sh), sp[0]),
-                  mul_f16x2(e2m1x2_to_f16x2(e[1][w] >> sh), sp[1]));
-          mma_f16(o[2 * i8 + 1], pa[u],
-                  mul_f16x2(e2m1x2_to_f16x2(d[0][w] >> sh), sp[0]),
-                  mul_f16x2(e2m1x2_to_f16x2(d[1][w] >> sh), sp[1]));
+        for (int w = 0; w < 2; ++w) {
+          uint32_t x[2][4], y[2][4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            e2m1x8_to_f16(e[t][w], x[t]);
+            e2m1x8_to_f16(d[t][w], y[t]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mma_f16(o[8 * w + 2 * i], pa[u], mul_f16x2(x[0][i], sp[0]),
+                    mul_f16x2(x[1][i], sp[1]));
+            mma_f16(o[8 * w + 2 * i + 1], pa[u], mul_f16x2(y[0][i], sp[0]),
+                    mul_f16x2(y[1][i], sp[1]));
+          }
         }
       }
     }

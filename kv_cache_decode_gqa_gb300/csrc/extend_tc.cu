@@ -517,11 +517,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t cw[2] = {w[g].x, w[g].y};
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
+          uint32_t h[4];
+          e2m1x8_to_f16(cw[q], h);
           uint4 y;
-          y.x = mul_f16x2(e2m1x2_to_f16x2(cw[q]), s2);
-          y.y = mul_f16x2(e2m1x2_to_f16x2(cw[q] >> 8), s2);
-          y.z = mul_f16x2(e2m1x2_to_f16x2(cw[q] >> 16), s2);
-          y.w = mul_f16x2(e2m1x2_to_f16x2(cw[q] >> 24), s2);
+          y.x = mul_f16x2(h[0], s2);
+          y.y = mul_f16x2(h[1], s2);
+          y.z = mul_f16x2(h[2], s2);
+          y.w = mul_f16x2(h[3], s2);
           const int c = 2 * g + q;
           *reinterpret_cast<uint4 *>(dst + (c >> 3) * kHalf +
                                      sw128(r, c & 7)) = y;

@@ -374,9 +374,12 @@ __global__ void __launch_bounds__(kThreads)
           const uint32_t w[2] = {u.x, u.y};
           uint32_t o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t v = e2m1x2_to_f16x2(w[j >> 2] >> (8 * (j & 3)));
-            o[j] = pack_bf16x2(f16lo(v) * s, f16hi(v) * s);
+          for (int q = 0; q < 2; ++q) {
+            uint32_t v[4];
+            e2m1x8_to_f16(w[q], v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o[4 * q + j] = pack_bf16x2(f16lo(v[j]) * s, f16hi(v[j]) * s);
           }
           uint4 *q = reinterpret_cast<uint4 *>(dst + c * 16);
           q[0] = make_uint4(o[0], o[1], o[2], o[3]);
