@@ -1082,7 +1082,8 @@ void set_paged(kvd::RowsParams &p, const kvd_cache *c, int32_t max_blocks,
 
 struct ExtendPlan {
   bool few = false;
-  kvd::ExtendParams p{};  // hp, n_splits, whole_units, chunks_per_split
+  kvd::FewPlan f{};
+  kvd::ExtendParams p{};  // n_splits, whole_units, chunks_per_split
   int blocks = 0, splits = 1;
   size_t ws_o_bytes = 0, ws_bytes = 0;
 };
@@ -1096,27 +1097,29 @@ ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
   ExtendPlan pl;
   const int g = n_h / c->n_kv;
   const int forced = g_decode_ctas.load(std::memory_order_relaxed);
-  if ((long)max_rows * g <= kvd::kFewRows) {
+  if ((long)max_rows * g <= kvd::kFewPairs) {
     pl.few = true;
-    const int hp = kvd::extend_few_heads(c->n_kv, c->block_size);
-    const int ch = kvd::extend_few_chunk(hp);
-    const long units = (long)s->batch * (c->n_kv / hp);
-    long unit_chunks = (s->max_seq_len + ch - 1) / ch;
+    const kvd::FewPlan f =
+        kvd::extend_few_plan(c->n_kv, c->block_size, max_rows * g, s->batch,
+                             s->max_seq_len, sms);
+    pl.f = f;
+    const long units = (long)s->batch * (c->n_kv / f.hp);
+    long unit_chunks = (s->max_seq_len + f.chunk - 1) / f.chunk;
     const long chunks = units * unit_chunks;
     if (s->window > 0)
       unit_chunks = std::min<long>(
-          unit_chunks, ((long)s->window + max_rows + ch - 2) / ch + 1);
-    pl.p.hp = hp;
+          unit_chunks,
+          ((long)s->window + max_rows + f.chunk - 2) / f.chunk + 1);
     long ctas = forced > 0 ? forced : sms;
     if (forced <= 0 && units <= ctas &&
-        unit_chunks * ch <= kWholeUnitChunks * kvd::kStageRows) {
+        unit_chunks * f.chunk <= kWholeUnitChunks * kvd::kStageRows) {
       pl.p.whole_units = 1;
       pl.p.n_splits = (int)std::max(units, 1L);
       return pl;
     }
     ctas = std::max(1L, std::min(ctas, std::max(chunks, 1L)));
     pl.p.n_splits = (int)ctas;
-    const size_t slots = (size_t)ctas * 2 * hp * kvd::kFewRows;
+    const size_t slots = (size_t)ctas * 2 * f.hp * 8 * f.tiles;
     pl.ws_o_bytes = round_up(slots * 128 * 4, 256);
     pl.ws_bytes = pl.ws_o_bytes + round_up(slots * 4, 256);
     return pl;
@@ -1425,7 +1428,7 @@ kvd_status kvd_gqa_extend(const kvd_cache *cache, const kvd_seqs *seqs,
   p.err = d->err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return launched(pl.few
-                      ? kvd::launch_extend_few(p, s)
+                      ? kvd::launch_extend_few(p, pl.f, s)
                       : kvd::launch_extend_tc(p, pl.blocks, pl.splits, s),
                   "gqa_extend");
 }

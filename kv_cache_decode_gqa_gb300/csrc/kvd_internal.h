@@ -195,13 +195,17 @@ cudaError_t launch_decode_mma(const DecodeParams &p, int dtype,
 // kv heads the tensor-core kernel takes per work unit (its plan and its
 // launch must agree).
 int mma_heads_per_unit(int n_kv, int block_size, int dtype);
-// kvd_gqa_extend, at most 16 (row, head) pairs a kv head: warp-level MMAs,
-// `hp` kv heads a unit and chunks of `extend_few_chunk` positions, as
-// planned by extend_few_heads.
-constexpr int kFewRows = 16;
-int extend_few_heads(int n_kv, int block_size);
-int extend_few_chunk(int hp);
-cudaError_t launch_extend_few(const ExtendParams &p, cudaStream_t s);
+// kvd_gqa_extend, at most kFewPairs (row, head) pairs a kv head: warp-level
+// MMAs over units of `hp` kv heads, in chunks of `chunk` positions, `tiles`
+// tiles of 8 pairs.
+constexpr int kFewPairs = 16;
+struct FewPlan {
+  int hp, chunk, tiles;
+};
+FewPlan extend_few_plan(int n_kv, int block_size, int pairs, long batch,
+                        int max_seq_len, int sms);
+cudaError_t launch_extend_few(const ExtendParams &p, const FewPlan &f,
+                              cudaStream_t s);
 // kvd_gqa_extend otherwise, on tcgen05: blocks of kExtendRows (row, head)
 // pairs of a kv head against chunks of kExtendChunk positions, each CTA
 // taking chunks_per_split of a block's chunks (0: all of them; else partials

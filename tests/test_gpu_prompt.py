@@ -439,6 +439,15 @@ EXTEND_CASES = [
     ([3, 2], [500, 2], 4, 1, 6, 7),
     ([2], [6000], 16, 2, 128, 0),
     ([1] * 2, [150, 100], 16, 2, 64, 1),
+    # -- up to 32
+    ([4] * 9, [4, 70, 1000, 333, 64, 65, 2000, 5, 128], 64, 8, 64, 0),
+    ([3, 1, 2], [700, 1, 3000], 18, 2, 32, 0),
+    ([4] * 40, [100 * i + 4 for i in range(40)], 64, 8, 64, 0),
+    ([5, 4], [4, 900], 24, 4, 16, 50),
+    ([2] * 50, [50 * i + 2 for i in range(50)], 32, 4, 64, 0),
+    ([1] * 64, [60 * i + 1 for i in range(64)], 64, 8, 64, 0),
+    ([1] * 64, [60 * i + 1 for i in range(64)], 32, 8, 16, 300),
+    ([1] * 64, [97 * i + 1 for i in range(64)], 12, 1, 6, 0),
     # -- one tile of pairs
     ([5], [5], 8, 1, 64, 0),
     ([4, 4, 4], [1000, 4, 2333], 64, 8, 64, 0),
