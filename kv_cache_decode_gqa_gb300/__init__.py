@@ -13,6 +13,8 @@ Cache layout (per layer): K and V tensors [num_blocks][n_kv][block_size]
 """
 import contextlib
 import ctypes
+import functools
+import inspect
 from dataclasses import dataclass
 from typing import Optional
 
@@ -349,27 +351,57 @@ def sparse_decode(cache, block_table, seq_lens, max_seq_len, indices, q,
 # ---------------------------------------------------------------------------
 def _one_device(first, *tensors):
     """The device of a call, all of whose tensors must lie on it."""
+    dev = first.device
     for t in tensors:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device} in "
-                             "one call")
-    return first.device
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device} in one call")
+    return dev
 
 
-@contextlib.contextmanager
 def _launching(device, stream):
-    """The stream of a call on `device` (made current for the call, as is
-    the stream, so that what the call allocates belongs to that stream)."""
+    """A context in which `device` and the call's stream are current (so that
+    what the call allocates belongs to that stream), or None where they are:
+    small calls are over sooner than two context managers."""
     import torch
+    if stream is None and device.index == torch.cuda.current_device():
+        return None
     if stream is not None and stream.device != device:
         raise ValueError(f"a stream of {stream.device} for tensors on "
                          f"{device}")
-    with torch.cuda.device(device):
-        if stream is None:
-            yield _stream(None)
-        else:
-            with torch.cuda.stream(stream):
-                yield _stream(stream)
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def _current(device):
+    """The current stream of `device`, which is current."""
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
+
+
+def _in_context(call):
+    """A call of this module from a function that checks its arguments and
+    returns (device, launch): launch(stream handle) runs with the device and
+    the keyword `stream` (default: the device's current stream) current."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        device, launch = call(*args, **kw)
+        context = _launching(device, stream)
+        if context is None:
+            return launch(_current(device))
+        with context:
+            return launch(_current(device))
+    sig = inspect.signature(call)
+    run.__signature__ = sig.replace(parameters=[
+        *sig.parameters.values(),
+        inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY,
+                          default=None)])
+    return run
 
 
 def _rows3(t, name, heads=None, width=None):
@@ -379,23 +411,30 @@ def _rows3(t, name, heads=None, width=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
         raise ValueError(f"{name} must be [rows][heads][width] with "
                          "contiguous vectors")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"{name} must have {heads} heads, got {t.shape[1]}")
-    if width is not None and t.shape[2] != width:
-        raise ValueError(f"{name} must be {width} wide, got {t.shape[2]}")
-    return _native.KvdRows(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0),
-                           t.stride(1))
+    if heads is not None and shape[1] != heads:
+        raise ValueError(f"{name} must have {heads} heads, got {shape[1]}")
+    if width is not None and shape[2] != width:
+        raise ValueError(f"{name} must be {width} wide, got {shape[2]}")
+    return _native.KvdRows(t.data_ptr(), shape[0], shape[1], stride[0],
+                           stride[1])
 
 
-def _new_rows(t):
+def _out_rows(out, like, rows, name):
+    """The output of a call that returns rows shaped as `like` (whose KvdRows
+    is `rows`): `out`, or a new contiguous tensor; and its KvdRows."""
     import torch
-    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    h, d = rows.heads, like.shape[2]
+    if out is not None:
+        return out, _rows3(out, name, h, d)
+    out = torch.empty_like(like, memory_format=torch.contiguous_format)
+    return out, _native.KvdRows(out.data_ptr(), rows.rows, h, h * d, d)
 
 
-@dataclass
+@dataclass(frozen=True)
 class RopePlan:
     """Frequencies and axes of rotary positions, on the device (rope_plan
     makes one; a model keeps it)."""
@@ -405,14 +444,19 @@ class RopePlan:
     n_axes: int
     pairing: str                     # "half" | "adjacent"
 
-    def struct(self, inverse=False):
+    def __post_init__(self):
         import torch
         _need(self.turns, "plan.turns", torch.int64, self.d_rot // 2)
         if self.axis is not None:
             _need(self.axis, "plan.axis", torch.uint8, self.d_rot // 2)
+        if self.pairing not in _PAIRINGS:
+            raise ValueError(f"pairing must be one of {sorted(_PAIRINGS)}")
+
+    def struct(self, inverse=False):
         return _native.KvdRopePlan(
-            _ptr(self.turns), _ptr(self.axis), self.d_rot, self.n_axes,
-            _PAIRINGS[self.pairing], int(bool(inverse)))
+            self.turns.data_ptr(),
+            None if self.axis is None else self.axis.data_ptr(), self.d_rot,
+            self.n_axes, _PAIRINGS[self.pairing], 1 if inverse else 0)
 
 
 _PAIRINGS = {"half": 0, "adjacent": 1}
@@ -483,32 +527,30 @@ def _positions(plan, positions, rows):
     return positions
 
 
-def rope(plan, positions, q, k=None, q_out=None, k_out=None, inverse=False,
-         stream=None):
+@_in_context
+def rope(plan, positions, q, k=None, q_out=None, k_out=None, inverse=False):
     """Rotate q [rows][n_h][d] (and k [rows][n_kv][d]) bf16 to positions
     int32 [n_axes][rows]: returns (q_out, k_out). Any strides with
     contiguous vectors; q_out=q rotates in place. ``inverse`` turns back
-    (also the gradient of a rotation)."""
+    (also the gradient of a rotation). ``stream``: as for the other calls."""
     qs = _rows3(q, "q")
     ks = None if k is None else _rows3(k, "k", width=q.shape[2])
     if k_out is not None and k is None:
         raise ValueError("k_out without k")
     r = plan.struct(inverse)
-    _positions(plan, positions, q.shape[0])
+    rows = qs.rows
+    _positions(plan, positions, rows)
     dev = _one_device(q, k, q_out, k_out, positions, plan.turns, plan.axis)
-    with _launching(dev, stream) as s:
-        if q_out is None:
-            q_out = _new_rows(q)
-        if k is not None and k_out is None:
-            k_out = _new_rows(k)
-        qo = _rows3(q_out, "q_out", q.shape[1], q.shape[2])
-        ko = None if k is None else _rows3(k_out, "k_out", k.shape[1],
-                                           k.shape[2])
-        check(lib().kvd_rope(ctypes.byref(r), _ptr(positions), q.shape[0],
-                             q.shape[2], ctypes.byref(qs), ctypes.byref(qo),
-                             ks and ctypes.byref(ks), ko and ctypes.byref(ko),
-                             s))
-    return q_out, k_out
+
+    def launch(s, q_out=q_out, k_out=k_out):
+        q_out, qo = _out_rows(q_out, q, qs, "q_out")
+        ko = None
+        if ks is not None:
+            k_out, ko = _out_rows(k_out, k, ks, "k_out")
+        check(lib().kvd_rope(r, positions.data_ptr(), rows, q.shape[2], qs,
+                             qo, ks, ko, s))
+        return q_out, k_out
+    return dev, launch
 
 
 def _ragged(cache, block_table, start, row_start):
@@ -522,8 +564,9 @@ def _ragged(cache, block_table, start, row_start):
     return B
 
 
+@_in_context
 def kv_write(cache, block_table, start, row_start, k_new, v_new=None,
-             rope=None, positions=None, q=None, q_out=None, stream=None):
+             rope=None, positions=None, q=None, q_out=None):
     """Write ragged new rows k_new (and v_new) [rows][n_kv][head_dim] bf16
     into the cache: rows row_start[b] .. row_start[b + 1] - 1 go to positions
     start[b] .. of sequence b. With ``rope`` (a RopePlan) and ``positions``
@@ -535,10 +578,10 @@ def kv_write(cache, block_table, start, row_start, k_new, v_new=None,
     vs = None
     if v_new is not None:
         vs = _rows3(v_new, "v_new", cache.n_kv, cache.head_dim)
-    qs = qo = r = None
+    qs = r = None
     if rope is not None:
         r = rope.struct()
-        _positions(rope, positions, k_new.shape[0])
+        _positions(rope, positions, ks.rows)
     elif q is not None or q_out is not None or positions is not None:
         raise ValueError("q and positions need rope")
     if q is not None:
@@ -549,22 +592,23 @@ def kv_write(cache, block_table, start, row_start, k_new, v_new=None,
                       v_new, positions, q, q_out,
                       rope and rope.turns, rope and rope.axis,
                       cache.k_inv_scale, cache.v_inv_scale)
-    with _launching(dev, stream) as s:
-        if q is not None:
-            if q_out is None:
-                q_out = _new_rows(q)
-            qo = _rows3(q_out, "q_out", q.shape[1], q.shape[2])
+
+    def launch(s, q_out=q_out):
+        qo = None
+        if qs is not None:
+            q_out, qo = _out_rows(q_out, q, qs, "q_out")
         check(lib().kvd_kv_write(
-            ctypes.byref(c), _ptr(block_table), block_table.shape[1],
-            _ptr(start), _ptr(row_start), B, ctypes.byref(ks),
-            vs and ctypes.byref(vs), r and ctypes.byref(r), _ptr(positions),
-            k_new.shape[0], qs and ctypes.byref(qs), qo and ctypes.byref(qo),
-            s))
-    return q_out
+            c, block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
+            row_start.data_ptr(), B, ks, vs, r,
+            None if positions is None else positions.data_ptr(), ks.rows, qs,
+            qo, s))
+        return q_out
+    return dev, launch
 
 
+@_in_context
 def kv_read(cache, block_table, start, row_start, rows, k_out=None,
-            v_out=None, stream=None):
+            v_out=None):
     """Read positions start[b] .. of every sequence back as bf16 rows
     row_start[b] .. row_start[b + 1] - 1: returns (k, v) [rows][n_kv]
     [head_dim] (v None for a K-only cache). ``rows``: rows of the outputs;
@@ -573,26 +617,27 @@ def kv_read(cache, block_table, start, row_start, rows, k_out=None,
     import torch
     c = cache.struct()
     B = _ragged(cache, block_table, start, row_start)
+    if cache.v is None and v_out is not None:
+        raise ValueError("v_out for a K-only cache")
     dev = _one_device(cache.k, cache.v, block_table, start, row_start, k_out,
                       v_out, cache.k_scale, cache.v_scale)
     shape = (int(rows), cache.n_kv, cache.head_dim)
-    with _launching(dev, stream) as s:
+
+    def launch(s, k_out=k_out, v_out=v_out):
         if k_out is None:
             k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        if cache.v is None:
-            if v_out is not None:
-                raise ValueError("v_out for a K-only cache")
-        elif v_out is None:
+        if v_out is None and cache.v is not None:
             v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        ks = _rows3(k_out, "k_out", *shape[1:])
-        vs = None if v_out is None else _rows3(v_out, "v_out", *shape[1:])
+        ks = _rows3(k_out, "k_out", shape[1], shape[2])
+        vs = None if v_out is None else _rows3(v_out, "v_out", shape[1],
+                                               shape[2])
         if ks.rows != shape[0] or (vs is not None and vs.rows != shape[0]):
             raise ValueError(f"outputs must have {shape[0]} rows")
         check(lib().kvd_kv_read(
-            ctypes.byref(c), _ptr(block_table), block_table.shape[1],
-            _ptr(start), _ptr(row_start), B, ctypes.byref(ks),
-            vs and ctypes.byref(vs), s))
-    return k_out, v_out
+            c, block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
+            row_start.data_ptr(), B, ks, vs, s))
+        return k_out, v_out
+    return dev, launch
 
 
 def extend_workspace_size(cache, block_table, seq_lens, max_seq_len, rows,
@@ -609,9 +654,10 @@ def extend_workspace_size(cache, block_table, seq_lens, max_seq_len, rows,
     return out.value
 
 
+@_in_context
 def gqa_extend(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
                max_rows=1, scale=None, out=None, lse=None, workspace=None,
-               want_lse=True, stream=None, window=0, window_start=None):
+               want_lse=True, window=0, window_start=None):
     """Attention of new tokens over an MXFP4 cache that holds them: q
     [rows][n_h][head_dim] bf16 (contiguous vectors) -> (out [rows][n_h]
     [head_dim] bf16, lse [rows][n_h] fp32). Rows row_start[b] ..
@@ -620,40 +666,46 @@ def gqa_extend(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
     sequence b's one new token. Each row attends to the positions up to its
     own, within ``window`` and from ``window_start`` if given."""
     import torch
-    qs = _rows3(q, "q", width=cache.head_dim)
+    d = cache.head_dim
+    qs = _rows3(q, "q", width=d)
     c = cache.struct()
-    s = _seqs(block_table, seq_lens, max_seq_len, 0, window, window_start)
-    rows, n_h = q.shape[0], q.shape[1]
+    seqs = _seqs(block_table, seq_lens, max_seq_len, 0, window, window_start)
+    rows, n_h, max_rows = qs.rows, qs.heads, int(max_rows)
     if row_start is not None:
-        _need(row_start, "row_start", torch.int32, seq_lens.numel() + 1)
+        _need(row_start, "row_start", torch.int32, seqs.batch + 1)
+    if out is not None:
+        _need(out, "out", torch.bfloat16, rows * n_h * d)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, rows * n_h)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
     dev = _one_device(q, cache.k, cache.v, block_table, seq_lens, row_start,
                       window_start, out, lse, workspace)
-    with _launching(dev, stream) as st:
+
+    def launch(s, out=out, lse=lse, workspace=workspace):
+        L = lib()
         if out is None:
-            out = torch.empty((rows, n_h, cache.head_dim),
-                              dtype=torch.bfloat16, device=dev)
-        _need(out, "out", torch.bfloat16, rows * n_h * cache.head_dim)
+            out = torch.empty((rows, n_h, d), dtype=torch.bfloat16,
+                              device=dev)
         if lse is None and want_lse:
             lse = torch.empty((rows, n_h), dtype=torch.float32, device=dev)
-        if lse is not None:
-            _need(lse, "lse", torch.float32, rows * n_h)
-        nbytes = 0
         if workspace is not None:
-            _need(workspace, "workspace", torch.uint8)
             nbytes = workspace.numel()
         else:
             need = ctypes.c_size_t(0)
-            check(lib().kvd_extend_workspace_size(
-                ctypes.byref(c), ctypes.byref(s), rows, int(max_rows), n_h,
-                ctypes.byref(need)))
+            check(L.kvd_extend_workspace_size(c, seqs, rows, max_rows, n_h,
+                                              need))
             nbytes = need.value
             if nbytes:
+                # every partial a call keeps here is written before it is read
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        check(lib().kvd_gqa_extend(
-            ctypes.byref(c), ctypes.byref(s), _ptr(row_start), int(max_rows),
-            ctypes.byref(qs), float(scale or 0.0), _ptr(out), _ptr(lse),
-            _ptr(workspace), nbytes, st))
-    return out, lse
+        check(L.kvd_gqa_extend(
+            c, seqs, None if row_start is None else row_start.data_ptr(),
+            max_rows, qs, float(scale or 0.0), out.data_ptr(),
+            None if lse is None else lse.data_ptr(),
+            None if workspace is None else workspace.data_ptr(), nbytes, s))
+        return out, lse
+    return dev, launch
 
 
 class BlockPool:
