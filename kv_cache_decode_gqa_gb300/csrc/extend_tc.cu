@@ -29,12 +29,13 @@
 // out again. Queries are scaled by a power of two per (row, head) into f16
 // (see extend_few.cu).
 //
-// Warp roles (512 threads, one CTA per SM; registers are moved from the
-// launch's 128 a thread to 176 / 96 / 64 a warpgroup):
-//   warps 0-3, 4-7   softmax of tile 0 and 1, query load, epilogue
-//   warps 8-11       widening
-//   warp 12          bulk copies of cached rows
-//   warp 13          tensor memory, MMA issue
+// Warp roles (640 threads, one CTA per SM; registers are moved from the
+// launch's 96 a thread to 168 for the softmax and 48 for the others):
+//   warps 0-3, 4-7     softmax of tile 0 and 1, query load, epilogue
+//   warps 8-11, 12-15  widening of K and of V (one group for both took 3,300
+//                      cycles a chunk, the softmax and products 2,300)
+//   warp 16            bulk copies of cached rows
+//   warp 17            tensor memory, MMA issue
 #include <algorithm>
 #include <cmath>
 
@@ -52,8 +53,8 @@ constexpr int kN = kExtendChunk;     // positions per chunk
 constexpr int kTile = 128 * 256;     // a 128 x 128 f16 operand tile, 32 KB
 constexpr int kHalf = 128 * 128;     // its 64-column half
 constexpr int kRaw = kN * kRow;      // raw K (or V) rows of a chunk
-constexpr int kThreads = 512;
-constexpr int kWiden0 = 8, kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kThreads = 640;
+constexpr int kWiden0 = 8, kLoadWarp = 16, kMmaWarp = 17;
 constexpr int kSoftBar = 1;
 constexpr float kSlack = 8.f;        // log2 units the reference may lag by
 
@@ -67,7 +68,7 @@ constexpr int F_OFF = RAW_OFF + kRawSlots * kRaw;  // float [4][128]
 constexpr int BAR_OFF = F_OFF + 4 * kM * 4;
 constexpr int kBars = 2 * (2 * kRawSlots) + 8 + 4 + 2;
 constexpr int FLAG_OFF = BAR_OFF + kBars * 8;      // int [8]
-constexpr int SCAN_OFF = FLAG_OFF + 32;            // int [16 + 16]
+constexpr int SCAN_OFF = FLAG_OFF + 32;            // int [20]
 constexpr int SMEM = SCAN_OFF + 128;
 static_assert(3 * kRaw <= kTile && SMEM <= 227 * 1024, "shared memory");
 
@@ -85,6 +86,33 @@ __device__ __forceinline__ void reg_inc() {
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Packed pairs of fp32 values, one instruction for both.
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b,
+                                              uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The largest of three, NaN only if all are.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // A row block of the batch: block `mb` of sequence b, its pairs [f0, f1),
@@ -236,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&vfull[i], 4);
       mbar_init(&vempty[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], kM);
+      mbar_init(&pfull[i], 4);
     }
     mbar_init(qfull, two ? 8 : 4);
     mbar_init(odone, 1);
@@ -271,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kWiden0) {
     // ======================= softmax ======================================
-    reg_inc<176>();
+    reg_inc<168>();
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // pair of the tile
     const int ri = two ? t * kM + r : r;   // pair of the block
@@ -352,13 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          mx[g] = __uint_as_float(x[g][0]);
+          mx[g] = fmaxf(__uint_as_float(x[g][0]), __uint_as_float(x[g][1]));
 #pragma unroll
-          for (int i = 1; i < 32; ++i)
-            mx[g] = fmaxf(mx[g], __uint_as_float(x[g][i]));
+          for (int i = 2; i < 32; i += 2)
+            mx[g] = max3(mx[g], __uint_as_float(x[g][i]),
+                         __uint_as_float(x[g][i + 1]));
         }
-        const float top =
-            fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl;
         const bool grow = top > ref + kSlack;  // from -inf: any score
         if (__any_sync(0xffffffffu, grow)) {
           const float al = grow ? ex2(ref - top) : 1.f;
@@ -380,27 +408,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float mu = ref == -INFINITY ? 0.f : ref;
-        float ls[4];
+        const uint64_t sl2 = pack_f32x2(sl, sl), mu2 = pack_f32x2(-mu, -mu);
+        uint64_t ls[2] = {0, 0};
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          ls[g] = 0.f;
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float e0 =
-                ex2(fmaf(__uint_as_float(x[g][2 * i]), sl, -mu));
-            const float e1 =
-                ex2(fmaf(__uint_as_float(x[g][2 * i + 1]), sl, -mu));
-            ls[g] += e0 + e1;
+            float e0, e1;
+            unpack_f32x2(
+                fma_f32x2(pack_f32x2(__uint_as_float(x[g][2 * i]),
+                                     __uint_as_float(x[g][2 * i + 1])),
+                          sl2, mu2),
+                e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            ls[i & 1] = add_f32x2(ls[i & 1], pack_f32x2(e0, e1));
             pk[i] = pack_f16x2(e0, e1);
           }
           tmem_st16(ts + 16 * g, pk);
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        {
+          float a0, a1;
+          unpack_f32x2(add_f32x2(ls[0], ls[1]), a0, a1);
+          l += a0 + a1;
+        }
         tmem_wait_st();
       }
       tc_fence_before();
-      mbar_arrive(&pfull[t]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[t]);
     }
     // ---- epilogue --------------------------------------------------------
     const bool ok = wait_all(odone, 0);
@@ -475,12 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kLoadWarp) {
     // ======================= widening =====================================
-    reg_dec<96>();
-    const int r = tid - kWiden0 * 32;  // row of the chunk
-    int rs = 0, rph = 0;
-    for (int u = 0; u < 2 * nch; ++u) {
-      const int i = u >> 1, st = i & 1, ph = (i >> 1) & 1;
-      const bool is_v = u & 1;
+    reg_dec<48>();
+    const int r = (tid - kWiden0 * 32) & 127;  // row of the chunk
+    const bool is_v = warp >= kWiden0 + 4;
+    uint64_t *tfull = is_v ? vfull : kfull, *tempty = is_v ? vempty : kempty;
+    // K rows are raw units 0, 2, 4, ..., V rows 1, 3, 5, ...
+    int rs = is_v, rph = 0;
+    for (int i = 0; i < nch; ++i) {
+      const int st = i & 1, ph = (i >> 1) & 1;
       if (!wait_all(&rawfull[rs], rph)) {
         give_up();
         break;
@@ -499,9 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&rawempty[rs]);
-      if (++rs == nraw) rs = 0, rph ^= 1;
+      if ((rs += 2) >= nraw) rs -= nraw, rph ^= 1;
       // the tile's last reader is done (a fresh barrier passes parity 1)
-      if (!wait_all(is_v ? &vempty[st] : &kempty[st], ph ^ 1)) {
+      if (!wait_all(&tempty[st], ph ^ 1)) {
         give_up();
         break;
       }
@@ -531,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(is_v ? &vfull[st] : &kfull[st]);
+      if (lane == 0) mbar_arrive(&tfull[st]);
     }
   } else {
-    reg_dec<64>();
+    reg_dec<48>();
     if (warp == kLoadWarp) {
       // ===================== bulk copies ==================================
       // In alternation K and V of a chunk. The attended positions are
@@ -610,13 +649,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q0 = smem_u32(smem + Q_OFF);
       const uint32_t k0 = smem_u32(smem + K_OFF);
       const uint32_t v0 = smem_u32(smem + V_OFF);
-      // S of step s (its chunk's K tile is awaited with the chunk's first
-      // step and given back with its last)
-      auto issue_s = [&](int s) -> bool {
-        const int t = s & 1, i = two ? s >> 1 : s, st = i & 1;
-        if ((!two || t == 0) && !wait_all(&kfull[st], (i >> 1) & 1))
-          return false;
-        tc_fence_after();
+      auto chunk_of = [&](int s) { return two ? s >> 1 : s; };
+      // Up to three barriers at once, one a lane: a wait costs a few hundred
+      // cycles here even when its phase is over (the shared memory pipe is
+      // busy with the widening).
+      auto wait3 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1,
+                       uint64_t *b2, uint32_t p2) {
+        uint64_t *bar = lane == 0 ? b0 : lane == 1 ? b1 : lane == 2 ? b2
+                                                                    : nullptr;
+        const uint32_t par = lane == 0 ? p0 : lane == 1 ? p1 : p2;
+        return __all_sync(0xffffffffu,
+                          bar == nullptr || mbar_wait(bar, par)) &&
+               !*s_abort;
+      };
+      // S of step s, whose chunk's K tile is there; it is given back with
+      // the chunk's last step
+      auto issue_s = [&](int s) {
+        const int t = s & 1, st = chunk_of(s) & 1;
         const uint64_t a = umma_desc_sw128(q0 + (two ? t * kTile : 0), 16,
                                            1024);
         const uint64_t bk = umma_desc_sw128(k0 + st * kTile, 16, 1024);
@@ -629,15 +678,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit_elect(&sfull[t]);
         if (!two || t == 1) umma_commit_elect(&kempty[st]);
-        return true;
       };
-      bool ok = wait_all(qfull, 0);
-      ok = ok && issue_s(0);
-      if (ok && nsteps > 1) ok = issue_s(1);
+      // the K barrier that step s waits for (its chunk's first step only)
+      auto kbar = [&](int s) -> uint64_t * {
+        return s < nsteps && (!two || (s & 1) == 0) ? &kfull[chunk_of(s) & 1]
+                                                    : nullptr;
+      };
+      auto kpar = [&](int s) { return (uint32_t)((chunk_of(s) >> 1) & 1); };
+      bool ok = wait3(qfull, 0, kbar(0), 0, kbar(1), kpar(1));
+      if (ok) {
+        tc_fence_after();
+        issue_s(0);
+        if (nsteps > 1) issue_s(1);
+      }
       for (int s = 0; ok && s < nsteps; ++s) {
-        const int t = s & 1, i = two ? s >> 1 : s, st = i & 1;
-        if (!two || t == 0) ok = wait_all(&vfull[st], (i >> 1) & 1);
-        ok = ok && wait_all(&pfull[t], (s >> 1) & 1);
+        const int t = s & 1, i = chunk_of(s), st = i & 1;
+        // P of this step, V of its chunk, K of the step after next's
+        ok = wait3(&pfull[t], (s >> 1) & 1,
+                   !two || t == 0 ? &vfull[st] : nullptr, (i >> 1) & 1,
+                   kbar(s + 2), kpar(s + 2));
         if (!ok) break;
         tc_fence_after();
         const uint64_t bv = umma_desc_sw128(v0 + st * kTile, kHalf, 1024);
@@ -648,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bv + (uint64_t)((kk * 2048) >> 4), idO,
                         (s > 1 || kk > 0) ? 1u : 0u);
         if (!two || t == 1) umma_commit_elect(&vempty[st]);
-        if (s + 2 < nsteps) ok = issue_s(s + 2);
+        if (s + 2 < nsteps) issue_s(s + 2);
       }
       if (!ok) give_up();
       // every MMA issued has completed before the epilogue and the dealloc
