@@ -160,8 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *qfull = pfull + 2;
   uint64_t *odone = qfull + 1;
   int *flags = reinterpret_cast<int *>(smem + FLAG_OFF);
-  volatile int *s_abort = flags;
-  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(flags + 1);
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(flags);
   int *s_blk = flags + 2;  // sequence and block of this CTA, total blocks
   int *s_scan = reinterpret_cast<int *>(smem + SCAN_OFF);
 
@@ -248,6 +247,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.lse[out_row(k.f0 + i)] = -INFINITY;
     return;
   }
+  // the swizzled tiles assume 1 KB atoms (every CTA sees the same layout)
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (tid == 0) report(p.err, DEVERR_TIMEOUT);
+    return;
+  }
   const bool two = np > kM;
   const int nraw = two ? kRawSlots : 2 * kRawSlots;
   // step s: tile s & 1; chunk s / 2 for two tiles, chunk s for one
@@ -268,9 +272,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(qfull, two ? 8 : 4);
     mbar_init(odone, 1);
-    // the swizzled tiles assume 1 KB atoms (every CTA sees the same layout)
-    *s_abort = (smem_u32(smem) & 1023u) != 0;
-    if (*s_abort) report(p.err, DEVERR_TIMEOUT);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -285,16 +286,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     return smem + (s < kRawSlots ? RAW_OFF + s * kRaw
                                  : Q_OFF + kTile + (s - kRawSlots) * kRaw);
   };
-  // Every wait is bounded; a role that gives up flags the abort and leaves
-  // its loop, and the others follow when their own waits run out.
+  // Every wait is bounded; a role that gives up leaves its loop, and the
+  // others follow when their own waits run out. (A flag to leave earlier
+  // would cost every wait a shared-memory load: 200 to 300 cycles here.)
   auto give_up = [&]() {
-    if (lane == 0) {
-      report(p.err, DEVERR_TIMEOUT);
-      *s_abort = 1;
-    }
+    if (lane == 0) report(p.err, DEVERR_TIMEOUT);
   };
   auto wait_all = [&](uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, !*s_abort && mbar_wait(bar, parity));
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
   };
 
   if (warp < kWiden0) {
@@ -650,17 +649,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k0 = smem_u32(smem + K_OFF);
       const uint32_t v0 = smem_u32(smem + V_OFF);
       auto chunk_of = [&](int s) { return two ? s >> 1 : s; };
-      // Up to three barriers at once, one a lane: a wait costs a few hundred
-      // cycles here even when its phase is over (the shared memory pipe is
-      // busy with the widening).
+      // Up to three barriers at once, one a lane, by polling: a wait costs a
+      // few hundred cycles here even when its phase is over (the shared
+      // memory pipe is busy with the tiles), and a suspending wait on
+      // several addresses slept through their completion.
       auto wait3 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1,
                        uint64_t *b2, uint32_t p2) {
         uint64_t *bar = lane == 0 ? b0 : lane == 1 ? b1 : lane == 2 ? b2
                                                                     : nullptr;
         const uint32_t par = lane == 0 ? p0 : lane == 1 ? p1 : p2;
-        return __all_sync(0xffffffffu,
-                          bar == nullptr || mbar_wait(bar, par)) &&
-               !*s_abort;
+        bool done = bar == nullptr;
+        for (int i = 0; i < (1 << 24); ++i) {
+          done = done || mbar_test_wait(bar, par);
+          if (__all_sync(0xffffffffu, done)) return true;
+        }
+        return false;
       };
       // S of step s, whose chunk's K tile is there; it is given back with
       // the chunk's last step
