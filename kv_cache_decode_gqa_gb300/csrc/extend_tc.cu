@@ -575,16 +575,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     reg_dec<48>();
     if (warp == kLoadWarp) {
       // ===================== bulk copies ==================================
-      // In alternation K and V of a chunk. The attended positions are
-      // widened to even bounds (rows of 72 bytes are copied in pairs; block
-      // sizes are even); blocks are one a lane, looked up a chunk ahead.
+      // In alternation K and V of a chunk. Chunks are looked up 32 / L at a
+      // time: lane l takes block l % L of chunk l / L of the batch (L: blocks
+      // a chunk may touch, a power of two), and later issues that block's
+      // copies. Attended positions are widened to even bounds (rows of 72
+      // bytes are copied in pairs; block sizes are even). L = 32 and more
+      // blocks (of 2 positions): a lane takes further ones when it issues.
       const int bs = p.block_size;
-      auto bounds = [&](int c, int &t0, int &t1, int &b0, int &nb) {
-        t0 = max(c * kN, k.lo) & ~1;
-        t1 = (min((c + 1) * kN, k.hi) + 1) & ~1;
-        b0 = t0 / bs;
-        nb = (t1 - 1) / bs - b0 + 1;
-      };
       auto block_of = [&](int lb) {
         int pb = p.block_table[(long)b * p.max_blocks + lb];
         if (pb < 0 || pb >= p.num_blocks) {
@@ -593,47 +590,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return pb;
       };
-      int t0, t1, b0, nb;
-      bounds(c0, t0, t1, b0, nb);
-      int pb = lane < nb ? block_of(b0 + lane) : 0;
+      int L = 1;
+      while (L < 32 && L < (bs % kN == 0   ? 1
+                            : kN % bs == 0 ? kN / bs
+                                           : kN / bs + 2))
+        L <<= 1;
+      const int lq = lane & (L - 1), batch = 32 / L;
+      const uint8_t *base_kv[2] = {p.k, p.v};
       int s = 0, ph = 1;
       int last[2 * kRawSlots];  // parity of each slot's last copy, or -1
 #pragma unroll
       for (int i = 0; i < 2 * kRawSlots; ++i) last[i] = -1;
       bool go = true;
-      for (int c = c0; go && c < c1; ++c) {
-        int u0 = 0, u1 = 0, v0 = 0, nv = 0, pbn = 0;
-        if (c + 1 < c1) {
-          bounds(c + 1, u0, u1, v0, nv);
-          if (lane < nv) pbn = block_of(v0 + lane);
+      for (int cb = c0; go && cb < c1; cb += batch) {
+        const int c = cb + lane / L;
+        int t0 = 0, t1 = 0, b0 = 0, nb = 0, pb = 0;
+        if (c < c1) {
+          t0 = max(c * kN, k.lo) & ~1;
+          t1 = (min((c + 1) * kN, k.hi) + 1) & ~1;
+          b0 = t0 / bs;
+          nb = (t1 - 1) / bs - b0 + 1;
+          if (lq < nb) pb = block_of(b0 + lq);
         }
-        for (int q = 0; q < 2; ++q) {  // K, V
-          go = wait_all(&rawempty[s], ph);
-          if (!go) {
-            give_up();
-            break;
-          }
-          if (lane == 0)
-            mbar_arrive_expect_tx(&rawfull[s], (uint32_t)(t1 - t0) * kRow);
-          __syncwarp();
-          const uint8_t *base = q ? p.v : p.k;
-          uint8_t *dst = raw_slot(s);
-          for (int j = lane; j < nb; j += 32) {
-            const int blk = j < 32 ? pb : block_of(b0 + j);
-            const int lb = b0 + j;
-            const int a0 = max(t0, lb * bs), a1 = min(t1, (lb + 1) * bs);
-            const long row = ((long)blk * p.n_kv + h) * bs + (a0 - lb * bs);
-            bulk_g2s(dst + (a0 - c * kN) * kRow, base + row * kRow,
-                     (uint32_t)(a1 - a0) * kRow, &rawfull[s]);
-          }
-          __syncwarp();
+        const int cnt = min(batch, c1 - cb);
+        for (int j = 0; go && j < cnt; ++j) {
 #pragma unroll
-          for (int i = 0; i < 2 * kRawSlots; ++i)
-            if (i == s) last[i] = ph ^ 1;
-          if (++s == nraw) s = 0, ph ^= 1;
+          for (int q = 0; q < 2; ++q) {  // K, V
+            go = go && wait_all(&rawempty[s], ph);
+            if (!go) break;
+            if (lane == j * L)
+              mbar_arrive_expect_tx(&rawfull[s], (uint32_t)(t1 - t0) * kRow);
+            __syncwarp();
+            if (lane / L == j) {
+              for (int m = lq; m < nb; m += L) {
+                const int blk = m < L ? pb : block_of(b0 + m);
+                const int lb = (b0 + m) * bs;
+                const int a0 = max(t0, lb), a1 = min(t1, lb + bs);
+                const long row = ((long)blk * p.n_kv + h) * bs + (a0 - lb);
+                bulk_g2s(raw_slot(s) + (a0 - c * kN) * kRow,
+                         base_kv[q] + row * kRow, (uint32_t)(a1 - a0) * kRow,
+                         &rawfull[s]);
+              }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2 * kRawSlots; ++i)
+              if (i == s) last[i] = ph ^ 1;
+            if (++s == nraw) s = 0, ph ^= 1;
+          }
         }
-        t0 = u0, t1 = u1, b0 = v0, nb = nv, pb = pbn;
       }
+      if (!go) give_up();
       if (!go) {
         // after an abort: every copy that was issued has landed before this
         // CTA gives its shared memory back
