@@ -1125,13 +1125,16 @@ ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
     return pl;
   }
   const long pairs = (long)rows * g;
-  pl.blocks = (int)(pairs / kvd::kExtendRows + std::min(s->batch, rows));
+  const int ctas_per_block = (long)max_rows * g > kvd::kExtendRows ? 2 : 1;
+  const int block_rows = ctas_per_block * kvd::kExtendRows;
+  pl.p.block_rows = block_rows;
+  pl.blocks = (int)(pairs / block_rows + std::min(s->batch, rows));
   const int ch = kvd::kExtendChunk;
   long chunks = (s->max_seq_len + ch - 1) / ch;
   if (s->window > 0)
     chunks = std::min<long>(
-        chunks, ((long)s->window + kvd::kExtendRows / g + ch) / ch + 2);
-  const long ctas = (long)pl.blocks * c->n_kv;
+        chunks, ((long)s->window + block_rows / g + ch) / ch + 2);
+  const long ctas = (long)pl.blocks * c->n_kv * ctas_per_block;
   const long want = forced > 0 ? forced : 4L * sms;
   if (forced > 0 || ctas < 2L * sms) {
     const long per = std::max(4L, (ctas * chunks + want - 1) / want);

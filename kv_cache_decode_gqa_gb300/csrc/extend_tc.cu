@@ -37,6 +37,7 @@
 //   warp 16            bulk copies of cached rows
 //   warp 17            tensor memory, MMA issue
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "kvd_common.cuh"
@@ -58,19 +59,30 @@ constexpr int kWiden0 = 8, kLoadWarp = 16, kMmaWarp = 17;
 constexpr int kSoftBar = 1;
 constexpr float kSlack = 8.f;        // log2 units the reference may lag by
 
-// shared memory: Q tiles, K ring, V ring (2 each), raw ring
-constexpr int Q_OFF = 0;
-constexpr int K_OFF = Q_OFF + 2 * kTile;
-constexpr int V_OFF = K_OFF + 2 * kTile;
-constexpr int RAW_OFF = V_OFF + 2 * kTile;
-constexpr int kRawSlots = 3;         // + 3 more in Q tile 1 when it is unused
-constexpr int F_OFF = RAW_OFF + kRawSlots * kRaw;  // float [4][128]
-constexpr int BAR_OFF = F_OFF + 4 * kM * 4;
-constexpr int kBars = 2 * (2 * kRawSlots) + 8 + 4 + 2;
-constexpr int FLAG_OFF = BAR_OFF + kBars * 8;      // int [8]
-constexpr int SCAN_OFF = FLAG_OFF + 32;            // int [20]
-constexpr int SMEM = SCAN_OFF + 128;
-static_assert(3 * kRaw <= kTile && SMEM <= 227 * 1024, "shared memory");
+// CTAS = 1 or 2 CTAs share a block's chunks (2: a cta_group::2 pair).
+// Shared memory: Q tiles, K ring, V ring (2 each), raw ring.
+template <int CTAS>
+struct TCfg {
+  static constexpr int ROWS = CTAS * kExtendRows;  // pairs per block
+  static constexpr int KV = kTile / CTAS;    // this CTA's part of a K, V tile
+  // 64-column half of its K part
+  static constexpr int KHALF = kHalf / CTAS;
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = Q_OFF + 2 * kTile;
+  static constexpr int V_OFF = K_OFF + 2 * KV;
+  static constexpr int RAW_OFF = V_OFF + 2 * KV;
+  // raw slots: one CTA has three, and three more in Q tile 1 when it is
+  // unused
+  static constexpr int OWN_SLOTS = CTAS == 1 ? 3 : 6;
+  static constexpr int SLOTS = 6;
+  static constexpr int F_OFF = RAW_OFF + OWN_SLOTS * kRaw;  // float [4][128]
+  static constexpr int BAR_OFF = F_OFF + 4 * kM * 4;
+  static constexpr int BARS = 2 * SLOTS + 8 + 4 + 2;
+  static constexpr int FLAG_OFF = BAR_OFF + BARS * 8;  // int [8]
+  static constexpr int SCAN_OFF = FLAG_OFF + 32;       // int [20]
+  static constexpr int SMEM = SCAN_OFF + 128;
+  static_assert(3 * kRaw <= kTile && SMEM <= 227 * 1024, "shared memory");
+};
 
 constexpr uint32_t kColS = 0, kColO = 256;         // + 128 * tile
 
@@ -128,8 +140,8 @@ __device__ __forceinline__ Block block_at(const ExtendParams &p, int b,
   Block k;
   k.n = seq_rows(p, b);
   k.T = min(max(p.seq_lens[b], 0), p.max_seq_len);
-  k.f0 = mb * kExtendRows;
-  k.f1 = min(k.f0 + kExtendRows, k.n * G);
+  k.f0 = mb * p.block_rows;
+  k.f1 = min(k.f0 + p.block_rows, k.n * G);
   const int first = k.T - k.n + k.f0 / G, last = k.T - k.n + (k.f1 - 1) / G;
   int lo = p.win_start ? max(p.win_start[b], 0) : 0;
   if (p.window > 0) lo = max(lo, first + 1 - p.window);
@@ -145,13 +157,16 @@ __device__ __forceinline__ void block_chunks(const Block &k, int &c0,
   c1 = k.lo < k.hi ? (k.hi + kN - 1) / kN : c0;
 }
 
+template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
     extend_tc_kernel(const __grid_constant__ ExtendParams p) {
+  using C = TCfg<CTAS>;
+  constexpr bool PAIR = CTAS == 2;
   extern __shared__ __align__(1024) uint8_t smem[];
-  float *fs = reinterpret_cast<float *>(smem + F_OFF);
-  uint64_t *rawfull = reinterpret_cast<uint64_t *>(smem + BAR_OFF);
-  uint64_t *rawempty = rawfull + 2 * kRawSlots;
-  uint64_t *kfull = rawempty + 2 * kRawSlots;  // [2] each
+  float *fs = reinterpret_cast<float *>(smem + C::F_OFF);
+  uint64_t *rawfull = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+  uint64_t *rawempty = rawfull + C::SLOTS;
+  uint64_t *kfull = rawempty + C::SLOTS;  // [2] each
   uint64_t *kempty = kfull + 2;
   uint64_t *vfull = kempty + 2;
   uint64_t *vempty = vfull + 2;
@@ -159,10 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *pfull = sfull + 2;
   uint64_t *qfull = pfull + 2;
   uint64_t *odone = qfull + 1;
-  int *flags = reinterpret_cast<int *>(smem + FLAG_OFF);
+  int *flags = reinterpret_cast<int *>(smem + C::FLAG_OFF);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(flags);
   int *s_blk = flags + 2;  // sequence and block of this CTA, total blocks
-  int *s_scan = reinterpret_cast<int *>(smem + SCAN_OFF);
+  int *s_scan = reinterpret_cast<int *>(smem + C::SCAN_OFF);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.n_h / p.n_kv;
@@ -172,8 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   // launch's predecessor
   // ---- which block: a scan of the sequences' block counts --------------
   // The last blocks come first: under the causal mask they are the longest.
-  const int h = (int)blockIdx.x % p.n_kv;
-  const int want = (int)blockIdx.x / p.n_kv;
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int item = (int)blockIdx.x / CTAS;  // the same for a pair's CTAs
+  const int h = item % p.n_kv;
+  const int want = item / p.n_kv;
   if (tid == 0) s_blk[0] = -1;
   {
     int cnt[2], sum = 0;
@@ -183,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cnt[j] = 0;
       if (b < p.batch) {
         const int n = seq_rows(p, b);
-        cnt[j] = (int)(((long)n * G + kExtendRows - 1) / kExtendRows);
+        cnt[j] = (int)(((long)n * G + C::ROWS - 1) / C::ROWS);
         if (blockIdx.x == 0 && blockIdx.y == 0) {
           if (n == 0 && p.row_start && p.row_start[b] != p.row_start[b + 1])
             report(p.err, DEVERR_LEN);
@@ -238,12 +255,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return (row0 + f / G) * p.n_h + (long)h * G + f % G;
   };
   if (nch <= 0) {  // nothing is seen (parts is 1)
-    for (int i = tid; i < np * (kD / 8); i += kThreads)
+    for (int i = rank * kThreads + tid; i < np * (kD / 8);
+         i += CTAS * kThreads)
       reinterpret_cast<uint4 *>(p.out + out_row(k.f0 + i / (kD / 8)) *
                                             kD)[i % (kD / 8)] =
           make_uint4(0, 0, 0, 0);
     if (p.lse)
-      for (int i = tid; i < np; i += kThreads)
+      for (int i = rank * kThreads + tid; i < np; i += CTAS * kThreads)
         p.lse[out_row(k.f0 + i)] = -INFINITY;
     return;
   }
@@ -252,39 +270,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) report(p.err, DEVERR_TIMEOUT);
     return;
   }
-  const bool two = np > kM;
-  const int nraw = two ? kRawSlots : 2 * kRawSlots;
+  const bool two = PAIR || np > kM;
+  const int nraw = two ? C::OWN_SLOTS : C::SLOTS;
   // step s: tile s & 1; chunk s / 2 for two tiles, chunk s for one
   const int nsteps = two ? 2 * nch : nch;
 
   if (tid == 0) {
-    for (int i = 0; i < 2 * kRawSlots; ++i) {
+    for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&rawfull[i], 1);
       mbar_init(&rawempty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&kfull[i], 4);
+      mbar_init(&kfull[i], 4 * CTAS);
       mbar_init(&kempty[i], 1);
-      mbar_init(&vfull[i], 4);
+      mbar_init(&vfull[i], 4 * CTAS);
       mbar_init(&vempty[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[i], 4 * CTAS);
     }
-    mbar_init(qfull, two ? 8 : 4);
+    mbar_init(qfull, CTAS * (two ? 8 : 4));
     mbar_init(odone, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(s_tmem, 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem2_alloc(s_tmem, 512);
+      tmem2_relinquish();
+    } else {
+      tmem_alloc(s_tmem, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the other CTA's barriers too
   tc_fence_after();
   const uint32_t tbase = *s_tmem;
   auto raw_slot = [&](int s) {
-    return smem + (s < kRawSlots ? RAW_OFF + s * kRaw
-                                 : Q_OFF + kTile + (s - kRawSlots) * kRaw);
+    return smem + (s < C::OWN_SLOTS
+                       ? C::RAW_OFF + s * kRaw
+                       : C::Q_OFF + kTile + (s - C::OWN_SLOTS) * kRaw);
   };
   // Every wait is bounded; a role that gives up leaves its loop, and the
   // others follow when their own waits run out. (A flag to leave earlier
@@ -295,17 +320,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_all = [&](uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
   };
+  // Arrivals that the MMA warp (CTA 0's in a pair) waits for, and commits
+  // that the roles of every CTA wait for.
+  auto arrive_mma = [&](uint64_t *bar) {
+    if constexpr (PAIR)
+      mbar_arrive_remote_cta(cluster_saddr(bar, 0));
+    else
+      mbar_arrive(bar);
+  };
+  auto commit = [&](uint64_t *bar) {
+    if constexpr (PAIR)
+      umma2_commit_elect(bar);
+    else
+      umma_commit_elect(bar);
+  };
 
   if (warp < kWiden0) {
     // ======================= softmax ======================================
     reg_inc<168>();
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // pair of the tile
-    const int ri = two ? t * kM + r : r;   // pair of the block
+    // pair of the block (a pair of CTAs: tile t's first half is CTA 0's)
+    const int ri = two ? (t * CTAS + rank) * kM + r : r;
     const bool live = ri < np;
     const int f = k.f0 + ri;
     const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-    int vlo = 0, vhi = 0;                  // positions this pair sees
+    // positions this pair sees (a pair that does not exist: all, so that its
+    // warp masks nothing for it; its query is 0 and nothing of it is stored)
+    int vlo = 0, vhi = INT_MAX;
     if (live) {
       const int pos = k.T - k.n + f / G;
       vhi = max(pos + 1, 0);
@@ -334,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float sc = __uint_as_float((uint32_t)e << 23);
       sl = fmaxf(p.scale_log2 * exp2f((float)(127 - e)), 1.17549435e-38f);
       if (two || t == 0) {
-        uint8_t *qt = smem + Q_OFF + (two ? t * kTile : 0);
+        uint8_t *qt = smem + C::Q_OFF + (two ? t * kTile : 0);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           uint4 w;
@@ -347,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(qfull);
+        if (lane == 0) arrive_mma(qfull);
       }
     }
     const bool warp_live = __any_sync(0xffffffffu, live);
@@ -368,13 +410,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; g < 4; ++g) tmem_wait_ld(x[g]);
         // columns [a, z) of the chunk are seen
         const int a = vlo - c * kN, z = vhi - c * kN;
-        if (__any_sync(0xffffffffu, a > 0 || z < kN)) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 4; ++g) {
+          // groups of 32 columns that some pair of the warp sees in part
+          if (__any_sync(0xffffffffu, a > 32 * g || z < 32 * g + 32)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (32 * g + i < a || 32 * g + i >= z)
                 x[g][i] = 0xff800000u;  // -inf
+          }
         }
         float mx[4];
 #pragma unroll
@@ -436,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[t]);
+      if (lane == 0) arrive_mma(&pfull[t]);
     }
     // ---- epilogue --------------------------------------------------------
     const bool ok = wait_all(odone, 0);
@@ -512,8 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kLoadWarp) {
     // ======================= widening =====================================
     reg_dec<48>();
-    const int r = (tid - kWiden0 * 32) & 127;  // row of the chunk
+    // A thread widens a row of the chunk, 128 columns; in a pair 64: CTA
+    // `rank` has K rows [64 rank, + 64) (N of the scores' product) and V
+    // columns [64 rank, + 64) (N of the outputs')
+    const int tw = (tid - kWiden0 * 32) & 127;
     const bool is_v = warp >= kWiden0 + 4;
+    constexpr int kGroups = 8 / CTAS;  // 16-column groups a thread
+    const int r = PAIR && !is_v ? tw & 63 : tw;        // row of the raw unit
+    const int g0 = !PAIR ? 0 : is_v ? 4 * rank : 4 * (tw >> 6);
+    const int row0c = PAIR && !is_v ? 64 * rank : 0;   // its chunk position
+    const uint32_t half = PAIR ? C::KHALF : kHalf;     // of the tile written
     uint64_t *tfull = is_v ? vfull : kfull, *tempty = is_v ? vempty : kempty;
     // K rows are raw units 0, 2, 4, ..., V rows 1, 3, 5, ...
     int rs = is_v, rph = 0;
@@ -524,16 +576,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const uint8_t *src = raw_slot(rs) + r * kRow;
-      uint2 w[9];
+      uint2 w[kGroups];
+      uint32_t sw[kGroups / 4];  // scales, four a word
 #pragma unroll
-      for (int g = 0; g < 9; ++g)
-        w[g] = *reinterpret_cast<const uint2 *>(src + 8 * g);
-      const int pos = (c0 + i) * kN + r;
+      for (int g = 0; g < kGroups; ++g)
+        w[g] = *reinterpret_cast<const uint2 *>(src + 8 * (g0 + g));
+#pragma unroll
+      for (int g = 0; g < kGroups / 4; ++g)
+        sw[g] = *reinterpret_cast<const uint32_t *>(src + 64 + g0 + 4 * g);
+      const int pos = (c0 + i) * kN + row0c + r;
       if (pos < k.lo || pos >= k.hi) {
         // a row that was not copied, or that no pair sees: zeros, so that 0
         // times it stays 0
 #pragma unroll
-        for (int g = 0; g < 9; ++g) w[g] = make_uint2(0, 0);
+        for (int g = 0; g < kGroups; ++g) w[g] = make_uint2(0, 0);
+#pragma unroll
+        for (int g = 0; g < kGroups / 4; ++g) sw[g] = 0;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&rawempty[rs]);
@@ -543,33 +601,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         give_up();
         break;
       }
-      uint8_t *dst = smem + (is_v ? V_OFF : K_OFF) + st * kTile;
-      const uint32_t sc[4] = {e4m3x2_to_f16x2((uint16_t)w[8].x),
-                              e4m3x2_to_f16x2((uint16_t)(w[8].x >> 16)),
-                              e4m3x2_to_f16x2((uint16_t)w[8].y),
-                              e4m3x2_to_f16x2((uint16_t)(w[8].y >> 16))};
+      uint8_t *dst = smem + (is_v ? C::V_OFF : C::K_OFF) + st * C::KV;
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const uint32_t s2 =
-            prmt(sc[g >> 1], 0, (g & 1) ? 0x3232 : 0x1010);
+      for (int g = 0; g < kGroups; ++g) {
+        const uint32_t sp = e4m3x2_to_f16x2(
+            (uint16_t)(sw[g >> 2] >> (16 * ((g >> 1) & 1))));
+        const uint32_t s2 = prmt(sp, 0, (g & 1) ? 0x3232 : 0x1010);
         const uint32_t cw[2] = {w[g].x, w[g].y};
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t h[4];
-          e2m1x8_to_f16(cw[q], h);
+          uint32_t x[4];
+          e2m1x8_to_f16(cw[q], x);
           uint4 y;
-          y.x = mul_f16x2(h[0], s2);
-          y.y = mul_f16x2(h[1], s2);
-          y.z = mul_f16x2(h[2], s2);
-          y.w = mul_f16x2(h[3], s2);
-          const int c = 2 * g + q;
-          *reinterpret_cast<uint4 *>(dst + (c >> 3) * kHalf +
+          y.x = mul_f16x2(x[0], s2);
+          y.y = mul_f16x2(x[1], s2);
+          y.z = mul_f16x2(x[2], s2);
+          y.w = mul_f16x2(x[3], s2);
+          // 16-byte piece of the row: of the CTA's own columns for V
+          const int c = 2 * ((PAIR && is_v ? 0 : g0) + g) + q;
+          *reinterpret_cast<uint4 *>(dst + (c >> 3) * half +
                                      sw128(r, c & 7)) = y;
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tfull[st]);
+      if (lane == 0) arrive_mma(&tfull[st]);
     }
   } else {
     reg_dec<48>();
@@ -598,9 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lq = lane & (L - 1), batch = 32 / L;
       const uint8_t *base_kv[2] = {p.k, p.v};
       int s = 0, ph = 1;
-      int last[2 * kRawSlots];  // parity of each slot's last copy, or -1
+      int last[C::SLOTS];  // parity of each slot's last copy, or -1
 #pragma unroll
-      for (int i = 0; i < 2 * kRawSlots; ++i) last[i] = -1;
+      for (int i = 0; i < C::SLOTS; ++i) last[i] = -1;
       bool go = true;
       for (int cb = c0; go && cb < c1; cb += batch) {
         const int c = cb + lane / L;
@@ -618,23 +674,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 2; ++q) {  // K, V
             go = go && wait_all(&rawempty[s], ph);
             if (!go) break;
+            // in a pair K rows are this CTA's half of the chunk
+            const int base = c * kN + (PAIR && q == 0 ? 64 * rank : 0);
+            const int u0 = PAIR && q == 0 ? max(t0, base) : t0;
+            const int u1 = PAIR && q == 0 ? min(t1, base + 64) : t1;
             if (lane == j * L)
-              mbar_arrive_expect_tx(&rawfull[s], (uint32_t)(t1 - t0) * kRow);
+              mbar_arrive_expect_tx(&rawfull[s],
+                                    (uint32_t)max(u1 - u0, 0) * kRow);
             __syncwarp();
             if (lane / L == j) {
               for (int m = lq; m < nb; m += L) {
                 const int blk = m < L ? pb : block_of(b0 + m);
                 const int lb = (b0 + m) * bs;
-                const int a0 = max(t0, lb), a1 = min(t1, lb + bs);
+                const int a0 = max(u0, lb), a1 = min(u1, lb + bs);
+                if (PAIR && a0 >= a1) continue;
                 const long row = ((long)blk * p.n_kv + h) * bs + (a0 - lb);
-                bulk_g2s(raw_slot(s) + (a0 - c * kN) * kRow,
+                bulk_g2s(raw_slot(s) + (a0 - base) * kRow,
                          base_kv[q] + row * kRow, (uint32_t)(a1 - a0) * kRow,
                          &rawfull[s]);
               }
             }
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 2 * kRawSlots; ++i)
+            for (int i = 0; i < C::SLOTS; ++i)
               if (i == s) last[i] = ph ^ 1;
             if (++s == nraw) s = 0, ph ^= 1;
           }
@@ -645,27 +707,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         // after an abort: every copy that was issued has landed before this
         // CTA gives its shared memory back
 #pragma unroll
-        for (int i = 0; i < 2 * kRawSlots; ++i)
+        for (int i = 0; i < C::SLOTS; ++i)
           if (last[i] >= 0) mbar_wait(&rawfull[i], last[i]);
       }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp && rank == 0) {
       // ===================== MMA issue ====================================
-      constexpr uint32_t idS = umma_idesc_f16(kM, kN, false);
-      constexpr uint32_t idO = umma_idesc_f16(kM, kD, true);
-      const uint32_t q0 = smem_u32(smem + Q_OFF);
-      const uint32_t k0 = smem_u32(smem + K_OFF);
-      const uint32_t v0 = smem_u32(smem + V_OFF);
+      constexpr uint32_t idS = umma_idesc_f16(CTAS * kM, kN, false);
+      constexpr uint32_t idO = umma_idesc_f16(CTAS * kM, kD, true);
+      const uint32_t q0 = smem_u32(smem + C::Q_OFF);
+      const uint32_t k0 = smem_u32(smem + C::K_OFF);
+      const uint32_t v0 = smem_u32(smem + C::V_OFF);
       auto chunk_of = [&](int s) { return two ? s >> 1 : s; };
-      // Up to three barriers at once, one a lane, by polling: a wait costs a
-      // few hundred cycles here even when its phase is over (the shared
-      // memory pipe is busy with the tiles), and a suspending wait on
-      // several addresses slept through their completion.
+      // A step's barriers: the one that comes last as a rule (P, or Q) by a
+      // suspending wait, which leaves the issue slots to the softmax warps;
+      // the others, as a rule complete by then, together, one a lane.
       auto wait3 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1,
                        uint64_t *b2, uint32_t p2) {
-        uint64_t *bar = lane == 0 ? b0 : lane == 1 ? b1 : lane == 2 ? b2
-                                                                    : nullptr;
-        const uint32_t par = lane == 0 ? p0 : lane == 1 ? p1 : p2;
+        if (!wait_all(b0, p0)) return false;
+        uint64_t *bar = lane == 1 ? b1 : lane == 2 ? b2 : nullptr;
+        const uint32_t par = lane == 1 ? p1 : p2;
         bool done = bar == nullptr;
+        if (b1 == nullptr && b2 == nullptr) return true;
         for (int i = 0; i < (1 << 24); ++i) {
           done = done || mbar_test_wait(bar, par);
           if (__all_sync(0xffffffffu, done)) return true;
@@ -678,16 +740,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = s & 1, st = chunk_of(s) & 1;
         const uint64_t a = umma_desc_sw128(q0 + (two ? t * kTile : 0), 16,
                                            1024);
-        const uint64_t bk = umma_desc_sw128(k0 + st * kTile, 16, 1024);
+        const uint64_t bk = umma_desc_sw128(k0 + st * C::KV, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < kD / 16; ++ks) {
-          const uint64_t off =
-              (uint64_t)(((ks >> 2) * kHalf + (ks & 3) * 32) >> 4);
-          umma_ss_elect(tbase + kColS + 128 * t, a + off, bk + off, idS,
-                        ks > 0 ? 1u : 0u);
+          const uint32_t step = (ks & 3) * 32;
+          const uint64_t ao = a + (((ks >> 2) * kHalf + step) >> 4);
+          const uint64_t bo = bk + (((ks >> 2) * C::KHALF + step) >> 4);
+          if constexpr (PAIR)
+            umma2_ss_elect(tbase + kColS + 128 * t, ao, bo, idS,
+                           ks > 0 ? 1u : 0u);
+          else
+            umma_ss_elect(tbase + kColS + 128 * t, ao, bo, idS,
+                          ks > 0 ? 1u : 0u);
         }
-        umma_commit_elect(&sfull[t]);
-        if (!two || t == 1) umma_commit_elect(&kempty[st]);
+        commit(&sfull[t]);
+        if (!two || t == 1) commit(&kempty[st]);
       };
       // the K barrier that step s waits for (its chunk's first step only)
       auto kbar = [&](int s) -> uint64_t * {
@@ -709,27 +776,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                    kbar(s + 2), kpar(s + 2));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t bv = umma_desc_sw128(v0 + st * kTile, kHalf, 1024);
+        const uint64_t bv = umma_desc_sw128(v0 + st * C::KV, kHalf, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kN / 16; ++kk)
-          umma_ts_elect(tbase + kColO + 128 * t,
-                        tbase + kColS + 128 * t + kk * 8,
-                        bv + (uint64_t)((kk * 2048) >> 4), idO,
-                        (s > 1 || kk > 0) ? 1u : 0u);
-        if (!two || t == 1) umma_commit_elect(&vempty[st]);
+        for (int kk = 0; kk < kN / 16; ++kk) {
+          const uint64_t bo = bv + (uint64_t)((kk * 2048) >> 4);
+          const uint32_t acc = (s > 1 || kk > 0) ? 1u : 0u;
+          if constexpr (PAIR)
+            umma2_ts_elect(tbase + kColO + 128 * t,
+                           tbase + kColS + 128 * t + kk * 8, bo, idO, acc);
+          else
+            umma_ts_elect(tbase + kColO + 128 * t,
+                          tbase + kColS + 128 * t + kk * 8, bo, idO, acc);
+        }
+        if (!two || t == 1) commit(&vempty[st]);
         if (s + 2 < nsteps) issue_s(s + 2);
       }
       if (!ok) give_up();
       // every MMA issued has completed before the epilogue and the dealloc
-      umma_commit_elect(odone);
+      commit(odone);
       mbar_wait(odone, 0);
     }
   }
   tc_fence_before();
-  __syncthreads();  // every read of tensor memory is done
+  // every read of tensor memory is done (a pair: and every arrival on the
+  // other CTA's barriers)
+  if constexpr (PAIR)
+    cluster_sync();
+  else
+    __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    if constexpr (PAIR)
+      tmem2_dealloc(tbase, 512);
+    else
+      tmem_dealloc(tbase, 512);
   }
 }
 
@@ -761,7 +841,7 @@ __global__ void __launch_bounds__(kRowMergeThreads)
     r0 = p.row_start[b];
   }
   if (row < r0 || row >= r0 + seq_rows(p, b)) return;  // no sequence's row
-  const Block k = block_at(p, b, ((row - r0) * G + hh % G) / kExtendRows, G);
+  const Block k = block_at(p, b, ((row - r0) * G + hh % G) / p.block_rows, G);
   int c0, c1;
   block_chunks(k, c0, c1);
   const int parts = (c1 - c0 + p.chunks_per_split - 1) / p.chunks_per_split;
@@ -781,17 +861,28 @@ __global__ void __launch_bounds__(kRowMergeThreads)
 
 }  // namespace
 
+template <int CTAS>
+static cudaError_t launch_tc_t(const ExtendParams &p, int blocks, int splits,
+                               cudaStream_t s) {
+  using C = TCfg<CTAS>;
+  static bool done[64] = {};
+  auto kern = extend_tc_kernel<CTAS>;
+  const cudaError_t e = set_smem_once(kern, C::SMEM, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(blocks * p.n_kv * CTAS, splits), dim3(kThreads),
+                    C::SMEM, s, CTAS, p);
+}
+
 cudaError_t launch_extend_tc(const ExtendParams &p, int blocks, int splits,
                              cudaStream_t s) {
-  static bool done[64] = {};
-  cudaError_t e = set_smem_once(extend_tc_kernel, SMEM, done);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(extend_tc_kernel, dim3(blocks * p.n_kv, splits),
-                 dim3(kThreads), SMEM, s, 1, p);
+  const cudaError_t e = p.block_rows == kExtendRows
+                            ? launch_tc_t<1>(p, blocks, splits, s)
+                            : launch_tc_t<2>(p, blocks, splits, s);
   if (e != cudaSuccess || splits <= 1) return e;
   const long rows = (long)p.rows * p.n_h;
   const long per = kRowMergeThreads / 32;
-  return launch_pdl(extend_merge_kernel, dim3((unsigned)((rows + per - 1) / per)),
+  return launch_pdl(extend_merge_kernel,
+                    dim3((unsigned)((rows + per - 1) / per)),
                     dim3(kRowMergeThreads), 0, s, 1, p);
 }
 

@@ -95,7 +95,9 @@ struct ExtendParams : DecodeParams {
   const int32_t *row_start;  // [batch + 1], or null: row b is sequence b's
   int32_t max_rows, rows;    // bound on a sequence's rows; rows of q
   long q_rs, q_hs;           // strides of q between rows and heads, elements
-  int32_t chunks_per_split;  // tensor-memory kernel: chunks a CTA takes
+  // tcgen05 kernel: pairs of a row block, and chunks of it that one CTA (or
+  // pair of CTAs) takes
+  int32_t block_rows, chunks_per_split;
 };
 
 struct IndexerParams {
@@ -206,10 +208,11 @@ FewPlan extend_few_plan(int n_kv, int block_size, int pairs, long batch,
                         int max_seq_len, int sms);
 cudaError_t launch_extend_few(const ExtendParams &p, const FewPlan &f,
                               cudaStream_t s);
-// kvd_gqa_extend otherwise, on tcgen05: blocks of kExtendRows (row, head)
-// pairs of a kv head against chunks of kExtendChunk positions, each CTA
-// taking chunks_per_split of a block's chunks (0: all of them; else partials
-// [split][rows][n_h] and a merge launch). `blocks`: a bound on the row
+// kvd_gqa_extend otherwise, on tcgen05: blocks of block_rows (row, head)
+// pairs of a kv head -- kExtendRows a CTA, 2 kExtendRows a pair of CTAs --
+// against chunks of kExtendChunk positions, chunks_per_split of a block's at
+// a time (0: all of them; else partials [split][rows][n_h] and a merge
+// launch). `blocks`: a bound on the row
 // blocks of the batch, `splits` on a block's splits.
 constexpr int kExtendRows = 256;
 constexpr int kExtendChunk = 128;
