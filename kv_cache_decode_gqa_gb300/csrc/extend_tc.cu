@@ -718,21 +718,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k0 = smem_u32(smem + C::K_OFF);
       const uint32_t v0 = smem_u32(smem + C::V_OFF);
       auto chunk_of = [&](int s) { return two ? s >> 1 : s; };
-      // A step's barriers: the one that comes last as a rule (P, or Q) by a
-      // suspending wait, which leaves the issue slots to the softmax warps;
-      // the others, as a rule complete by then, together, one a lane.
+      // A step's barriers: first those that are complete by then as a rule,
+      // one a lane; last the one that is not (P, or Q), by a suspending wait,
+      // which leaves the issue slots to the softmax warps.
       auto wait3 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1,
-                       uint64_t *b2, uint32_t p2) {
-        if (!wait_all(b0, p0)) return false;
-        uint64_t *bar = lane == 1 ? b1 : lane == 2 ? b2 : nullptr;
-        const uint32_t par = lane == 1 ? p1 : p2;
-        bool done = bar == nullptr;
-        if (b1 == nullptr && b2 == nullptr) return true;
-        for (int i = 0; i < (1 << 24); ++i) {
-          done = done || mbar_test_wait(bar, par);
-          if (__all_sync(0xffffffffu, done)) return true;
+                       uint64_t *b2, uint32_t p2) -> bool {
+        if (b1 != nullptr || b2 != nullptr) {
+          uint64_t *bar = lane == 1 ? b1 : lane == 2 ? b2 : nullptr;
+          const uint32_t par = lane == 1 ? p1 : p2;
+          bool done = bar == nullptr;
+          int i = 0;
+          for (; i < (1 << 24); ++i) {
+            done = done || mbar_test_wait(bar, par);
+            if (__all_sync(0xffffffffu, done)) break;
+          }
+          if (i == (1 << 24)) return false;
         }
-        return false;
+        return wait_all(b0, p0);
       };
       // S of step s, whose chunk's K tile is there; it is given back with
       // the chunk's last step
