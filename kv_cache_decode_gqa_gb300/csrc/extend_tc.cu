@@ -30,12 +30,12 @@
 // (see extend_few.cu).
 //
 // Warp roles (640 threads, one CTA per SM; registers are moved from the
-// launch's 96 a thread to 168 for the softmax and 48 for the others):
+// launch's 96 a thread to 128 for the softmax and 72 for the others):
 //   warps 0-3, 4-7     softmax of tile 0 and 1, query load, epilogue
 //   warps 8-11, 12-15  widening of K and of V (one group for both took 3,300
 //                      cycles a chunk, the softmax and products 2,300)
 //   warp 16            bulk copies of cached rows
-//   warp 17            tensor memory, MMA issue
+//   warps 17, 18       MMA issue of tile 0 and 1 (17: tensor memory)
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -51,6 +51,7 @@ constexpr int kD = 128;
 constexpr int kRow = 72;             // bytes of a cached row
 constexpr int kM = 128;              // pairs per tile
 constexpr int kN = kExtendChunk;     // positions per chunk
+constexpr int kS = kN / 2;           // positions per product (half a chunk)
 constexpr int kTile = 128 * 256;     // a 128 x 128 f16 operand tile, 32 KB
 constexpr int kHalf = 128 * 128;     // its 64-column half
 constexpr int kRaw = kN * kRow;      // raw K (or V) rows of a chunk
@@ -77,13 +78,14 @@ struct TCfg {
   static constexpr int SLOTS = 6;
   static constexpr int F_OFF = RAW_OFF + OWN_SLOTS * kRaw;  // float [4][128]
   static constexpr int BAR_OFF = F_OFF + 4 * kM * 4;
-  static constexpr int BARS = 2 * SLOTS + 8 + 4 + 2;
+  static constexpr int BARS = 2 * SLOTS + 8 + 10 + 2;
   static constexpr int FLAG_OFF = BAR_OFF + BARS * 8;  // int [8]
   static constexpr int SCAN_OFF = FLAG_OFF + 32;       // int [20]
   static constexpr int SMEM = SCAN_OFF + 128;
   static_assert(3 * kRaw <= kTile && SMEM <= 227 * 1024, "shared memory");
 };
 
+// Tensor memory: two score buffers of 64 columns a tile, then the outputs.
 constexpr uint32_t kColS = 0, kColO = 256;         // + 128 * tile
 
 // 16-byte piece c (0..7) of row r in a 128-byte-swizzled 64-column half.
@@ -170,9 +172,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *kempty = kfull + 2;
   uint64_t *vfull = kempty + 2;
   uint64_t *vempty = vfull + 2;
-  uint64_t *sfull = vempty + 2;
-  uint64_t *pfull = sfull + 2;
-  uint64_t *qfull = pfull + 2;
+  uint64_t *sfull = vempty + 2;  // [tile][buffer]
+  uint64_t *pfull = sfull + 4;   // [tile][buffer]
+  uint64_t *pvdone = pfull + 4;  // [tile]
+  uint64_t *qfull = pvdone + 2;
   uint64_t *odone = qfull + 1;
   int *flags = reinterpret_cast<int *>(smem + C::FLAG_OFF);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(flags);
@@ -272,8 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const bool two = PAIR || np > kM;
   const int nraw = two ? C::OWN_SLOTS : C::SLOTS;
-  // step s: tile s & 1; chunk s / 2 for two tiles, chunk s for one
-  const int nsteps = two ? 2 * nch : nch;
+  // Step v of tile t: half v & 1 of a chunk -- chunk v / 2 of the range for
+  // two tiles, chunks t, t + 2, ... for one tile's two halves
+  auto chunk_of = [&](int t, int v) { return two ? v >> 1 : (v & ~1) + t; };
+  auto steps_of = [&](int t) { return two ? 2 * nch : (nch - t + 1) & ~1; };
 
   if (tid == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
@@ -282,14 +287,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], 4 * CTAS);
-      mbar_init(&kempty[i], 1);
+      mbar_init(&kempty[i], two ? 2 : 1);  // one commit a tile
       mbar_init(&vfull[i], 4 * CTAS);
-      mbar_init(&vempty[i], 1);
+      mbar_init(&vempty[i], two ? 2 : 1);
+      mbar_init(&pvdone[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4 * CTAS);
     }
     mbar_init(qfull, CTAS * (two ? 8 : 4));
-    mbar_init(odone, 1);
+    mbar_init(odone, 2);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -337,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kWiden0) {
     // ======================= softmax ======================================
-    reg_inc<168>();
+    reg_inc<128>();
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // pair of the tile
     // pair of the block (a pair of CTAs: tile t's first half is CTA 0's)
@@ -394,24 +402,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const bool warp_live = __any_sync(0xffffffffu, live);
     float ref = -INFINITY, l = 0.f;
-    for (int j = 0, s = t; s < nsteps; s += 2, ++j) {
-      const int c = c0 + (two ? j : s);
-      if (!wait_all(&sfull[t], j & 1)) {
+    const uint64_t sl2 = pack_f32x2(sl, sl);
+    const int nv = steps_of(t);
+    for (int v = 0; v < nv; ++v) {
+      const int buf = v & 1;
+      const int pos0 = (c0 + chunk_of(t, v)) * kN + buf * kS;
+      if (!wait_all(&sfull[2 * t + buf], (v >> 1) & 1)) {
         give_up();
         break;
       }
       tc_fence_after();
       if (warp_live) {
-        uint32_t x[4][32];
-        const uint32_t ts = tl + kColS + 128 * t;
+        uint32_t x[2][32];
+        const uint32_t ts = tl + kColS + 128 * t + kS * buf;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) tmem_ld32(ts + 32 * g, x[g]);
+        for (int g = 0; g < 2; ++g) tmem_ld32(ts + 32 * g, x[g]);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) tmem_wait_ld(x[g]);
-        // columns [a, z) of the chunk are seen
-        const int a = vlo - c * kN, z = vhi - c * kN;
+        for (int g = 0; g < 2; ++g) tmem_wait_ld(x[g]);
+        // columns [a, z) are seen
+        const int a = vlo - pos0, z = vhi - pos0;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
           // groups of 32 columns that some pair of the warp sees in part
           if (__any_sync(0xffffffffu, a > 32 * g || z < 32 * g + 32)) {
 #pragma unroll
@@ -423,11 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          mx[g] = fmaxf(__uint_as_float(x[g][0]), __uint_as_float(x[g][1]));
+          const uint32_t *y = &x[g >> 1][16 * (g & 1)];
+          mx[g] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 #pragma unroll
-          for (int i = 2; i < 32; i += 2)
-            mx[g] = max3(mx[g], __uint_as_float(x[g][i]),
-                         __uint_as_float(x[g][i + 1]));
+          for (int i = 2; i < 16; i += 2)
+            mx[g] = max3(mx[g], __uint_as_float(y[i]),
+                         __uint_as_float(y[i + 1]));
         }
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl;
         const bool grow = top > ref + kSlack;  // from -inf: any score
@@ -435,8 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float al = grow ? ex2(ref - top) : 1.f;
           if (grow) ref = top;
           l *= al;
-          if (j > 0) {
-            // sfull of this step followed PV of the tile's last step
+          if (v > 0) {
+            // the tile's last product into O has to be over (this step's
+            // scores followed the one before it)
+            if (!wait_all(&pvdone[t], (v - 1) & 1)) {
+              give_up();
+              break;
+            }
+            tc_fence_after();
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
               uint32_t o[16];
@@ -451,10 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float mu = ref == -INFINITY ? 0.f : ref;
-        const uint64_t sl2 = pack_f32x2(sl, sl), mu2 = pack_f32x2(-mu, -mu);
+        const uint64_t mu2 = pack_f32x2(-mu, -mu);
         uint64_t ls[2] = {0, 0};
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -480,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_mma(&pfull[t]);
+      if (lane == 0) arrive_mma(&pfull[2 * t + buf]);
     }
     // ---- epilogue --------------------------------------------------------
     const bool ok = wait_all(odone, 0);
@@ -508,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ncol = two ? kD : kD / 2;
     const int col0 = two ? 0 : t * (kD / 2);
     const uint32_t ta = tl + kColO + (two ? 128 * t : 0) + col0;
-    const bool second = !two && nsteps > 1;
+    const bool second = !two && nch > 1;
     if (warp_live && ok) {
 #pragma unroll 1
       for (int g = 0; g < ncol; g += 32) {
@@ -555,16 +573,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kLoadWarp) {
     // ======================= widening =====================================
-    reg_dec<48>();
+    reg_dec<72>();
     // A thread widens a row of the chunk, 128 columns; in a pair 64: CTA
-    // `rank` has K rows [64 rank, + 64) (N of the scores' product) and V
-    // columns [64 rank, + 64) (N of the outputs')
+    // `rank` has the K rows [32 rank, + 32) of either half of the chunk (N of
+    // the scores' products) and V columns [64 rank, + 64) (N of the outputs')
     const int tw = (tid - kWiden0 * 32) & 127;
     const bool is_v = warp >= kWiden0 + 4;
     constexpr int kGroups = 8 / CTAS;  // 16-column groups a thread
     const int r = PAIR && !is_v ? tw & 63 : tw;        // row of the raw unit
     const int g0 = !PAIR ? 0 : is_v ? 4 * rank : 4 * (tw >> 6);
-    const int row0c = PAIR && !is_v ? 64 * rank : 0;   // its chunk position
+    // its position in the chunk
+    const int cpos = PAIR && !is_v ? (r & 31) + 64 * (r >> 5) + 32 * rank : r;
     const uint32_t half = PAIR ? C::KHALF : kHalf;     // of the tile written
     uint64_t *tfull = is_v ? vfull : kfull, *tempty = is_v ? vempty : kempty;
     // K rows are raw units 0, 2, 4, ..., V rows 1, 3, 5, ...
@@ -584,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int g = 0; g < kGroups / 4; ++g)
         sw[g] = *reinterpret_cast<const uint32_t *>(src + 64 + g0 + 4 * g);
-      const int pos = (c0 + i) * kN + row0c + r;
+      const int pos = (c0 + i) * kN + cpos;
       if (pos < k.lo || pos >= k.hi) {
         // a row that was not copied, or that no pair sees: zeros, so that 0
         // times it stays 0
@@ -628,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) arrive_mma(&tfull[st]);
     }
   } else {
-    reg_dec<48>();
+    reg_dec<72>();
     if (warp == kLoadWarp) {
       // ===================== bulk copies ==================================
       // In alternation K and V of a chunk. Chunks are looked up 32 / L at a
@@ -674,24 +693,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 2; ++q) {  // K, V
             go = go && wait_all(&rawempty[s], ph);
             if (!go) break;
-            // in a pair K rows are this CTA's half of the chunk
-            const int base = c * kN + (PAIR && q == 0 ? 64 * rank : 0);
-            const int u0 = PAIR && q == 0 ? max(t0, base) : t0;
-            const int u1 = PAIR && q == 0 ? min(t1, base + 64) : t1;
+            // all positions of the chunk, or (K in a pair) this CTA's 32 of
+            // each half
+            const int runs = PAIR && q == 0 ? 2 : 1;
+            int u0[2], u1[2];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int at = c * kN + 64 * w + 32 * rank;
+              u0[w] = runs == 1 ? t0 : max(t0, at);
+              u1[w] = runs == 1 ? t1 : max(min(t1, at + 32), u0[w]);
+            }
             if (lane == j * L)
-              mbar_arrive_expect_tx(&rawfull[s],
-                                    (uint32_t)max(u1 - u0, 0) * kRow);
+              mbar_arrive_expect_tx(
+                  &rawfull[s],
+                  (uint32_t)(u1[0] - u0[0] + (runs == 2 ? u1[1] - u0[1] : 0)) *
+                      kRow);
             __syncwarp();
             if (lane / L == j) {
               for (int m = lq; m < nb; m += L) {
                 const int blk = m < L ? pb : block_of(b0 + m);
                 const int lb = (b0 + m) * bs;
-                const int a0 = max(u0, lb), a1 = min(u1, lb + bs);
-                if (PAIR && a0 >= a1) continue;
-                const long row = ((long)blk * p.n_kv + h) * bs + (a0 - lb);
-                bulk_g2s(raw_slot(s) + (a0 - base) * kRow,
-                         base_kv[q] + row * kRow, (uint32_t)(a1 - a0) * kRow,
-                         &rawfull[s]);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                  if (w >= runs) break;
+                  const int a0 = max(u0[w], lb), a1 = min(u1[w], lb + bs);
+                  if (a0 >= a1) continue;
+                  const long row = ((long)blk * p.n_kv + h) * bs + (a0 - lb);
+                  // row of the raw unit: run w starts at 32 w
+                  const int to = runs == 1
+                                     ? a0 - c * kN
+                                     : a0 - (c * kN + 32 * w + 32 * rank);
+                  bulk_g2s(raw_slot(s) + to * kRow, base_kv[q] + row * kRow,
+                           (uint32_t)(a1 - a0) * kRow, &rawfull[s]);
+                }
               }
             }
             __syncwarp();
@@ -710,14 +744,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::SLOTS; ++i)
           if (last[i] >= 0) mbar_wait(&rawfull[i], last[i]);
       }
-    } else if (warp == kMmaWarp && rank == 0) {
+    } else if ((warp == kMmaWarp || warp == kMmaWarp + 1) && rank == 0) {
       // ===================== MMA issue ====================================
-      constexpr uint32_t idS = umma_idesc_f16(CTAS * kM, kN, false);
+      constexpr uint32_t idS = umma_idesc_f16(CTAS * kM, kS, false);
       constexpr uint32_t idO = umma_idesc_f16(CTAS * kM, kD, true);
       const uint32_t q0 = smem_u32(smem + C::Q_OFF);
       const uint32_t k0 = smem_u32(smem + C::K_OFF);
       const uint32_t v0 = smem_u32(smem + C::V_OFF);
-      auto chunk_of = [&](int s) { return two ? s >> 1 : s; };
       // A step's barriers: first those that are complete by then as a rule,
       // one a lane; last the one that is not (P, or Q), by a suspending wait,
       // which leaves the issue slots to the softmax warps.
@@ -736,62 +769,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return wait_all(b0, p0);
       };
-      // S of step s, whose chunk's K tile is there; it is given back with
-      // the chunk's last step
-      auto issue_s = [&](int s) {
-        const int t = s & 1, st = chunk_of(s) & 1;
+      // One warp a tile: a wait costs 300 cycles and more here even when its
+      // phase is over (the shared memory pipe is busy with the tiles), and
+      // the tiles' waits then overlap. Each tile touches its own tensor
+      // memory only; a K or V tile is free when both have read it.
+      const int t = warp - kMmaWarp;
+      const int nv = steps_of(t);
+      // scores of step v, whose K tile is there
+      auto issue_s = [&](int v) {
+        const int st = chunk_of(t, v) & 1, buf = v & 1;
         const uint64_t a = umma_desc_sw128(q0 + (two ? t * kTile : 0), 16,
                                            1024);
-        const uint64_t bk = umma_desc_sw128(k0 + st * C::KV, 16, 1024);
+        // rows of this half of the chunk: 64, or 32 in each CTA of a pair
+        const uint64_t bk = umma_desc_sw128(
+            k0 + st * C::KV + buf * (kS / CTAS) * 128, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < kD / 16; ++ks) {
           const uint32_t step = (ks & 3) * 32;
           const uint64_t ao = a + (((ks >> 2) * kHalf + step) >> 4);
           const uint64_t bo = bk + (((ks >> 2) * C::KHALF + step) >> 4);
+          const uint32_t d = tbase + kColS + 128 * t + kS * buf;
           if constexpr (PAIR)
-            umma2_ss_elect(tbase + kColS + 128 * t, ao, bo, idS,
-                           ks > 0 ? 1u : 0u);
+            umma2_ss_elect(d, ao, bo, idS, ks > 0 ? 1u : 0u);
           else
-            umma_ss_elect(tbase + kColS + 128 * t, ao, bo, idS,
-                          ks > 0 ? 1u : 0u);
+            umma_ss_elect(d, ao, bo, idS, ks > 0 ? 1u : 0u);
         }
-        commit(&sfull[t]);
-        if (!two || t == 1) commit(&kempty[st]);
+        commit(&sfull[2 * t + buf]);
+        if (buf == 1) commit(&kempty[st]);  // the chunk's last step
       };
-      // the K barrier that step s waits for (its chunk's first step only)
-      auto kbar = [&](int s) -> uint64_t * {
-        return s < nsteps && (!two || (s & 1) == 0) ? &kfull[chunk_of(s) & 1]
-                                                    : nullptr;
+      // the K barrier that step v waits for (a chunk's first step only)
+      auto kbar = [&](int v) -> uint64_t * {
+        return v < nv && (v & 1) == 0 ? &kfull[chunk_of(t, v) & 1] : nullptr;
       };
-      auto kpar = [&](int s) { return (uint32_t)((chunk_of(s) >> 1) & 1); };
-      bool ok = wait3(qfull, 0, kbar(0), 0, kbar(1), kpar(1));
-      if (ok) {
+      auto kpar = [&](int v) {
+        return (uint32_t)((chunk_of(t, v) >> 1) & 1);
+      };
+      // two steps of scores ahead; then per step the product with V and the
+      // scores of the step after next, into the buffer P just left
+      bool ok = wait3(qfull, 0, kbar(0), kpar(0), nullptr, 0);
+      if (ok && nv > 0) {
         tc_fence_after();
         issue_s(0);
-        if (nsteps > 1) issue_s(1);
+        issue_s(1);
       }
-      for (int s = 0; ok && s < nsteps; ++s) {
-        const int t = s & 1, i = chunk_of(s), st = i & 1;
-        // P of this step, V of its chunk, K of the step after next's
-        ok = wait3(&pfull[t], (s >> 1) & 1,
-                   !two || t == 0 ? &vfull[st] : nullptr, (i >> 1) & 1,
-                   kbar(s + 2), kpar(s + 2));
+      for (int v = 0; ok && v < nv; ++v) {
+        const int i = chunk_of(t, v), st = i & 1, buf = v & 1;
+        ok = wait3(&pfull[2 * t + buf], (v >> 1) & 1,
+                   buf == 0 ? &vfull[st] : nullptr, (i >> 1) & 1, kbar(v + 2),
+                   kpar(v + 2));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t bv = umma_desc_sw128(v0 + st * C::KV, kHalf, 1024);
+        const uint64_t bv =
+            umma_desc_sw128(v0 + st * C::KV + buf * kS * 128, kHalf, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kN / 16; ++kk) {
+        for (int kk = 0; kk < kS / 16; ++kk) {
           const uint64_t bo = bv + (uint64_t)((kk * 2048) >> 4);
-          const uint32_t acc = (s > 1 || kk > 0) ? 1u : 0u;
+          const uint32_t acc = (v > 0 || kk > 0) ? 1u : 0u;
+          const uint32_t d = tbase + kColO + 128 * t;
+          const uint32_t pa = tbase + kColS + 128 * t + kS * buf + kk * 8;
           if constexpr (PAIR)
-            umma2_ts_elect(tbase + kColO + 128 * t,
-                           tbase + kColS + 128 * t + kk * 8, bo, idO, acc);
+            umma2_ts_elect(d, pa, bo, idO, acc);
           else
-            umma_ts_elect(tbase + kColO + 128 * t,
-                          tbase + kColS + 128 * t + kk * 8, bo, idO, acc);
+            umma_ts_elect(d, pa, bo, idO, acc);
         }
-        if (!two || t == 1) commit(&vempty[st]);
-        if (s + 2 < nsteps) issue_s(s + 2);
+        commit(&pvdone[t]);
+        if (buf == 1) commit(&vempty[st]);
+        if (v + 2 < nv) issue_s(v + 2);
       }
       if (!ok) give_up();
       // every MMA issued has completed before the epilogue and the dealloc
