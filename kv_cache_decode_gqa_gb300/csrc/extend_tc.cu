@@ -671,21 +671,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            : kN / bs + 2))
         L <<= 1;
       const int lq = lane & (L - 1), batch = 32 / L;
-      const uint8_t *base_kv[2] = {p.k, p.v};
-      int s = 0, ph = 1;
-      int last[C::SLOTS];  // parity of each slot's last copy, or -1
-#pragma unroll
-      for (int i = 0; i < C::SLOTS; ++i) last[i] = -1;
+      int s = 0, ph = 1, units = 0;
       bool go = true;
       for (int cb = c0; go && cb < c1; cb += batch) {
+        // this lane's block: its positions [x0, x1) of its chunk, and where
+        // position 0 would lie in the cache if the block went back that far
         const int c = cb + lane / L;
-        int t0 = 0, t1 = 0, b0 = 0, nb = 0, pb = 0;
+        int t0 = 0, t1 = 0, x0 = 0, x1 = 0;
+        long at = 0;
         if (c < c1) {
           t0 = max(c * kN, k.lo) & ~1;
           t1 = (min((c + 1) * kN, k.hi) + 1) & ~1;
-          b0 = t0 / bs;
-          nb = (t1 - 1) / bs - b0 + 1;
-          if (lq < nb) pb = block_of(b0 + lq);
+          const int lb = t0 / bs + lq;
+          x0 = max(t0, lb * bs);
+          x1 = min(t1, (lb + 1) * bs);
+          if (x0 < x1)
+            at = (((long)block_of(lb) * p.n_kv + h) * bs - (long)lb * bs) *
+                 kRow;
         }
         const int cnt = min(batch, c1 - cb);
         for (int j = 0; go && j < cnt; ++j) {
@@ -693,56 +695,62 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 2; ++q) {  // K, V
             go = go && wait_all(&rawempty[s], ph);
             if (!go) break;
-            // all positions of the chunk, or (K in a pair) this CTA's 32 of
-            // each half
-            const int runs = PAIR && q == 0 ? 2 : 1;
-            int u0[2], u1[2];
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const int at = c * kN + 64 * w + 32 * rank;
-              u0[w] = runs == 1 ? t0 : max(t0, at);
-              u1[w] = runs == 1 ? t1 : max(min(t1, at + 32), u0[w]);
-            }
-            if (lane == j * L)
-              mbar_arrive_expect_tx(
-                  &rawfull[s],
-                  (uint32_t)(u1[0] - u0[0] + (runs == 2 ? u1[1] - u0[1] : 0)) *
-                      kRow);
-            __syncwarp();
             if (lane / L == j) {
-              for (int m = lq; m < nb; m += L) {
-                const int blk = m < L ? pb : block_of(b0 + m);
-                const int lb = (b0 + m) * bs;
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                  if (w >= runs) break;
-                  const int a0 = max(u0[w], lb), a1 = min(u1[w], lb + bs);
-                  if (a0 >= a1) continue;
-                  const long row = ((long)blk * p.n_kv + h) * bs + (a0 - lb);
-                  // row of the raw unit: run w starts at 32 w
-                  const int to = runs == 1
-                                     ? a0 - c * kN
-                                     : a0 - (c * kN + 32 * w + 32 * rank);
-                  bulk_g2s(raw_slot(s) + to * kRow, base_kv[q] + row * kRow,
-                           (uint32_t)(a1 - a0) * kRow, &rawfull[s]);
+              uint8_t *dst = raw_slot(s);
+              const uint8_t *src = q ? p.v : p.k;
+              // (copies may land before the expectation is set: the phase
+              // ends with that arrival at the earliest)
+              uint64_t *bar = &rawfull[s];
+              // positions [u0, u1), of which this lane's block has some, to
+              // rows (position - base) of the raw unit
+              auto copy = [&](int u0, int u1, int base) {
+                for (int m = lq; ; m += L) {
+                  int a0 = max(u0, x0), a1 = min(u1, x1);
+                  long off = at;
+                  if (m > lq) {  // blocks of 2 positions: a lane has several
+                    const int lb = t0 / bs + m;
+                    a0 = max(u0, lb * bs), a1 = min(u1, (lb + 1) * bs);
+                    if (a0 < a1)
+                      off = (((long)block_of(lb) * p.n_kv + h) * bs -
+                             (long)lb * bs) * kRow;
+                  }
+                  if (a0 < a1)
+                    bulk_g2s(dst + (a0 - base) * kRow,
+                             src + off + (long)a0 * kRow,
+                             (uint32_t)(a1 - a0) * kRow, bar);
+                  if (L < 32 || (m + L) * bs + t0 / bs * bs >= t1) break;
                 }
+              };
+              if (PAIR && q == 0) {
+                // this CTA's 32 positions of either half of the chunk
+                const int p0 = c * kN + 32 * rank, p1 = p0 + kS;
+                const int a0 = max(t0, p0), a1 = max(min(t1, p0 + 32), a0);
+                const int b0 = max(t0, p1), b1 = max(min(t1, p1 + 32), b0);
+                if (lq == 0)
+                  mbar_arrive_expect_tx(
+                      bar, (uint32_t)(a1 - a0 + b1 - b0) * kRow);
+                copy(a0, a1, p0);
+                copy(b0, b1, p1 - 32);
+              } else {
+                if (lq == 0)
+                  mbar_arrive_expect_tx(bar, (uint32_t)(t1 - t0) * kRow);
+                copy(t0, t1, c * kN);
               }
             }
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < C::SLOTS; ++i)
-              if (i == s) last[i] = ph ^ 1;
+            ++units;
             if (++s == nraw) s = 0, ph ^= 1;
           }
         }
       }
-      if (!go) give_up();
       if (!go) {
-        // after an abort: every copy that was issued has landed before this
-        // CTA gives its shared memory back
-#pragma unroll
-        for (int i = 0; i < C::SLOTS; ++i)
-          if (last[i] >= 0) mbar_wait(&rawfull[i], last[i]);
+        give_up();
+        // every copy that was issued has landed before this CTA gives its
+        // shared memory back
+        for (int i = 0; i < nraw && i < units; ++i) {
+          const int u = units - 1 - i;
+          mbar_wait(&rawfull[u % nraw], (u / nraw) & 1);
+        }
       }
     } else if ((warp == kMmaWarp || warp == kMmaWarp + 1) && rank == 0) {
       // ===================== MMA issue ====================================
