@@ -61,6 +61,9 @@ struct FCfg {
   static constexpr int PAIRS = 8 * RT;      // pair slots of a kv head
   static constexpr int GU = HP * PAIRS;     // pair slots of a unit
   static constexpr int STAGE = HP * CH * kRow;  // K (or V) of a chunk
+  // With 16 warps a thread has 96 registers: one chain of score products and
+  // V's loads behind them then win over two chains and early loads.
+  static constexpr bool LEAN = W == 16;
   // flush slot: 8 * SR pairs of every warp's state at a time
   static constexpr int SR = W * RT > 16 ? 16 / W : RT;
   static constexpr int SLOT = W * 8 * SR * (kD + 2);  // floats
@@ -68,7 +71,8 @@ struct FCfg {
                                                    // [head][k][tile][lane]
   static constexpr int FIXED =
       SLOT * 4 + QF + (int)sizeof(WorkPartition) + 64 + 2 * 16 * 8;
-  static constexpr int NS_FIT = (226 * 1024 - FIXED) / (2 * STAGE);
+  // (223 KB: a merge CTA fits beside this one)
+  static constexpr int NS_FIT = (223 * 1024 - FIXED) / (2 * STAGE);
   static constexpr int NS = NS_FIT > W ? W : NS_FIT;
   static constexpr int SLOT_OFF = 2 * NS * STAGE;
   static constexpr int QF_OFF = SLOT_OFF + SLOT * 4;
@@ -76,7 +80,7 @@ struct FCfg {
   static constexpr int BAR_OFF =
       (WP_OFF + (int)sizeof(WorkPartition) + 15) / 16 * 16;
   static constexpr int SMEM = BAR_OFF + 2 * NS * 8;
-  static_assert(TPW % 16 == 0 && NS >= 2 && SMEM <= 226 * 1024, "shape");
+  static_assert(TPW % 16 == 0 && NS >= 2 && SMEM <= 223 * 1024, "shape");
 };
 
 // An 8 x 8 matrix of 16-bit elements, a row a quad of lanes, transposed.
@@ -432,26 +436,30 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
         const int pos0 = ctok + wt0 + 16 * u;  // the tile's first position
         const uint8_t *kr = kl + u * 16 * kRow;
         const uint8_t *vr = vl + u * 16 * kRow;
-        // V's codes and scales, on their way during the scores
+        // V's codes and scales: on their way during the scores, or (LEAN)
+        // behind them
         uint2 v0[2], v1[2];  // tokens 2 qc + 8 t and the next
         uint32_t vs[2];
         const bool outside = pos0 < ulo || pos0 + 16 > T;
+        auto load_v = [&]() {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint8_t *row = vr + 8 * t * kRow;
-          v0[t] = *reinterpret_cast<const uint2 *>(row);
-          v1[t] = *reinterpret_cast<const uint2 *>(row + kRow);
-          uint32_t a = row[64 - 7 * qr], z = row[kRow + 64 - 7 * qr];
-          if (outside) {
-            // rows outside the unit's positions were not copied: their
-            // scales are taken as 0, so that 0 times them stays 0
-            const int pos = pos0 + 8 * t + 2 * qc;
-            if (pos < ulo || pos >= T) a = 0;
-            if (pos + 1 < ulo || pos + 1 >= T) z = 0;
+          for (int t = 0; t < 2; ++t) {
+            const uint8_t *row = vr + 8 * t * kRow;
+            v0[t] = *reinterpret_cast<const uint2 *>(row);
+            v1[t] = *reinterpret_cast<const uint2 *>(row + kRow);
+            uint32_t a = row[64 - 7 * qr], z = row[kRow + 64 - 7 * qr];
+            if (outside) {
+              // rows outside the unit's positions were not copied: their
+              // scales are taken as 0, so that 0 times them stays 0
+              const int pos = pos0 + 8 * t + 2 * qc;
+              if (pos < ulo || pos >= T) a = 0;
+              if (pos + 1 < ulo || pos + 1 >= T) z = 0;
+            }
+            vs[t] = a | (z << 8);
           }
-          vs[t] = a | (z << 8);
-        }
-        // ---- S^T = K Q^T of 16 tokens (two chains of products) ----
+        };
+        if constexpr (!C::LEAN) load_v();
+        // ---- S^T = K Q^T of 16 tokens (two chains of products, or one) ----
         float sc[RT][4], sd[RT][4];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -485,15 +493,17 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
 #pragma unroll
               for (int r = 0; r < RT; ++r) {
                 const uint2 f = qf[((2 * k4 + h2) * RT + r) * 32 + lane];
-                mma_f16(h2 ? sd[r] : sc[r], a, f.x, f.y);
+                mma_f16(h2 && !C::LEAN ? sd[r] : sc[r], a, f.x, f.y);
               }
             }
           }
         }
+        if constexpr (!C::LEAN) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+          for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) sc[r][q] += sd[r][q];
+            for (int q = 0; q < 4; ++q) sc[r][q] += sd[r][q];
+        }
         // ---- exponentials (q: pair q % 2, token qr + 8 (q / 2)) ----
         bool grow = false;
         if (pos0 < all_lo || pos0 + 16 > all_hi) {
@@ -553,6 +563,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
           pb[r][1] = transpose_8x8(pack_f16x2(e2, e3));
         }
         // ---- O^T += V^T P^T ----
+        if constexpr (C::LEAN) load_v();
         uint32_t e[2][2], d[2][2];  // [token pair][word]: even, odd dims
         uint32_t sp[2];
 #pragma unroll
@@ -604,12 +615,18 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
 }
 
 // Log-sum-exp merge of the units that several CTAs of the launch before
-// share (as merge_dense_kernel, with a unit's rows spread over sequences'
-// rows): four lanes per float4 of outputs, two rows a CTA.
-constexpr int kRowMergeThreads = 256;
+// share, up to 8 parts' loads of a float4 in flight a lane: one warp a pair,
+// or (LANES = 4, units of many parts) four lanes a float4 and a CTA a pair.
+// A CTA is small enough to sit beside one of
+// that launch (128 threads, 64 registers, 1 KB for batches up to 64), so
+// that the partition is rebuilt while it still runs, and takes every
+// gridDim.x-th group of pairs. (256 threads and a CTA per two pairs
+// started only when the other launch had left the SMs: 10 us in all for 32
+// sequences of 8 kv heads.)
+constexpr int kRowMergeThreads = 128;
 
-template <int NB>
-__global__ void __launch_bounds__(kRowMergeThreads)
+template <int NB, int LANES>
+__global__ void __launch_bounds__(kRowMergeThreads, 8)
     merge_few_kernel(const __grid_constant__ ExtendParams p, int n_units,
                      int hp, int chunk, int slots) {
   __shared__ WorkPartitionT<NB> wp;
@@ -624,36 +641,42 @@ __global__ void __launch_bounds__(kRowMergeThreads)
   if (total == 0) return;
   const int P = min(p.n_splits, total);
   const int G = p.n_h / p.n_kv;
-  const int u = blockIdx.x;
-  const int b = u / n_units, h = u - b * n_units;
-  if (wp.nch[b] == 0) return;
-  const int ustart = wp.pre[b] + h * wp.nch[b];
-  const int c_first = cta_of(ustart, total, P);
-  const int parts = cta_of(ustart + wp.nch[b] - 1, total, P) - c_first + 1;
-  if (parts == 1) return;
-  const int rows = seq_rows(p, b) * G;
   const int gu = hp * slots;  // pair slots of a unit
-  const long row0 = p.row_start ? p.row_start[b] : b;
-  auto slot = [&](int i) { return (long)(c_first + i) * 2 + (i == 0 ? 1 : 0); };
-  const int x = threadIdx.x & 127;  // 32 float4 x 4 lanes
-  for (int jg = blockIdx.y * 2 + (threadIdx.x >> 7); jg < hp * rows;
-       jg += gridDim.y * 2) {
-    const int j = jg / rows, g = jg - j * rows;
-    const int sl = j * slots + g, e4 = x >> 2;
+  const int per_head = min(slots, p.max_rows * G);
+  const int per_unit = hp * per_head;
+  constexpr int PAIR_THREADS = 32 * LANES, PAIRS = kRowMergeThreads /
+                                                  PAIR_THREADS;
+  const int x = threadIdx.x % PAIR_THREADS, e4 = x / LANES;
+  const int step = gridDim.x * PAIRS;
+  const int items = p.batch * n_units * per_unit;
+  for (int it = blockIdx.x * PAIRS + threadIdx.x / PAIR_THREADS; it < items;
+       it += step) {
+    const int u = it / per_unit, jg = it - u * per_unit;
+    const int j = jg / per_head, g = jg - j * per_head;
+    const int b = u / n_units, h = u - b * n_units;
+    if (wp.nch[b] == 0 || g >= seq_rows(p, b) * G) continue;
+    const int ustart = wp.pre[b] + h * wp.nch[b];
+    const int c_first = cta_of(ustart, total, P);
+    const int parts = cta_of(ustart + wp.nch[b] - 1, total, P) - c_first + 1;
+    if (parts == 1) continue;
+    const long row0 = p.row_start ? p.row_start[b] : b;
+    const int sl = j * slots + g;
     float M, W;
     float4 acc;
-    quad_merge<4>(p.ws_lse, p.ws_o, gu, kD, sl, sl * (kD / 4) + e4, parts,
-                  slot, M, W, acc);
-    if ((x & 3) == 0) {
-      const float iw = W == 0.f ? 0.f : 1.f / W;
-      const long at = (row0 + g / G) * p.n_h + (long)(h * hp + j) * G + g % G;
-      uint2 packed;
-      packed.x = pack_bf16x2(acc.x * iw, acc.y * iw);
-      packed.y = pack_bf16x2(acc.z * iw, acc.w * iw);
-      reinterpret_cast<uint2 *>(p.out + at * kD)[e4] = packed;
-      if (e4 == 0 && p.lse)
-        p.lse[at] = W == 0.f ? -INFINITY : M + logf(W);
-    }
+    quad_merge<LANES>(p.ws_lse, p.ws_o, gu, kD, sl, sl * (kD / 4) + e4, parts,
+                      [&](int i) {
+                        return (long)(c_first + i) * 2 + (i == 0 ? 1 : 0);
+                      },
+                      M, W, acc);
+    if (x % LANES != 0) continue;
+    const float iw = W == 0.f ? 0.f : 1.f / W;
+    const long at = (row0 + g / G) * p.n_h + (long)(h * hp + j) * G + g % G;
+    uint2 packed;
+    packed.x = pack_bf16x2(acc.x * iw, acc.y * iw);
+    packed.y = pack_bf16x2(acc.z * iw, acc.w * iw);
+    reinterpret_cast<uint2 *>(p.out + at * kD)[e4] = packed;
+    if (e4 == 0 && p.lse)
+      p.lse[at] = W == 0.f ? -INFINITY : M + logf(W);
   }
 }
 
@@ -667,15 +690,19 @@ cudaError_t launch_few_t(const ExtendParams &p, cudaStream_t s) {
   e = launch_pdl(kern, dim3(p.n_splits), dim3(C::THREADS), C::SMEM, s, 1, p);
   if (e != cudaSuccess || p.whole_units || p.n_splits <= 1) return e;
   const int n_units = p.n_kv / HP;
-  const int pairs = HP * std::min(C::PAIRS, p.max_rows * (p.n_h / p.n_kv));
-  const dim3 grid(p.batch * n_units, (pairs + 1) / 2);
-  if (p.batch <= kMergeSmallBatch)
-    return launch_pdl(merge_few_kernel<kMergeSmallBatch>, grid,
-                      dim3(kRowMergeThreads), 0, s, 1, p, n_units, HP, CH,
-                      C::PAIRS);
-  return launch_pdl(merge_few_kernel<kMaxDecodeBatch>, grid,
-                    dim3(kRowMergeThreads), 0, s, 1, p, n_units, HP, CH,
-                    C::PAIRS);
+  const long pairs = (long)p.batch * n_units * HP *
+                     std::min(C::PAIRS, p.max_rows * (p.n_h / p.n_kv));
+  // parts of a unit of average length
+  const bool many = p.n_splits > 6L * p.batch * n_units;
+  const long per = many ? 1 : kRowMergeThreads / 32;
+  const dim3 grid((unsigned)std::min((pairs + per - 1) / per, 304L));
+  auto merge = p.batch <= kMergeSmallBatch
+                   ? (many ? merge_few_kernel<kMergeSmallBatch, 4>
+                           : merge_few_kernel<kMergeSmallBatch, 1>)
+                   : (many ? merge_few_kernel<kMaxDecodeBatch, 4>
+                           : merge_few_kernel<kMaxDecodeBatch, 1>);
+  return launch_pdl(merge, grid, dim3(kRowMergeThreads), 0, s, 1, p, n_units,
+                    HP, CH, C::PAIRS);
 }
 
 template <int HP, int CH, int W1, int W2>
