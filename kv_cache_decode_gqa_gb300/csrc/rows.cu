@@ -30,13 +30,14 @@ constexpr int kThreads = 256;
 // One 16-channel group of bf16 values (8 words) as E2M1 codes and an E4M3
 // scale, the same bytes as store_mxfp4_group. There each code is E2M1(q),
 // q = x / s correctly rounded, i.e. decided by comparing q with the
-// midpoints m of the grid. Here q comes as x * (1 / s), which may miss a tie
-// x = m s by an ulp. x has 8 significand bits and m s at most 7, so x / s is
-// either m or at least m / 256 away from it (>= 2^-10, as m >= 1/4); adding
-// and subtracting 1.5 * 2^12 rounds q to a multiple of 2^-11, which restores
-// every tie (the midpoints are multiples of 1/4) and moves no other value
-// past a midpoint. The hardware conversion then rounds ties to even and
-// saturates as e2m1_code does. Groups that hold a NaN take the plain path.
+// midpoints m of the grid. Here fma(x, 1 / s, M) - M, M = 1.5 * 2^12, gives q
+// rounded to a multiple of 2^-11. x has 8 significand bits and m s at most 7,
+// so x / s is either m or at least m / 256 >= 2^-10 away from it: a tie comes
+// out as m (a multiple of 1/4) although 1 / s is rounded, and no other value
+// passes a midpoint. Values of 8 and more, where M no longer rounds like
+// that, and infinities saturate either way. The hardware conversion then
+// rounds ties to even and saturates as e2m1_code does. Groups that hold a NaN
+// take the plain path.
 __device__ __forceinline__ void mxfp4_group(uint8_t *codes, uint8_t *scale,
                                             const uint16_t *src) {
   const uint4 u0 = *reinterpret_cast<const uint4 *>(src);
@@ -61,11 +62,9 @@ __device__ __forceinline__ void mxfp4_group(uint8_t *codes, uint8_t *scale,
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x0 = bf16lo(w[j]), x1 = bf16hi(w[j]);
-      float q0 = fminf(fmaxf(x0 * r, -8.f), 8.f);
-      float q1 = fminf(fmaxf(x1 * r, -8.f), 8.f);
       // the sign of a value that rounds to 0 is kept (as e2m1_code keeps it)
-      q0 = copysignf(__fsub_rn(__fadd_rn(q0, kMagic), kMagic), x0);
-      q1 = copysignf(__fsub_rn(__fadd_rn(q1, kMagic), kMagic), x1);
+      const float q0 = copysignf(fmaf(x0, r, kMagic) - kMagic, x0);
+      const float q1 = copysignf(fmaf(x1, r, kMagic) - kMagic, x1);
       uint32_t b;
       asm("{\n\t.reg .b8 t;\n\t"
           "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
@@ -88,6 +87,18 @@ __device__ __forceinline__ float2 turn(uint64_t turns, int pos, bool inverse) {
   float s, c;
   sincospif(h, &s, &c);
   return make_float2(c, inverse ? -s : s);
+}
+
+// Eight E2M1 codes times their group's scale as bf16, exactly (6 significand
+// bits), through fp32. (Packed bf16 multiplications of the shifted f16 codes
+// take fewer instructions and ran 10% slower.)
+__device__ __forceinline__ void mxfp4_to_bf16(uint32_t codes, float scale,
+                                              uint32_t (&o)[4]) {
+  uint32_t h[4];
+  e2m1x8_to_f16(codes, h);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = pack_bf16x2(f16lo(h[j]) * scale, f16hi(h[j]) * scale);
 }
 
 // The sequence of ragged row r, or -1 for padding.
@@ -143,72 +154,86 @@ __device__ __forceinline__ uint32_t rot_hi(uint32_t a, uint32_t b, float2 c0,
                      fmaf(bf16hi(b), c1.x, bf16hi(a) * c1.y));
 }
 
-// Piece c of the rotation of one row-head from src to dst (which may be the
-// same), with the row's cosines and sines cs. VEC: 8 pairs (half) or 4
-// (adjacent) a piece and 16-byte accesses, then pieces of 8 channels that
-// stay; else one pair, then one channel a piece.
-template <bool VEC>
-__device__ __forceinline__ void rotate_piece(const RopeParams &rp, int d,
-                                             const uint16_t *src,
-                                             uint16_t *dst, const float2 *cs,
-                                             int c) {
-  const int half = rp.half;
-  if constexpr (VEC) {
-    const int nrot = rp.adjacent ? half / 4 : half / 8;
-    if (c >= nrot) {  // channels past d_rot
-      const int at = 2 * half + (c - nrot) * 8;
-      *reinterpret_cast<uint4 *>(dst + at) =
-          *reinterpret_cast<const uint4 *>(src + at);
-    } else if (rp.adjacent) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(src + c * 8);
-      uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 t = cs[c * 4 + j];
-        const float a = bf16lo(w[j]), b = bf16hi(w[j]);
-        w[j] = pack_bf16x2(fmaf(a, t.x, -(b * t.y)), fmaf(b, t.x, a * t.y));
-      }
-      *reinterpret_cast<uint4 *>(dst + c * 8) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      const uint4 x = *reinterpret_cast<const uint4 *>(src + c * 8);
-      const uint4 y = *reinterpret_cast<const uint4 *>(src + half + c * 8);
-      const uint32_t a[4] = {x.x, x.y, x.z, x.w};
-      const uint32_t b[4] = {y.x, y.y, y.z, y.w};
-      uint32_t lo[4], hi[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 t =
-            *reinterpret_cast<const float4 *>(cs + c * 8 + 2 * j);
-        const float2 t0 = make_float2(t.x, t.y), t1 = make_float2(t.z, t.w);
-        lo[j] = rot_lo(a[j], b[j], t0, t1);
-        hi[j] = rot_hi(a[j], b[j], t0, t1);
-      }
-      *reinterpret_cast<uint4 *>(dst + c * 8) =
-          make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      *reinterpret_cast<uint4 *>(dst + half + c * 8) =
-          make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    }
+// One piece of the rotation of a row-head: 16-byte pieces of 8 pairs (half)
+// or 4 (adjacent), then of 8 channels that stay. Loading and finishing are
+// apart so that the next piece's loads are in flight meanwhile.
+struct RotPiece {
+  uint16_t *dst;
+  const float2 *cs;
+  uint4 x, y;
+  int c;
+};
+
+__device__ __forceinline__ void load_piece(const RopeParams &rp, int nrot,
+                                           const uint16_t *src, RotPiece &q) {
+  const int c = q.c;
+  if (c >= nrot) {  // channels past d_rot
+    q.x = *reinterpret_cast<const uint4 *>(src + 2 * rp.half + (c - nrot) * 8);
   } else {
-    if (c >= half) {
-      const int at = half + c;  // 2 * half + (c - half)
-      dst[at] = src[at];
-      return;
-    }
-    const int i = rp.adjacent ? 2 * c : c, j = rp.adjacent ? 2 * c + 1
-                                                           : c + half;
-    const float a = __uint_as_float((uint32_t)src[i] << 16);
-    const float b = __uint_as_float((uint32_t)src[j] << 16);
-    const float2 t = cs[c];
-    dst[i] = f2bf(fmaf(a, t.x, -(b * t.y)));
-    dst[j] = f2bf(fmaf(b, t.x, a * t.y));
+    q.x = *reinterpret_cast<const uint4 *>(src + c * 8);
+    if (!rp.adjacent)
+      q.y = *reinterpret_cast<const uint4 *>(src + rp.half + c * 8);
   }
+}
+
+__device__ __forceinline__ void finish_piece(const RopeParams &rp, int nrot,
+                                             const RotPiece &q) {
+  const int half = rp.half, c = q.c;
+  uint16_t *dst = q.dst;
+  const float2 *cs = q.cs;
+  if (c >= nrot) {
+    *reinterpret_cast<uint4 *>(dst + 2 * half + (c - nrot) * 8) = q.x;
+  } else if (rp.adjacent) {
+    uint32_t w[4] = {q.x.x, q.x.y, q.x.z, q.x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 t = cs[c * 4 + j];
+      const float a = bf16lo(w[j]), b = bf16hi(w[j]);
+      w[j] = pack_bf16x2(fmaf(a, t.x, -(b * t.y)), fmaf(b, t.x, a * t.y));
+    }
+    *reinterpret_cast<uint4 *>(dst + c * 8) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    const uint32_t a[4] = {q.x.x, q.x.y, q.x.z, q.x.w};
+    const uint32_t b[4] = {q.y.x, q.y.y, q.y.z, q.y.w};
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 t = *reinterpret_cast<const float4 *>(cs + c * 8 + 2 * j);
+      const float2 t0 = make_float2(t.x, t.y), t1 = make_float2(t.z, t.w);
+      lo[j] = rot_lo(a[j], b[j], t0, t1);
+      hi[j] = rot_hi(a[j], b[j], t0, t1);
+    }
+    *reinterpret_cast<uint4 *>(dst + c * 8) =
+        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4 *>(dst + half + c * 8) =
+        make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  }
+}
+
+// The same element by element, where no 16-byte access fits: pair c, or
+// channel half + c past d_rot.
+__device__ __forceinline__ void rotate_pair(const RopeParams &rp,
+                                            const uint16_t *src, uint16_t *dst,
+                                            const float2 *cs, int c) {
+  if (c >= rp.half) {
+    const int at = rp.half + c;  // 2 * half + (c - half)
+    dst[at] = src[at];
+    return;
+  }
+  const int i = rp.adjacent ? 2 * c : c;
+  const int j = rp.adjacent ? 2 * c + 1 : c + rp.half;
+  const float a = __uint_as_float((uint32_t)src[i] << 16);
+  const float b = __uint_as_float((uint32_t)src[j] << 16);
+  const float2 t = cs[c];
+  dst[i] = f2bf(fmaf(a, t.x, -(b * t.y)));
+  dst[j] = f2bf(fmaf(b, t.x, a * t.y));
 }
 
 // WRITE: the cache write (dtype DT), else the rotation alone. A CTA takes
 // rows [tile * blockIdx.x, + tile) and the blockIdx.y-th share of the heads.
 template <bool VEC, bool WRITE, int DT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
     rows_kernel(const __grid_constant__ RowsParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ long s_slot[kMaxRowTile];
@@ -250,26 +275,53 @@ __global__ void __launch_bounds__(kThreads)
     const int heads = nq + nk;
     const int step = kThreads / L;
     int r = 0, h = tid / L;
-    while (heads > 0) {
-      while (h >= heads) h -= heads, ++r;
-      if (r >= nr) break;
-      const long row = r0 + r;
-      const bool is_q = h < nq;
-      if (!WRITE || s_slot[r] != kPadding) {
-        const uint16_t *src =
-            is_q ? p.q + row * p.q_rs + (qh0 + h) * p.q_hs
-                 : p.k + row * p.k_rs + (kh0 + h - nq) * p.k_hs;
-        uint16_t *dst =
-            is_q ? p.q_out + row * p.qo_rs + (qh0 + h) * p.qo_hs
-            : WRITE
-                ? sk + ((long)r * nk + h - nq) * d
-                : p.k_out + row * p.ko_rs + (kh0 + h - nq) * p.ko_hs;
-        // in place the channels past d_rot are already there
+    // the next row-head of this thread that has a row: source, destination
+    auto next = [&](const uint16_t *&src, uint16_t *&dst) {
+      for (; heads > 0; h += step) {
+        while (h >= heads) h -= heads, ++r;
+        if (r >= nr) return false;
+        if (WRITE && s_slot[r] == kPadding) continue;
+        const long row = r0 + r;
+        const bool is_q = h < nq;
+        src = is_q ? p.q + row * p.q_rs + (qh0 + h) * p.q_hs
+                   : p.k + row * p.k_rs + (kh0 + h - nq) * p.k_hs;
+        dst = is_q    ? p.q_out + row * p.qo_rs + (qh0 + h) * p.qo_hs
+              : WRITE ? sk + ((long)r * nk + h - nq) * d
+                      : p.k_out + row * p.ko_rs + (kh0 + h - nq) * p.ko_hs;
+        return true;
+      }
+      return false;
+    };
+    const uint16_t *src;
+    if constexpr (VEC) {
+      // one piece a row-head and thread (at most 256 pieces)
+      RotPiece cur, nxt;
+      cur.c = nxt.c = tid & (L - 1);
+      auto fetch = [&](RotPiece &q) {
+        while (next(src, q.dst)) {
+          q.cs = cs + r * rp.half;
+          h += step;
+          // in place the channels past d_rot are already there
+          if (q.c < (src == q.dst ? nrot : pieces)) {
+            load_piece(rp, nrot, src, q);
+            return true;
+          }
+        }
+        return false;
+      };
+      bool more = fetch(cur);
+      while (more) {
+        more = fetch(nxt);
+        finish_piece(rp, nrot, cur);
+        cur = nxt;
+      }
+    } else {
+      uint16_t *dst;
+      for (; next(src, dst); h += step) {
         const int end = src == dst ? nrot : pieces;
         for (int c = tid & (L - 1); c < end; c += L)
-          rotate_piece<VEC>(rp, d, src, dst, cs + r * rp.half, c);
+          rotate_pair(rp, src, dst, cs + r * rp.half, c);
       }
-      h += step;
     }
   }
   if constexpr (WRITE) {
@@ -371,19 +423,12 @@ __global__ void __launch_bounds__(kThreads)
           const uint2 u = *reinterpret_cast<const uint2 *>(src + c * 8);
           const uint32_t g = src[p.d / 2 + c];
           const float s = f16lo(e4m3x2_to_f16x2((uint16_t)g));
-          const uint32_t w[2] = {u.x, u.y};
-          uint32_t o[8];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t v[4];
-            e2m1x8_to_f16(w[q], v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              o[4 * q + j] = pack_bf16x2(f16lo(v[j]) * s, f16hi(v[j]) * s);
-          }
+          uint32_t o[2][4];
+          mxfp4_to_bf16(u.x, s, o[0]);
+          mxfp4_to_bf16(u.y, s, o[1]);
           uint4 *q = reinterpret_cast<uint4 *>(dst + c * 16);
-          q[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          q[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          q[0] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+          q[1] = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
         }
       }
     }
@@ -461,7 +506,7 @@ cudaError_t launch_rows(const RowsParams &in, bool write, int sms,
     return cudaErrorNotSupported;
   bool vec = true;
   if (p.rope.on) {
-    vec = p.d % 8 == 0 &&
+    vec = p.d % 8 == 0 && p.d <= 2048 &&
           (p.rope.adjacent ? p.rope.half % 4 == 0 : p.rope.half % 8 == 0);
     if (p.n_h)
       vec = vec && vec_ok(p.q, p.q_rs, p.q_hs) &&
