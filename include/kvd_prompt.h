@@ -159,8 +159,8 @@ kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
  *   workspace at least kvd_extend_workspace_size() bytes, 256-byte aligned
  *             (NULL when that is 0); see "Workspace" in kvd.h
  * Rows from row_start[batch] on are left as they were. A sequence whose
- * row_start entries descend, pass q->rows or are more than max_rows apart
- * is skipped and flagged KVD_DEVERR_LEN. Scores and sums in fp32; the
+ * row_start entries descend (or follow a descent), pass q->rows or are more
+ * than max_rows apart is skipped and flagged KVD_DEVERR_LEN. Scores and sums in fp32; the
  * queries enter the first product as f16 with a power-of-two scale per
  * (row, head), the probabilities enter the second as f16.
  * Supported: an MXFP4 cache (head_dim 128), n_h / n_kv of 1 .. 128, at most

@@ -571,7 +571,8 @@ def kv_write(cache, block_table, start, row_start, k_new, v_new=None,
     into the cache: rows row_start[b] .. row_start[b + 1] - 1 go to positions
     start[b] .. of sequence b. With ``rope`` (a RopePlan) and ``positions``
     the keys are rotated on the way, and so is q [rows][n_h][head_dim] if
-    given: returns q_out (None without q; q_out=q rotates in place)."""
+    given: returns q_out (None without q; q_out=q rotates in place). Rows of
+    a new q_out that no sequence owns are not initialised."""
     c = cache.struct()
     B = _ragged(cache, block_table, start, row_start)
     ks = _rows3(k_new, "k_new", cache.n_kv, cache.head_dim)
@@ -664,7 +665,8 @@ def gqa_extend(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
     row_start[b + 1] - 1 (int32 [batch + 1]) are the last positions of
     sequence b, at most ``max_rows`` of them; without row_start row b is
     sequence b's one new token. Each row attends to the positions up to its
-    own, within ``window`` and from ``window_start`` if given."""
+    own, within ``window`` and from ``window_start`` if given. Rows of new
+    outputs that no sequence owns are not initialised."""
     import torch
     d = cache.head_dim
     qs = _rows3(q, "q", width=d)

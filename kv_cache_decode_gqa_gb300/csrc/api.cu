@@ -3,6 +3,7 @@
 // device memory or synchronises, except kvd_device_error().
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1088,10 +1089,13 @@ struct ExtendPlan {
   size_t ws_o_bytes = 0, ws_bytes = 0;
 };
 
-// Few (row, head) pairs a kv head: the stream-K kernel with one CTA per SM.
-// Else row blocks of 256 pairs: enough of them fill the SMs by themselves
-// (two waves and more); fewer are split over the positions into about four
-// waves of equal shares, so that ragged lengths level out.
+// Few (row, head) pairs a kv head (at most 16): the stream-K kernel with one
+// CTA per SM. Else blocks of 256 pairs a CTA, or of 512 a pair of CTAs where
+// a sequence may have more than 256 (one prompt chunk of 1,021 tokens over
+// 32,000, 56 heads: 802 us with pairs, 856 us without). Enough blocks fill
+// the SMs by themselves (two waves and more); fewer are split over the
+// positions into about four waves of equal shares, so that ragged lengths
+// level out.
 ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
                        int max_rows, int n_h, int sms) {
   ExtendPlan pl;
@@ -1137,7 +1141,9 @@ ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
   const long ctas = (long)pl.blocks * c->n_kv * ctas_per_block;
   const long want = forced > 0 ? forced : 4L * sms;
   if (forced > 0 || ctas < 2L * sms) {
-    const long per = std::max(4L, (ctas * chunks + want - 1) / want);
+    // (a launch has at most 65,535 splits)
+    const long per = std::max({4L, (ctas * chunks + want - 1) / want,
+                               (chunks + 65534) / 65535});
     if (per < chunks) {
       pl.p.chunks_per_split = (int)per;
       pl.splits = (int)((chunks + per - 1) / per);

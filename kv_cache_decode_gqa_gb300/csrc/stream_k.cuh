@@ -52,8 +52,9 @@ __device__ __forceinline__ int seq_first(const DecodeParams &p, int b, int T,
 __device__ __forceinline__ int seq_rows(const ExtendParams &p, int b) {
   if (!p.row_start) return 1;
   const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
-  return r0 < 0 || r1 < r0 || r1 > p.rows || r1 - r0 > p.max_rows ? 0
-                                                                  : r1 - r0;
+  if (r0 < 0 || r1 < r0 || r1 > p.rows || r1 - r0 > p.max_rows) return 0;
+  // after a descent the rows may be another sequence's
+  return b > 0 && p.row_start[b - 1] > r0 ? 0 : r1 - r0;
 }
 __device__ __forceinline__ int seq_lo(const ExtendParams &p, int b, int T) {
   const int n = seq_rows(p, b);

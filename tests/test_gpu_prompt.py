@@ -484,3 +484,333 @@ def test_extend(case):
     _check(out, lse, _attend_ref(c, bt, lens, counts, q, window))
     assert bool((out[rows:] == 9).all()) and bool((lse[rows:] == 9).all())
     assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("counts,lens,window,starts", [
+    ([1, 1, 1], [200, 90, 10], 0, [50, 89, 40]),       # the last sees nothing
+    ([4, 4], [300, 64], 20, [290, 62]),
+    ([60, 3], [900, 70], 0, [500, 69]),
+    ([90, 80], [700, 600], 128, [640, 599]),
+])
+def test_extend_from_replay_starts(counts, lens, window, starts):
+    g = _gen(7)
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 2, 64, "mxfp4")
+    q = _randn(g, sum(counts), 16, D)
+    out, lse = K.gqa_extend(c, bt, _i32(lens), max(lens), q, _starts(counts),
+                            max(counts), window=window,
+                            window_start=_i32(starts))
+    _check(out, lse, _attend_ref(c, bt, lens, counts, q, window, starts))
+    assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("counts", [[1, 2], [20, 10], [70, 40]])
+def test_extend_strided_queries_scales_and_no_lse(counts):
+    """Queries inside a fused projection, a scale of the caller's, and
+    queries of very different magnitudes: 2^-100 and 2^100 side by side."""
+    g = _gen(31)
+    lens = [n + 130 for n in counts]
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 2, 64, "mxfp4")
+    qkv = _randn(g, sum(counts), 12, D)
+    q = qkv[:, 2:10]
+    big = torch.tensor([2.0 ** -100, 2.0 ** -130, 1, 2.0 ** -8] * 2,
+                       device="cuda")
+    q.copy_((q.float() * big[:, None]).to(BF))
+    args = (c, bt, _i32(lens), max(lens), q, _starts(counts), max(counts))
+    out, lse = K.gqa_extend(*args, scale=0.25)
+    _check(out, lse, _attend_ref(c, bt, lens, counts, q, scale=0.25))
+    out2, none = K.gqa_extend(*args, scale=0.25, want_lse=False)
+    assert none is None and torch.equal(out, out2)
+
+
+@pytest.mark.parametrize("counts,n_h", [([3], 8), ([30], 8), ([120], 8)])
+def test_extend_nan_and_infinite_queries_stay_in_their_rows(counts, n_h):
+    g = _gen(41)
+    lens = [counts[0] + 300]
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 2, 64, "mxfp4")
+    q = _randn(g, counts[0], n_h, D)
+    args = (c, bt, _i32(lens), lens[0])
+    want, wl = K.gqa_extend(*args, q, _starts(counts), counts[0])
+    q[1, 2, 5] = float("nan")
+    q[2, 0, 0] = float("inf")
+    out, lse = K.gqa_extend(*args, q, _starts(counts), counts[0])
+    bad = torch.zeros((counts[0], n_h), dtype=torch.bool, device="cuda")
+    bad[1, 2] = bad[2, 0] = True
+    assert torch.equal(out[~bad], want[~bad])
+    assert torch.equal(lse[~bad], wl[~bad])
+    assert bool(torch.isnan(out[1, 2]).all()) and bool(torch.isnan(lse[1, 2]))
+
+
+@pytest.mark.parametrize("max_rows", [1, 4, 40])
+def test_extend_flags_bad_lists_lengths_and_blocks(max_rows):
+    g = _gen(51)
+    lens = [200, 120, 300]
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 1, 64, "mxfp4")
+    n = max_rows
+    q = _randn(g, 3 * n, 8, D)
+    good = [0, n, 2 * n, 3 * n]
+
+    def run(rs=good, lens=lens, table=bt, top=300):
+        out = torch.full((3 * n, 8, D), 9.0, dtype=BF, device="cuda")
+        K.gqa_extend(c, table, _i32(lens), top, q, _i32(rs), n, out=out)
+        return out
+    want = run()
+    assert K.device_error() == 0
+    # a list that descends, passes the rows or jumps too far: that sequence
+    # is skipped, the others are right
+    for bad in ([0, n, 0, n], [0, n, 2 * n, 3 * n + 1], [0, n, n, 3 * n + 9]):
+        out = run(bad)
+        assert K.device_error() == K.DEVERR_LEN
+        assert torch.equal(out[:n], want[:n])
+    # a length above the bound is clamped to it
+    out = run(lens=[200, 500, 300])
+    assert K.device_error() == K.DEVERR_LEN
+    assert torch.equal(out[:n], want[:n])
+    bad = bt.clone()
+    bad[1, 0] = blocks + 5
+    out = run(table=bad)
+    assert K.device_error() == K.DEVERR_BLOCK
+    assert torch.equal(out[:n], want[:n]) and torch.equal(out[2 * n:],
+                                                          want[2 * n:])
+
+
+def test_extend_single_tokens_match_gqa_decode():
+    """Query groups that gqa_decode takes: the same values within the two
+    calls' roundings."""
+    g = _gen(61)
+    lens = [1, 64, 1000, 4097]
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 8, 64, "mxfp4")
+    q = _randn(g, 4, 32, D)
+    a, la = K.gqa_extend(c, bt, _i32(lens), 4097, q)
+    b, lb = K.gqa_decode(c, bt, _i32(lens), 4097, q)
+    assert float((la - lb).abs().max()) <= 1e-4
+    ref = _attend_ref(c, bt, lens, [1] * 4, q)
+    _check(a, la, ref)
+    # gqa_decode's own probabilities are rounded more coarsely (2^-8)
+    assert float((a.float() - b.float()).abs().max()) <= 0.02
+
+
+def test_prompt_then_tokens_run_together():
+    """A model's use: two prompts written with rotated keys and attended in
+    two chunks, then single tokens; every step against the fp64 formula over
+    everything written so far."""
+    g = _gen(71)
+    n_kv, n_h, bs = 2, 16, 16
+    plan = K.rope_plan(D, sections=[16, 24, 24])
+    total = [150, 40]
+    bt, blocks = _table(g, [t + 8 for t in total], bs)
+    c = _cache(g, blocks, n_kv, bs, "mxfp4", fill=False)
+    past = [0, 0]
+    for counts in ([100, 33], [50, 7], [1, 1], [1, 1], [3, 0]):
+        rows = sum(counts)
+        qkv = _randn(g, rows, n_h + 2 * n_kv, D)
+        q, k, v = qkv[:, :n_h], qkv[:, n_h:n_h + n_kv], qkv[:, n_h + n_kv:]
+        pos = torch.randint(0, 300, (3, rows), generator=g,
+                            device="cuda").to(torch.int32)
+        rs = _starts(counts)
+        wq, wk = K.rope(plan, pos, q, k)
+        qr = K.kv_write(c, bt, _i32(past), rs, k, v, rope=plan, positions=pos,
+                        q=q)
+        assert torch.equal(qr, wq)
+        kb, vb = K.kv_read(c, bt, _i32(past), rs, rows)
+        bits = wk.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+        want = oracle.mxfp4_rows_to_f64(oracle.mxfp4_encode_rows(bits), D)
+        assert torch.equal(kb.cpu().double(), torch.from_numpy(want))
+        past = [a + b for a, b in zip(past, counts)]
+        out, lse = K.gqa_extend(c, bt, _i32(past), max(past), qr, rs,
+                                max(counts))
+        _check(out, lse, _attend_ref(c, bt, past, counts, qr))
+    assert K.device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# graphs, streams, repetition
+# ---------------------------------------------------------------------------
+def _step(c, bt, past, lens, rs, max_rows, qkv, n_h, n_kv, plan, pos):
+    q, k, v = qkv[:, :n_h], qkv[:, n_h:n_h + n_kv], qkv[:, n_h + n_kv:]
+    qr = K.kv_write(c, bt, past, rs, k, v, rope=plan, positions=pos, q=q)
+    out, lse = K.gqa_extend(c, bt, lens, bt.shape[1] * c.block_size, qr, rs,
+                            max_rows)
+    kb, vb = K.kv_read(c, bt, past, rs, qkv.shape[0])
+    return qr, out, lse, kb, vb
+
+
+@pytest.mark.parametrize("counts,n_kv", [([1, 1], 8), ([5, 6], 8),
+                                         ([200, 90], 2)])
+def test_captured_and_replayed(counts, n_kv):
+    """Two graphs of the same step share no workspace; replays with other
+    inputs, other lengths and interleaved with eager calls."""
+    g = _gen(81)
+    n_h = 8 * n_kv
+    rows = sum(counts)
+    bt, blocks = _table(g, [2000, 1200], 64)
+    plan = K.rope_plan(D)
+    rs = _starts(counts)
+    state = []
+    for i in range(2):
+        c = _cache(g, blocks, n_kv, 64, "mxfp4")
+        state.append(dict(
+            c=c, past=_i32([1500, 700]), qkv=_randn(g, rows, n_h + 2 * n_kv,
+                                                    D),
+            pos=torch.randint(0, 999, (1, rows), generator=g,
+                              device="cuda").to(torch.int32)))
+    for s in state:
+        s["lens"] = s["past"] + _i32(counts)
+
+    def run(s):
+        return _step(s["c"], bt, s["past"], s["lens"], rs, max(counts),
+                     s["qkv"], n_h, n_kv, plan, s["pos"])
+    for s in state:
+        run(s)
+    torch.cuda.synchronize()
+    for s in state:
+        s["graph"] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(s["graph"]):
+            s["out"] = run(s)
+    for past in ([1500, 700], [3, 0], [1799, 64]):
+        for s in state:
+            s["past"].copy_(_i32(past))
+            s["lens"].copy_(_i32([a + b for a, b in zip(past, counts)]))
+            s["qkv"].copy_(_randn(g, *s["qkv"].shape))
+        for s in state:
+            s["graph"].replay()
+        torch.cuda.synchronize()
+        got = [[t.clone() for t in s["out"]] for s in state]
+        for s, o in zip(state, got):
+            for a, b in zip(o, run(s)):
+                assert torch.equal(a, b)
+    assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("counts,n_kv", [([1] * 8, 8), ([200, 90], 2)])
+def test_on_another_stream_and_repeated(counts, n_kv):
+    """A stream of the caller's, both ways of naming it, and the same bits
+    from every repetition."""
+    g = _gen(91)
+    n_h = 8 * n_kv
+    lens = [700 + 100 * i for i in range(len(counts))]
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, n_kv, 64, "mxfp4")
+    q = _randn(g, sum(counts), n_h, D)
+    args = (c, bt, _i32(lens), max(lens), q, _starts(counts), max(counts))
+    want, wl = K.gqa_extend(*args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        a, la = K.gqa_extend(*args, stream=side)
+        with torch.cuda.stream(side):
+            b, lb = K.gqa_extend(*args)
+        side.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, want)
+        assert torch.equal(la, wl) and torch.equal(lb, wl)
+
+
+def test_workspace_of_the_caller():
+    g = _gen(101)
+    lens = [3000]
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 1, 64, "mxfp4")
+    q = _randn(g, 40, 8, D)
+    rs = _starts([40])
+    n = K.extend_workspace_size(c, bt, _i32(lens), 3000, 40, 8, 40)
+    assert n > 0
+    args = (c, bt, _i32(lens), 3000, q, rs, 40)
+    want, _ = K.gqa_extend(*args)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # NaN
+    out, _ = K.gqa_extend(*args, workspace=ws)
+    assert torch.equal(out, want)
+    with pytest.raises(K.KvdError, match="workspace"):
+        K.gqa_extend(*args, workspace=ws[:n - 256])
+    # no launch of few CTAs or many changes the values beyond the merge's
+    # rounding
+    for ctas in (1, 7, 1000):
+        K.set_tuning(decode_ctas=ctas)
+        try:
+            out, lse = K.gqa_extend(*args)
+            one, l1 = K.gqa_extend(c, bt, _i32(lens), 3000, q[:1])
+        finally:
+            K.set_tuning()
+        _check(out, lse, _attend_ref(c, bt, lens, [40], q))
+        _check(one, l1, _attend_ref(c, bt, lens, [1], q[:1]))
+
+
+def test_empty_calls():
+    g = _gen(111)
+    bt, blocks = _table(g, [10], 16)
+    c = _cache(g, blocks, 2, 16, "mxfp4")
+    none = _randn(g, 0, 2, D)
+    rs = _i32([0, 0])
+    K.kv_write(c, bt, _i32([0]), rs, none, none)
+    k, v = K.kv_read(c, bt, _i32([0]), rs, 0)
+    out, lse = K.gqa_extend(c, bt, _i32([10]), 10, _randn(g, 0, 4, D), rs, 0)
+    plan = K.rope_plan(D)
+    q, _ = K.rope(plan, _i32([[]]).reshape(1, 0), none)
+    assert k.shape == v.shape == q.shape == (0, 2, D)
+    assert out.shape == (0, 4, D) and lse.shape == (0, 4)
+    # rows that no sequence owns: nothing is written, nothing attended
+    rows = _randn(g, 3, 2, D)
+    before = c.k.clone()
+    K.kv_write(c, bt, _i32([0]), rs, rows, rows)
+    o = torch.full((3, 4, D), 5.0, dtype=BF, device="cuda")
+    K.gqa_extend(c, bt, _i32([10]), 10, _randn(g, 3, 4, D), rs, 3, out=o)
+    assert torch.equal(c.k, before) and bool((o == 5).all())
+    assert K.device_error() == 0
+
+
+def test_tensors_of_two_devices_are_refused():
+    g = _gen(121)
+    bt, blocks = _table(g, [10], 16)
+    c = _cache(g, blocks, 2, 16, "mxfp4")
+
+    class Elsewhere(torch.Tensor):
+        @property
+        def device(self):
+            return torch.device("cuda", 7)
+    q = _randn(g, 1, 4, D).as_subclass(Elsewhere)
+    with pytest.raises(ValueError, match="in one call"):
+        K.gqa_extend(c, bt, _i32([10]), 10, q)
+
+
+def test_offsets_past_32_bits():
+    """Blocks and rows whose byte (and element) offsets pass 2^32: written,
+    read back, attended by every kernel, rotated."""
+    g = _gen(131)
+    n_kv, bs = 8, 64
+    blocks = 2 ** 32 // (n_kv * bs * 72) + 100
+    cache = [torch.empty((blocks, n_kv, bs, 72), dtype=torch.uint8,
+                         device="cuda") for _ in range(2)]
+    c = K.PagedCache(*cache, bs, n_kv, D, "mxfp4")
+    counts = [200, 150]
+    bt = _i32([[blocks - 1 - i for i in range(4)],
+               [1, blocks - 9, 0, blocks - 8]])
+    k, v = (_randn(g, 350, n_kv, D) for _ in range(2))
+    rs, start = _starts(counts), _i32([0, 0])
+    K.kv_write(c, bt, start, rs, k, v)
+    small = K.PagedCache(*(t[[blocks - 1 - i for i in range(4)] +
+                             [1, blocks - 9, 0]].contiguous() for t in cache),
+                         bs, n_kv, D, "mxfp4")
+    st = _i32([[0, 1, 2, 3], [4, 5, 6, 0]])
+    for a, b in zip(K.kv_read(c, bt, start, rs, 350),
+                    K.kv_read(small, st, start, rs, 350)):
+        assert torch.equal(a, b)
+    for n in (1, 3, 20, 70):
+        q = _randn(g, 2 * n, 64, D)
+        args = (_i32(counts), 200, q, _starts([n, n]), n)
+        a, la = K.gqa_extend(c, bt, *args)
+        b, lb = K.gqa_extend(small, st, *args)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    assert K.device_error() == 0
+    del c, cache
+    far = torch.empty(2 ** 32 + 4096, dtype=BF, device="cuda")
+    rows = far.as_strided((5, 2, D), (2 ** 30, 512, 1))
+    x = _randn(g, 5, 2, D)
+    rows.copy_(x)
+    plan = K.rope_plan(D)
+    pos = _i32([[1, 2, 3, 4, 5]])
+    want, _ = K.rope(plan, pos, x)
+    K.rope(plan, pos, rows, q_out=rows)
+    assert torch.equal(rows, want)
