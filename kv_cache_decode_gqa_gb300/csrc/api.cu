@@ -15,6 +15,7 @@
 #include "kvd.h"
 #include "kvd_prompt.h"
 #include "kvd_internal.h"
+#include "prompt_internal.h"
 
 namespace {
 

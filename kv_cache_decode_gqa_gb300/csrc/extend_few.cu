@@ -40,8 +40,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "kvd_common.cuh"
-#include "stream_k.cuh"
+#include "prompt_common.cuh"
 
 namespace kvd {
 namespace {
@@ -120,7 +119,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
     s_producer_done = 0;
   }
   __syncthreads();
-  build_partition(wp, p, &s_len_err, CH, n_units);
+  build_rows_partition(wp, p, &s_len_err, CH, n_units);
   const int total = wp.total;
   const int P = p.whole_units ? (int)gridDim.x
                               : min((int)gridDim.x, max(total, 1));
@@ -192,8 +191,8 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
       if (mine < n) {
         cur = cursor_at(wp, p.batch, lo + mine);
         const int len = wp.len[cur.b];
-        tok = seq_first(p, cur.b, len, CH) + cur.k * CH;
-        t0 = max(tok, seq_lo(p, cur.b, len)) & ~1;
+        tok = rows_first(p, cur.b, len, CH) + cur.k * CH;
+        t0 = max(tok, rows_lo(p, cur.b, len)) & ~1;
         t1 = (min(tok + CH, len) + 1) & ~1;
         b0 = t0 / bs;
         nb = (t1 - 1) / bs - b0 + 1;
@@ -272,7 +271,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
     T = wp.len[b];
     un = seq_rows(p, b);
     urow = p.row_start ? p.row_start[b] : b;
-    ulo = seq_lo(p, b, T);
+    ulo = rows_lo(p, b, T);
     const int kvh = h * HP + hj;
     // (every warp of a head writes the same query fragments; finish_unit's
     // barriers keep them apart from the last unit's readers)
@@ -416,7 +415,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
     const ChunkCursor cc = cursor_at(wp, p.batch, x);
     start_unit(cc.b, cc.h);
     const int nk = min(wp.nch[cc.b] - cc.k, hi - x);  // chunks of the unit
-    int ctok = seq_first(p, cc.b, T, CH) + cc.k * CH;
+    int ctok = rows_first(p, cc.b, T, CH) + cc.k * CH;
     // positions that every pair sees; others are masked pair by pair
     const int all_lo =
         max(p.win_start ? max(p.win_start[cc.b], 0) : 0,
@@ -635,7 +634,7 @@ __global__ void __launch_bounds__(kRowMergeThreads, 8)
   // the lengths and row lists are read before the launch before completes:
   // it does not write them, and it lets this one start only after its own
   // predecessor has completed
-  build_partition(wp, p, &s_len_err, chunk, n_units);
+  build_rows_partition(wp, p, &s_len_err, chunk, n_units);
   pdl_wait();
   const int total = wp.total;
   if (total == 0) return;

@@ -40,9 +40,8 @@
 #include <climits>
 #include <cmath>
 
-#include "kvd_common.cuh"
-#include "stream_k.cuh"
-#include "tcgen05.cuh"
+#include "prompt_common.cuh"
+#include "tcgen05_pair.cuh"
 
 namespace kvd {
 namespace {

@@ -316,15 +316,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar,
   return false;
 }
 
-// The same with release semantics at CTA scope only: for arrivals that
-// publish data of this SM (its shared memory after a proxy fence, its tensor
-// memory after a wait) to work that the other CTA's thread starts on this SM.
-// 100 ns one way where the cluster-scope release took 360 (idle SM).
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr)
-               : "memory");
-}
-
 __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -500,36 +491,6 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t b) {
       : "=r"(r)
       : "r"(b & 0xffu));
   return r;
-}
-
-// The eight E2M1 codes of a word (first code in the low nibble) to four f16
-// pairs, exact. The unpacked bytes let the conversion pick its byte itself:
-// 41 pairs a cycle and SM against 20 with a shift before each conversion
-// (measured with 16 warps, one multiply a pair).
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-      : "r"(w));
-}
-
-// Product of two f16 pairs, each rounded to nearest even.
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Exponent field of the power of two that takes a query row whose largest
-// bf16 magnitude has bits `amax` into [2^14, 2^15), where f16 holds it (1
-// for a row with an infinity or NaN, which then shows in its outputs).
-__device__ __forceinline__ int row_exponent(uint32_t amax) {
-  const int e = max((int)(amax >> 7), 1);
-  return e == 255 ? 127 : min(268 - e, 254);
 }
 
 // One 16-channel group of a new bf16 row into an MXFP4 row: 8 bytes of

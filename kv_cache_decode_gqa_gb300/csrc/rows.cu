@@ -20,7 +20,7 @@
 // 16-channel group instead of 16 exact divisions (mxfp4_group).
 #include <algorithm>
 
-#include "kvd_common.cuh"
+#include "prompt_common.cuh"
 
 namespace kvd {
 namespace {

@@ -46,24 +46,6 @@ __device__ __forceinline__ int seq_first(const DecodeParams &p, int b, int T,
   return lo - lo % chunk;
 }
 
-// The same for a call whose sequences have several new rows each
-// (kvd_gqa_extend): the first row's window reaches lowest. A sequence
-// without rows attends to nothing.
-__device__ __forceinline__ int seq_rows(const ExtendParams &p, int b) {
-  if (!p.row_start) return 1;
-  const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
-  if (r0 < 0 || r1 < r0 || r1 > p.rows || r1 - r0 > p.max_rows) return 0;
-  // after a descent the rows may be another sequence's
-  return b > 0 && p.row_start[b - 1] > r0 ? 0 : r1 - r0;
-}
-__device__ __forceinline__ int seq_lo(const ExtendParams &p, int b, int T) {
-  const int n = seq_rows(p, b);
-  if (n == 0) return T;
-  int lo = p.win_start ? p.win_start[b] : 0;
-  if (p.window > 0) lo = max(lo, T - n + 1 - p.window);
-  return min(max(lo, 0), T);
-}
-
 // Whether any sequence of the call has a lower bound (window or start).
 __device__ __forceinline__ bool has_window(const DecodeParams &p) {
   return p.window > 0 || p.win_start != nullptr;
@@ -74,9 +56,9 @@ __device__ __forceinline__ bool has_window(const DecodeParams &p) {
 // length from its first chunk's start (seq_first; 0 when nothing is
 // attended). Every thread of the block calls it (blockDim.x a multiple of
 // 32); it ends with a barrier.
-template <int NB, class Params>
+template <int NB>
 __device__ __forceinline__ void build_partition(WorkPartitionT<NB> &wp,
-                                                const Params &p,
+                                                const DecodeParams &p,
                                                 int *len_error,
                                                 int chunk = kStageRows,
                                                 int units = -1) {

@@ -51,13 +51,6 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n,
          ((uint32_t)(m >> 4) << 24);
 }
 
-// The same with f16 A and B (type bits 0).
-__host__ __device__ constexpr uint32_t umma_idesc_f16(int m, int n,
-                                                      bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-
 // D (TMEM) [+]= A (shared) x B (shared).
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc,
                                         uint64_t b_desc, uint32_t idesc,
@@ -121,66 +114,6 @@ __device__ __forceinline__ void umma_commit_elect(uint64_t *bar) {
       "elect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster."
       "b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
-
-// The CTA-pair forms (cta_group::2; every tcgen05 instruction of a kernel
-// uses one form): the pair's CTA 0 issues for both. M = 256: each CTA holds
-// 128 rows of A, D (and a tensor-memory A) in its own memory; B's N columns
-// are split, each CTA's shared memory holding half of them at the same
-// offset. Commits arrive on the barrier at `bar`'s offset in both CTAs.
-__device__ __forceinline__ void umma2_ss_elect(uint32_t d_tmem,
-                                               uint64_t a_desc,
-                                               uint64_t b_desc,
-                                               uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void umma2_ts_elect(uint32_t d_tmem,
-                                               uint32_t a_tmem,
-                                               uint64_t b_desc,
-                                               uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
-          d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void umma2_commit_elect(uint64_t *bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "mov.b16 m, 3;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."
-      "multicast::cluster.b64 [%0], m;\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tmem2_alloc(uint32_t *dst, uint32_t ncols) {
-  asm volatile(
-      "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-          smem_u32(dst)),
-      "r"(ncols)
-      : "memory");
-}
-__device__ __forceinline__ void tmem2_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::
-                   : "memory");
-}
-__device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile(
-      "tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr),
-      "r"(ncols)
       : "memory");
 }
 
@@ -254,31 +187,6 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
         "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
         "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
         "+r"(r[30]), "+r"(r[31])
-      :
-      : "memory");
-}
-
-// 16 consecutive columns of this thread's lane, and the wait for them.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
-        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]),
-        "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
-        "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-        "+r"(r[15])
       :
       : "memory");
 }
