@@ -154,15 +154,19 @@ kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
  *   q         rows x n_h, head_dim wide, 16-byte aligned, strides multiples
  *             of 8; head h reads KV head h / (n_h / n_kv)
  *   scale     softmax scale; <= 0 selects 1/sqrt(head_dim)
- *   out       device bf16 [rows][n_h][head_dim], 16-byte aligned
+ *   out       device bf16 [rows][n_h][head_dim], 16-byte aligned; must not
+ *             overlap q
  *   lse       device fp32 [rows][n_h] or NULL
  *   workspace at least kvd_extend_workspace_size() bytes, 256-byte aligned
  *             (NULL when that is 0); see "Workspace" in kvd.h
  * Rows from row_start[batch] on are left as they were. A sequence whose
  * row_start entries descend (or follow a descent), pass q->rows or are more
- * than max_rows apart is skipped and flagged KVD_DEVERR_LEN. Scores and sums in fp32; the
- * queries enter the first product as f16 with a power-of-two scale per
- * (row, head), the probabilities enter the second as f16.
+ * than max_rows apart is skipped and flagged KVD_DEVERR_LEN. Scores and sums
+ * in fp32; the queries enter the first product as f16 with a power-of-two
+ * scale per (row, head), the probabilities enter the second as f16. A query
+ * that is not finite stays in its own (row, head). The writing calls store
+ * finite groups only; where a caller's own bytes hold a NaN scale of V, rows
+ * of the same sequence that do not see the position may become NaN as well.
  * Supported: an MXFP4 cache (head_dim 128), n_h / n_kv of 1 .. 128, at most
  * 1024 sequences a call. seqs->flags must be valid and are ignored.
  */

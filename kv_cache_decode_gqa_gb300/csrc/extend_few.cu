@@ -1,5 +1,5 @@
 // Attention of few new rows a sequence over an MXFP4 cache: kvd_gqa_extend
-// where a kv head serves at most 32 (row, query head) pairs -- single tokens,
+// where a kv head serves at most 16 (row, query head) pairs -- single tokens,
 // or a few speculated ones.
 //
 // A position costs 144 bytes a kv head (72 of K, 72 of V) and 2 x 128
@@ -21,7 +21,15 @@
 // So the widening does not grow with the pairs, and pairs beyond 8 cost only
 // their products and exponentials. (With O = P V, pairs on M = 16, and the
 // maxima reduced every chunk, decode at 8 pairs took 806 instructions per 16
-// tokens and ran at a fifth of HBM's rate.)
+// tokens and ran at a fifth of HBM's rate.) At 32 pairs the tcgen05 kernel is
+// ahead (16 sequences of 4 rows and 8 heads a group over 9,200 positions: 99
+// us there, 194 us with four tiles of pairs here).
+//
+// Measured: 32 single tokens, 8 kv heads of 8 pairs over 4,600 positions
+// (171 MB), 55 us, of which the merge launch is 8 (the copies and the merge
+// alone: 52 us); 4 kv heads of 16 pairs over 18,400 positions (341 MB), 111
+// us (the copies alone 72 us: there the widening, products and exponentials
+// of 8 warps bind it; 16 warps spill with two tiles of pairs, 12 took 116 us).
 //
 // A code times its E4M3 scale is exact in f16 (6 significand bits). Queries
 // are bf16; each (row, head) is scaled by a power of two so that its largest
