@@ -1093,10 +1093,15 @@ struct ExtendPlan {
 // Few (row, head) pairs a kv head (at most 16): the stream-K kernel with one
 // CTA per SM. Else blocks of 256 pairs a CTA, or of 512 a pair of CTAs where
 // a sequence may have more than 256 (one prompt chunk of 1,021 tokens over
-// 32,000, 56 heads: 802 us with pairs, 856 us without). Enough blocks fill
+// 32,000, 56 heads: 802 us with pairs, 856 us without, in four waves). Enough blocks fill
 // the SMs by themselves (two waves and more); fewer are split over the
-// positions into about four waves of equal shares, so that ragged lengths
-// level out.
+// positions. Several sequences are split into three waves of parts, were all
+// as long as max_seq_len, so that ragged lengths level out (4 rows of each of
+// 16 sequences of 2K to 14K: 95 us; two waves 103, four 109, eight 119). One
+// sequence's blocks are about equally long, and the number of parts whose
+// last wave ends first is taken (the chunk above: 3 waves of halves, 726 us;
+// thirds, in 4.4 waves, 802). A choice by the lengths themselves, on the
+// device, cost every CTA 1 to 4 us and found no better parts.
 ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
                        int max_rows, int n_h, int sms) {
   ExtendPlan pl;
@@ -1133,18 +1138,33 @@ ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
   const int ctas_per_block = (long)max_rows * g > kvd::kExtendRows ? 2 : 1;
   const int block_rows = ctas_per_block * kvd::kExtendRows;
   pl.p.block_rows = block_rows;
-  pl.blocks = (int)(pairs / block_rows + std::min(s->batch, rows));
+  pl.blocks =
+      (int)((pairs + (long)std::min(s->batch, rows) * (block_rows - 1)) /
+            block_rows);
   const int ch = kvd::kExtendChunk;
   long chunks = (s->max_seq_len + ch - 1) / ch;
   if (s->window > 0)
     chunks = std::min<long>(
         chunks, ((long)s->window + block_rows / g + ch) / ch + 2);
   const long ctas = (long)pl.blocks * c->n_kv * ctas_per_block;
-  const long want = forced > 0 ? forced : 4L * sms;
+  const long want = forced > 0 ? forced : 3L * sms;
   if (forced > 0 || ctas < 2L * sms) {
+    long per = (ctas * chunks + want - 1) / want;
+    if (forced <= 0 && s->batch == 1) {
+      // a part costs kPartCost chunks beyond its own: its queries, the
+      // filling and emptying of the pipeline, its share of the merge
+      constexpr long kPartCost = 4;
+      const long most = std::max(1L, 16L * sms / ctas);
+      long best = -1;
+      for (long n = 1; n <= most && n <= chunks; ++n) {
+        const long each = (chunks + n - 1) / n;
+        const long cost =
+            (ctas * n + sms - 1) / sms * (each + kPartCost);
+        if (best < 0 || cost < best) best = cost, per = each;
+      }
+    }
     // (a launch has at most 65,535 splits)
-    const long per = std::max({4L, (ctas * chunks + want - 1) / want,
-                               (chunks + 65534) / 65535});
+    per = std::max({4L, per, (chunks + 65534) / 65535});
     if (per < chunks) {
       pl.p.chunks_per_split = (int)per;
       pl.splits = (int)((chunks + per - 1) / per);

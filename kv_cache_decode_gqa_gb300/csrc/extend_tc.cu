@@ -26,18 +26,18 @@
 // swizzled tiles that both products read. Raw rows come through a ring of
 // bulk copies, so that the widening never waits for HBM.
 //
-// Measured: 1,021 rows over 32,000 positions, 56 heads of 8 kv heads, in 797
-// us (1,194 TFLOP/s, 62% of cuBLAS's bf16 rate; 856 us without the pairs);
-// whole prompts of 7,001 rows in two sequences, 64 heads, in 426 us; 4 rows
-// of each of 16 sequences over 9,200 positions (171 MB) in 99 us. Without
-// the exponentials the first takes 627 us, without the widening 779, without
-// most of the products 744, with none of them 478: it is the time from a
+// Measured: 1,021 rows over 32,000 positions, 56 heads of 8 kv heads, in 726
+// us (1,311 TFLOP/s, 68% of cuBLAS's bf16 rate); whole prompts of 7,001 rows
+// in two sequences, 64 heads, in 426 us; 4 rows of each of 16 sequences over
+// 8,700 positions (160 MB) in 95 us. In a less even split (797 us) the first
+// took 627 us without the exponentials, 779 without the widening, 744 without
+// most of the products, 478 with none of them: it is the time from a
 // product's end to the softmax and from P back to the next product that is
 // left, one after the other in each of a tile's two buffers. (Softmax groups
 // that take turns on named barriers: 850 us; one S buffer of 128 positions a
 // tile: the same; K and V handed over by halves of a chunk: the 426 us became
-// 452; a third K tile in the place of an unused second tile: the 99 us became
-// 111, for the ring of raw rows shrinks.)
+// 452; a third K tile in the place of an unused second tile: 4% slower for
+// the few rows, for the ring of raw rows shrinks.)
 //
 // The softmax keeps a reference maximum per pair and moves it only when a
 // chunk exceeds it by more than 2^8 (the accumulator is rescaled then, in
@@ -146,25 +146,34 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// A row block of the batch: block `mb` of sequence b, its pairs [f0, f1),
-// and the positions [lo, hi) they see.
+// What a sequence's blocks are computed from.
+struct Seq {
+  int n, T;  // its rows and visible length
+  int s;     // its first visible position
+};
+
+__device__ __forceinline__ Seq seq_at(const ExtendParams &p, int b) {
+  Seq q;
+  q.n = seq_rows(p, b);
+  q.T = min(max(p.seq_lens[b], 0), p.max_seq_len);
+  q.s = p.win_start ? max(p.win_start[b], 0) : 0;
+  return q;
+}
+
+// A row block: the pairs [f0, f1) of block `mb` of a sequence, and the
+// positions [lo, hi) they see.
 struct Block {
-  int n, T;    // rows and visible length of the sequence
   int f0, f1;
   int lo, hi;
 };
 
-__device__ __forceinline__ Block block_at(const ExtendParams &p, int b,
+__device__ __forceinline__ Block block_at(const ExtendParams &p, const Seq &q,
                                           int mb, int G) {
   Block k;
-  k.n = seq_rows(p, b);
-  k.T = min(max(p.seq_lens[b], 0), p.max_seq_len);
   k.f0 = mb * p.block_rows;
-  k.f1 = min(k.f0 + p.block_rows, k.n * G);
-  const int first = k.T - k.n + k.f0 / G, last = k.T - k.n + (k.f1 - 1) / G;
-  int lo = p.win_start ? max(p.win_start[b], 0) : 0;
-  if (p.window > 0) lo = max(lo, first + 1 - p.window);
-  k.lo = lo;
+  k.f1 = min(k.f0 + p.block_rows, q.n * G);
+  const int first = q.T - q.n + k.f0 / G, last = q.T - q.n + (k.f1 - 1) / G;
+  k.lo = p.window > 0 ? max(q.s, first + 1 - p.window) : q.s;
   k.hi = max(last + 1, 0);
   return k;
 }
@@ -174,6 +183,11 @@ __device__ __forceinline__ void block_chunks(const Block &k, int &c0,
                                              int &c1) {
   c0 = k.lo / kN;
   c1 = k.lo < k.hi ? (k.hi + kN - 1) / kN : c0;
+}
+
+// Equal parts, of at most `per` chunks (0: one part), of a block's n chunks.
+__device__ __forceinline__ int block_parts(int per, int n) {
+  return per > 0 ? max((n + per - 1) / per, 1) : 1;
 }
 
 template <int CTAS>
@@ -196,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *odone = qfull + 1;
   int *flags = reinterpret_cast<int *>(smem + C::FLAG_OFF);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(flags);
-  int *s_blk = flags + 2;  // sequence and block of this CTA, total blocks
+  // this CTA's sequence, its block of it, and the sequence's Seq
+  int *s_blk = flags + 2;
   int *s_scan = reinterpret_cast<int *>(smem + C::SCAN_OFF);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -214,15 +229,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) s_blk[0] = -1;
   {
     int cnt[2], sum = 0;
+    Seq sq[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int b = 2 * tid + j;
       cnt[j] = 0;
+      sq[j] = Seq{0, 0, 0};
+      if (b < p.batch) sq[j] = seq_at(p, b);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int b = 2 * tid + j;
       if (b < p.batch) {
-        const int n = seq_rows(p, b);
-        cnt[j] = (int)(((long)n * G + C::ROWS - 1) / C::ROWS);
+        cnt[j] = (int)(((long)sq[j].n * G + C::ROWS - 1) / C::ROWS);
         if (blockIdx.x == 0 && blockIdx.y == 0) {
-          if (n == 0 && p.row_start && p.row_start[b] != p.row_start[b + 1])
+          if (sq[j].n == 0 && p.row_start &&
+              p.row_start[b] != p.row_start[b + 1])
             report(p.err, DEVERR_LEN);
           if (p.seq_lens[b] > p.max_seq_len) report(p.err, DEVERR_LEN);
         }
@@ -250,6 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mine >= excl && mine < excl + cnt[j]) {
         s_blk[0] = 2 * tid + j;
         s_blk[1] = mine - excl;
+        s_blk[2] = sq[j].n;
+        s_blk[3] = sq[j].T;
+        s_blk[4] = sq[j].s;
       }
       excl += cnt[j];
     }
@@ -257,12 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int b = s_blk[0], mb = s_blk[1];
   if (b < 0) return;  // past the batch's blocks
-  const Block k = block_at(p, b, mb, G);
+  const Seq q = {s_blk[2], s_blk[3], s_blk[4]};
+  const Block k = block_at(p, q, mb, G);
   int c0, c1;
   block_chunks(k, c0, c1);
-  const int per = p.chunks_per_split > 0 ? p.chunks_per_split
-                                         : max(c1 - c0, 1);
-  const int parts = max((c1 - c0 + per - 1) / per, 1);
+  const int parts = block_parts(p.chunks_per_split, c1 - c0);
+  const int per = (c1 - c0 + parts - 1) / parts;
   const int part = blockIdx.y;
   if (part >= parts) return;
   c0 += part * per;
@@ -374,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warp masks nothing for it; its query is 0 and nothing of it is stored)
     int vlo = 0, vhi = INT_MAX;
     if (live) {
-      const int pos = k.T - k.n + f / G;
+      const int pos = q.T - q.n + f / G;
       vhi = max(pos + 1, 0);
-      vlo = p.win_start ? max(p.win_start[b], 0) : 0;
+      vlo = q.s;
       if (p.window > 0) vlo = max(vlo, pos + 1 - p.window);
     }
     // ---- the pair's query, scaled into f16 (tile t, or both halves' one)
@@ -384,11 +409,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       uint4 x[16];
       uint32_t m = 0;
-      const uint16_t *q = p.q + (row0 + f / G) * p.q_rs +
-                          ((long)h * G + f % G) * p.q_hs;
+      const uint16_t *src = p.q + (row0 + f / G) * p.q_rs +
+                            ((long)h * G + f % G) * p.q_hs;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        x[c] = live ? reinterpret_cast<const uint4 *>(q)[c]
+        x[c] = live ? reinterpret_cast<const uint4 *>(src)[c]
                     : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
@@ -911,10 +936,11 @@ __global__ void __launch_bounds__(kRowMergeThreads)
     r0 = p.row_start[b];
   }
   if (row < r0 || row >= r0 + seq_rows(p, b)) return;  // no sequence's row
-  const Block k = block_at(p, b, ((row - r0) * G + hh % G) / p.block_rows, G);
+  const Block k = block_at(p, seq_at(p, b),
+                           ((row - r0) * G + hh % G) / p.block_rows, G);
   int c0, c1;
   block_chunks(k, c0, c1);
-  const int parts = (c1 - c0 + p.chunks_per_split - 1) / p.chunks_per_split;
+  const int parts = block_parts(p.chunks_per_split, c1 - c0);
   if (parts <= 1) return;  // written whole
   const long n = (long)p.rows * p.n_h;
   float M, W;

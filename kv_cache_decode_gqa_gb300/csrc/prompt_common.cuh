@@ -53,10 +53,13 @@ __device__ __forceinline__ int row_exponent(uint32_t amax) {
 // New rows of sequence b; 0 for a row list that is not one.
 __device__ __forceinline__ int seq_rows(const ExtendParams &p, int b) {
   if (!p.row_start) return 1;
+  // (three loads at once; a branch between them would chain their latencies)
+  const int rp = p.row_start[max(b - 1, 0)];
   const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
-  if (r0 < 0 || r1 < r0 || r1 > p.rows || r1 - r0 > p.max_rows) return 0;
   // after a descent the rows may be another sequence's
-  return b > 0 && p.row_start[b - 1] > r0 ? 0 : r1 - r0;
+  const bool bad = (r0 < 0) | (r1 < r0) | (r1 > p.rows) |
+                   ((long)r1 - r0 > p.max_rows) | (rp > r0);
+  return bad ? 0 : r1 - r0;
 }
 
 // First position the rows of sequence b attend to (its visible length is T):

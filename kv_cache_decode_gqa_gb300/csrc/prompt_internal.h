@@ -46,7 +46,7 @@ struct ExtendParams : DecodeParams {
   int32_t max_rows, rows;    // bound on a sequence's rows; rows of q
   long q_rs, q_hs;           // strides of q between rows and heads, elements
   // tcgen05 kernel: pairs of a row block, and chunks of it that one CTA (or
-  // pair of CTAs) takes
+  // pair of CTAs) takes at most
   int32_t block_rows, chunks_per_split;
 };
 
@@ -71,10 +71,10 @@ cudaError_t launch_extend_few(const ExtendParams &p, const FewPlan &f,
                               cudaStream_t s);
 // kvd_gqa_extend otherwise, on tcgen05: blocks of block_rows (row, head)
 // pairs of a kv head -- kExtendRows a CTA, 2 kExtendRows a pair of CTAs --
-// against chunks of kExtendChunk positions, chunks_per_split of a block's at
-// a time (0: all of them; else partials [split][rows][n_h] and a merge
-// launch). `blocks`: a bound on the row
-// blocks of the batch, `splits` on a block's splits.
+// against chunks of kExtendChunk positions, a block's in equal parts of at
+// most chunks_per_split (0: one part; else partials [split][rows][n_h] and a
+// merge launch). `blocks`: a bound on the row blocks of the batch, `splits`
+// on a block's parts.
 constexpr int kExtendRows = 256;
 constexpr int kExtendChunk = 128;
 cudaError_t launch_extend_tc(const ExtendParams &p, int blocks, int splits,
