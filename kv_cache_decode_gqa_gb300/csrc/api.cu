@@ -1129,6 +1129,7 @@ ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
     }
     ctas = std::max(1L, std::min(ctas, std::max(chunks, 1L)));
     pl.p.n_splits = (int)ctas;
+    if (chunks >= 8 * ctas) pl.p.gap = kvd::kUnitGap;
     const size_t slots = (size_t)ctas * 2 * f.hp * 8 * f.tiles;
     pl.ws_o_bytes = round_up(slots * 128 * 4, 256);
     pl.ws_bytes = pl.ws_o_bytes + round_up(slots * 4, 256);

@@ -42,9 +42,10 @@
 // so f16 rounds them by 2^-11, 1/8 of the bf16 output's rounding.
 //
 // Work is split as in the other dense decode kernels (stream_k.cuh): one CTA
-// per SM with an equal share of all chunks, a producer warp that keeps a
-// ring of chunks in flight with bulk copies, W consumer warps, and a merge
-// launch for the units that CTAs share.
+// per SM with an equal share of all chunks (and of p.gap empty ones a unit
+// where the shares are long), a producer warp that keeps a ring of chunks in
+// flight with bulk copies, W consumer warps, and a merge launch for the units
+// that CTAs share.
 #include <algorithm>
 #include <cmath>
 
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
     s_producer_done = 0;
   }
   __syncthreads();
-  build_rows_partition(wp, p, &s_len_err, CH, n_units);
+  build_rows_partition(wp, p, &s_len_err, CH, n_units, p.gap);
   const int total = wp.total;
   const int P = p.whole_units ? (int)gridDim.x
                               : min((int)gridDim.x, max(total, 1));
@@ -191,13 +192,16 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
       L <<= 1;
     const int q = lane & (L - 1), batch = 32 / L;
     int s = 0, ph = 1;  // a fresh barrier passes a wait for parity 1
+    int used = 0;       // stages filled so far
     bool go = true;
     for (int base = 0; go && base < n; base += batch) {
       const int mine = base + lane / L;
       int tok = 0, t0 = 0, t1 = 0, b0 = 0, nb = 0, pb = 0;
       ChunkCursor cur{0, 0, 0};
-      if (mine < n) {
-        cur = cursor_at(wp, p.batch, lo + mine);
+      if (mine < n) cur = cursor_at(wp, p.batch, lo + mine);
+      const bool empty_chunk =
+          mine >= n || cur.k >= wp.nch[cur.b] - p.gap;
+      if (!empty_chunk) {
         const int len = wp.len[cur.b];
         tok = rows_first(p, cur.b, len, CH) + cur.k * CH;
         t0 = max(tok, rows_lo(p, cur.b, len)) & ~1;
@@ -208,14 +212,16 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
       }
       const int cnt = min(batch, n - base);
       for (int j = 0; j < cnt; ++j) {
+        if (__shfl_sync(0xffffffffu, empty_chunk, j * L)) continue;
         go = mbar_wait(&empty[s], ph);
         if (!go) report(p.err, DEVERR_TIMEOUT);
         go = __all_sync(0xffffffffu, go && !s_abort);
         if (!go) break;
         if (lane == j * L) {
           mbar_arrive_expect_tx(&full[s], 2u * HP * (t1 - t0) * kRow);
-          s_issued = base + j + 1;
+          s_issued = used + 1;
         }
+        ++used;
         __syncwarp();
         if (lane / L == j) {
           for (int k = q; k < nb; k += L) {
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
     float *wl = wm + W * SP;       // [warp][SP]
     float *wo = wl + W * SP;       // [warp][SP][D]
     const int ustart = wp.pre[b] + h * wp.nch[b];
-    const int uend = ustart + wp.nch[b];
+    const int uend = ustart + wp.nch[b] - p.gap;
     const bool whole = ustart >= lo && uend <= hi;
     const long wslot = c * 2 + partial_side(ustart, lo);
     const int pairs = un * G;
@@ -421,8 +427,11 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
   int s = 0, ph = 0;
   for (int x = lo; x < hi;) {
     const ChunkCursor cc = cursor_at(wp, p.batch, x);
+    const int left = wp.nch[cc.b] - cc.k;  // of the unit, empty ones with it
+    const int nk = min(left - p.gap, hi - x);
+    x += left;
+    if (nk <= 0) continue;
     start_unit(cc.b, cc.h);
-    const int nk = min(wp.nch[cc.b] - cc.k, hi - x);  // chunks of the unit
     int ctok = rows_first(p, cc.b, T, CH) + cc.k * CH;
     // positions that every pair sees; others are masked pair by pair
     const int all_lo =
@@ -606,7 +615,6 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
       if (++s == C::NS) s = 0, ph ^= 1;
     }
     finish_unit(cc.b, cc.h);
-    x += nk;
   }
   if (s_abort && tid == 0) {
     // after an abort: every copy that was issued has landed before this CTA
@@ -627,9 +635,10 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
 // A CTA is small enough to sit beside one of
 // that launch (128 threads, 64 registers, 1 KB for batches up to 64), so
 // that the partition is rebuilt while it still runs, and takes every
-// gridDim.x-th group of pairs. (256 threads and a CTA per two pairs
-// started only when the other launch had left the SMs: 10 us in all for 32
-// sequences of 8 kv heads.)
+// gridDim.x-th group of pairs; eight fit an SM (two an SM: 3 to 4 us more for
+// 2,048 pairs). (256 threads and a CTA per two pairs started only when the
+// other launch had left the SMs: 10 us in all for 32 sequences of 8 kv
+// heads.)
 constexpr int kRowMergeThreads = 128;
 
 template <int NB, int LANES>
@@ -642,7 +651,7 @@ __global__ void __launch_bounds__(kRowMergeThreads, 8)
   // the lengths and row lists are read before the launch before completes:
   // it does not write them, and it lets this one start only after its own
   // predecessor has completed
-  build_rows_partition(wp, p, &s_len_err, chunk, n_units);
+  build_rows_partition(wp, p, &s_len_err, chunk, n_units, p.gap);
   pdl_wait();
   const int total = wp.total;
   if (total == 0) return;
@@ -664,7 +673,8 @@ __global__ void __launch_bounds__(kRowMergeThreads, 8)
     if (wp.nch[b] == 0 || g >= seq_rows(p, b) * G) continue;
     const int ustart = wp.pre[b] + h * wp.nch[b];
     const int c_first = cta_of(ustart, total, P);
-    const int parts = cta_of(ustart + wp.nch[b] - 1, total, P) - c_first + 1;
+    const int parts =
+        cta_of(ustart + wp.nch[b] - p.gap - 1, total, P) - c_first + 1;
     if (parts == 1) continue;
     const long row0 = p.row_start ? p.row_start[b] : b;
     const int sl = j * slots + g;
@@ -702,7 +712,7 @@ cudaError_t launch_few_t(const ExtendParams &p, cudaStream_t s) {
   // parts of a unit of average length
   const bool many = p.n_splits > 6L * p.batch * n_units;
   const long per = many ? 1 : kRowMergeThreads / 32;
-  const dim3 grid((unsigned)std::min((pairs + per - 1) / per, 304L));
+  const dim3 grid((unsigned)std::min((pairs + per - 1) / per, 1216L));
   auto merge = p.batch <= kMergeSmallBatch
                    ? (many ? merge_few_kernel<kMergeSmallBatch, 4>
                            : merge_few_kernel<kMergeSmallBatch, 1>)

@@ -81,13 +81,16 @@ __device__ __forceinline__ int rows_first(const ExtendParams &p, int b, int T,
 }
 
 // build_partition (stream_k.cuh) for these sequences: `units` units each of
-// the chunks of `chunk` positions that the sequence's rows see. Every thread
-// of the block calls it; it ends with a barrier.
+// the chunks of `chunk` positions that the sequence's rows see and of `gap`
+// empty ones behind them, which stand for what a change of units costs the
+// CTA that makes it. Every thread of the block calls it; it ends with a
+// barrier.
 template <int NB>
 __device__ __forceinline__ void build_rows_partition(WorkPartitionT<NB> &wp,
                                                      const ExtendParams &p,
                                                      int *len_error,
-                                                     int chunk, int units) {
+                                                     int chunk, int units,
+                                                     int gap) {
   const int tid = threadIdx.x, nthreads = blockDim.x;
   __shared__ int warp_tot[32];
   // a run of consecutive sequences a thread, then a scan over the threads
@@ -104,7 +107,7 @@ __device__ __forceinline__ void build_rows_partition(WorkPartitionT<NB> &wp,
     const int lo = rows_lo(p, b, T);
     const int rows = lo < T ? T - (lo - lo % chunk) : 0;
     wp.len[b] = T;
-    wp.nch[b] = (rows + chunk - 1) / chunk;
+    wp.nch[b] = rows > 0 ? (rows + chunk - 1) / chunk + gap : 0;
     local += wp.nch[b] * units;
   }
   const int lane = tid & 31, warp = tid >> 5, nwarps = (nthreads + 31) >> 5;

@@ -45,6 +45,9 @@ struct ExtendParams : DecodeParams {
   const int32_t *row_start;  // [batch + 1], or null: row b is sequence b's
   int32_t max_rows, rows;    // bound on a sequence's rows; rows of q
   long q_rs, q_hs;           // strides of q between rows and heads, elements
+  // warp-MMA kernel: chunks that a change of units counts as in its CTAs'
+  // equal shares
+  int32_t gap;
   // tcgen05 kernel: pairs of a row block, and chunks of it that one CTA (or
   // pair of CTAs) takes at most
   int32_t block_rows, chunks_per_split;
@@ -61,7 +64,14 @@ cudaError_t launch_read(const RowsParams &p, int sms, cudaStream_t s);
 // kvd_gqa_extend, at most kFewPairs (row, head) pairs a kv head: warp-level
 // MMAs over units of `hp` kv heads, in chunks of `chunk` positions, `tiles`
 // tiles of 8 pairs.
+//
+// A change of units (kUnitGap): its queries' loads and its outputs take 3 to 5
+// us, a chunk about 1.1. (A pass of 32 sequences of 8 kv heads in a graph: 51.5
+// us with 0, 50.1 with 3, 49.0 with 4, 49.5 with 6; of 4 kv heads of 16 pairs
+// over 18,400 positions: 98.9, 93.9, 93.8, 94.0.) Shares of a few chunks are
+// cut evenly.
 constexpr int kFewPairs = 16;
+constexpr int kUnitGap = 4;
 struct FewPlan {
   int hp, chunk, tiles;
 };
