@@ -908,19 +908,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Log-sum-exp merge of the blocks that the launch before split over the
-// positions: one warp per output row, a float4 a lane, up to 8 parts'
-// loads in flight.
-constexpr int kRowMergeThreads = 256;
-
-__global__ void __launch_bounds__(kRowMergeThreads)
-    extend_merge_kernel(const __grid_constant__ ExtendParams p) {
-  pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long at = (long)blockIdx.x * (kRowMergeThreads / 32) + (threadIdx.x >> 5);
-  if (at >= (long)p.rows * p.n_h) return;
-  const int row = (int)(at / p.n_h), hh = (int)(at % p.n_h);
+// Parts of output row `at`, 0 where no sequence has it. Reads what the launch
+// before does not write.
+__device__ __forceinline__ int merge_parts(const ExtendParams &p, long at) {
+  if (at >= (long)p.rows * p.n_h) return 0;
+  const int row = (int)at / p.n_h, hh = (int)at - row * p.n_h;  // below 2^31
   const int G = p.n_h / p.n_kv;
   int b = row, r0 = row;
   if (p.row_start) {
@@ -935,13 +927,30 @@ __global__ void __launch_bounds__(kRowMergeThreads)
     b = lo;
     r0 = p.row_start[b];
   }
-  if (row < r0 || row >= r0 + seq_rows(p, b)) return;  // no sequence's row
-  const Block k = block_at(p, seq_at(p, b),
-                           ((row - r0) * G + hh % G) / p.block_rows, G);
+  const Seq q = seq_at(p, b);
+  if (row < r0 || row >= r0 + q.n) return 0;  // no sequence's row
+  const Block k =
+      block_at(p, q, ((row - r0) * G + hh % G) / p.block_rows, G);
   int c0, c1;
   block_chunks(k, c0, c1);
-  const int parts = block_parts(p.chunks_per_split, c1 - c0);
-  if (parts <= 1) return;  // written whole
+  return block_parts(p.chunks_per_split, c1 - c0);
+}
+
+// Log-sum-exp merge of the blocks that the launch before split over the
+// positions: one warp per output row, a float4 a lane, up to 8 parts'
+// loads in flight. The row's parts are found while that launch still runs (it
+// lets this one start only after its own predecessor has completed).
+constexpr int kRowMergeThreads = 256;
+
+__global__ void __launch_bounds__(kRowMergeThreads)
+    extend_merge_kernel(const __grid_constant__ ExtendParams p) {
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long at =
+      (long)blockIdx.x * (kRowMergeThreads / 32) + (threadIdx.x >> 5);
+  const int parts = merge_parts(p, at);
+  pdl_wait();
+  if (parts <= 1) return;  // written whole, or no sequence's row
   const long n = (long)p.rows * p.n_h;
   float M, W;
   float4 acc;
