@@ -1095,13 +1095,15 @@ struct ExtendPlan {
 // a sequence may have more than 256 (one prompt chunk of 1,021 tokens over
 // 32,000, 56 heads: 802 us with pairs, 856 us without, in four waves). Enough blocks fill
 // the SMs by themselves (two waves and more); fewer are split over the
-// positions. Several sequences are split into three waves of parts, were all
-// as long as max_seq_len, so that ragged lengths level out (4 rows of each of
-// 16 sequences of 2K to 14K: 95 us; two waves 103, four 109, eight 119). One
+// positions. Several sequences are split into 8 / 7 waves of parts, were all
+// as long as max_seq_len: ragged ones then fill about one. (Means over eight
+// draws of lengths, us, for 16 sequences of 4 rows to 16K positions, 6 of 9 to
+// 8K, 4 of 175 to 12K, 3 of 30 to 32K: 105, 36, 198, 99; one wave 115, 39,
+// 198, 101; two waves 106, 46, 209, 109; three 106, 46, 221, 115.) One
 // sequence's blocks are about equally long, and the number of parts whose
-// last wave ends first is taken (the chunk above: 3 waves of halves, 726 us;
+// last wave ends first is taken (the chunk above: 3 waves of halves, 722 us;
 // thirds, in 4.4 waves, 802). A choice by the lengths themselves, on the
-// device, cost every CTA 1 to 4 us and found no better parts.
+// device, cost every CTA 1 to 4 us.
 ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
                        int max_rows, int n_h, int sms) {
   ExtendPlan pl;
@@ -1148,16 +1150,17 @@ ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
     chunks = std::min<long>(
         chunks, ((long)s->window + block_rows / g + ch) / ch + 2);
   const long ctas = (long)pl.blocks * c->n_kv * ctas_per_block;
-  const long want = forced > 0 ? forced : 3L * sms;
+  const long want = forced > 0 ? forced : 8L * sms / 7;
   if (forced > 0 || ctas < 2L * sms) {
     long per = (ctas * chunks + want - 1) / want;
     if (forced <= 0 && s->batch == 1) {
       // a part costs kPartCost chunks beyond its own: its queries, the
       // filling and emptying of the pipeline, its share of the merge
       constexpr long kPartCost = 4;
-      const long most = std::max(1L, 16L * sms / ctas);
       long best = -1;
-      for (long n = 1; n <= most && n <= chunks; ++n) {
+      for (long w = 1; w <= 16; ++w) {  // waves, and the parts that fill them
+        const long n = std::min(w * sms / ctas, chunks);
+        if (n < 1) continue;
         const long each = (chunks + n - 1) / n;
         const long cost =
             (ctas * n + sms - 1) / sms * (each + kPartCost);

@@ -22,14 +22,14 @@
 // their products and exponentials. (With O = P V, pairs on M = 16, and the
 // maxima reduced every chunk, decode at 8 pairs took 806 instructions per 16
 // tokens and ran at a fifth of HBM's rate.) At 32 pairs the tcgen05 kernel is
-// ahead (16 sequences of 4 rows and 8 heads a group over 9,200 positions: 99
+// ahead (16 sequences of 4 rows and 8 heads a group over 9,200 positions: 102
 // us there, 194 us with four tiles of pairs here).
 //
 // Measured: 32 single tokens, 8 kv heads of 8 pairs over 4,600 positions
-// (171 MB), 55 us, of which the merge launch is 8 (the copies and the merge
-// alone: 52 us); 4 kv heads of 16 pairs over 18,400 positions (341 MB), 111
-// us (the copies alone 72 us: there the widening, products and exponentials
-// of 8 warps bind it; 16 warps spill with two tiles of pairs, 12 took 116 us).
+// (171 MB), 46 us (the first bytes arrive after 6, the merge launch takes 5);
+// 4 kv heads of 16 pairs over 18,400 positions (341 MB), 107 us (with no work
+// on them the copies took 72: the widening, products and exponentials of 8
+// warps bind it; 16 warps spill with two tiles of pairs, 12 took 5% longer).
 //
 // A code times its E4M3 scale is exact in f16 (6 significand bits). Queries
 // are bf16; each (row, head) is scaled by a power of two so that its largest

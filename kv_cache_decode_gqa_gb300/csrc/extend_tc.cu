@@ -26,17 +26,17 @@
 // swizzled tiles that both products read. Raw rows come through a ring of
 // bulk copies, so that the widening never waits for HBM.
 //
-// Measured: 1,021 rows over 32,000 positions, 56 heads of 8 kv heads, in 726
-// us (1,311 TFLOP/s, 68% of cuBLAS's bf16 rate); whole prompts of 7,001 rows
-// in two sequences, 64 heads, in 426 us; 4 rows of each of 16 sequences over
-// 8,700 positions (160 MB) in 95 us. In a less even split (797 us) the first
+// Measured: 1,021 rows over 32,000 positions, 56 heads of 8 kv heads, in 719
+// us (1,323 TFLOP/s, 68% of cuBLAS's bf16 rate); whole prompts of 7,001 rows
+// in two sequences, 64 heads, in 437 us; 4 rows of each of 16 sequences over
+// 8,700 positions (160 MB) in 102 us. In a less even split (797 us) the first
 // took 627 us without the exponentials, 779 without the widening, 744 without
 // most of the products, 478 with none of them: it is the time from a
 // product's end to the softmax and from P back to the next product that is
 // left, one after the other in each of a tile's two buffers. (Softmax groups
 // that take turns on named barriers: 850 us; one S buffer of 128 positions a
-// tile: the same; K and V handed over by halves of a chunk: the 426 us became
-// 452; a third K tile in the place of an unused second tile: 4% slower for
+// tile: the same; K and V handed over by halves of a chunk: the second took 452
+// us instead of 426; a third K tile in the place of an unused second tile: 4% slower for
 // the few rows, for the ring of raw rows shrinks.)
 //
 // The softmax keeps a reference maximum per pair and moves it only when a
