@@ -35,9 +35,9 @@
 // product's end to the softmax and from P back to the next product that is
 // left, one after the other in each of a tile's two buffers. (Softmax groups
 // that take turns on named barriers: 850 us; one S buffer of 128 positions a
-// tile: the same; K and V handed over by halves of a chunk: the second took 452
-// us instead of 426; a third K tile in the place of an unused second tile: 4% slower for
-// the few rows, for the ring of raw rows shrinks.)
+// tile: the same; K and V handed over by halves of a chunk: the second took
+// 6% longer; a third K tile in the place of an unused second tile: 4% slower
+// for the few rows, for the ring of raw rows shrinks.)
 //
 // The softmax keeps a reference maximum per pair and moves it only when a
 // chunk exceeds it by more than 2^8 (the accumulator is rescaled then, in

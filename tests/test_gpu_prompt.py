@@ -524,6 +524,21 @@ def test_extend_strided_queries_scales_and_no_lse(counts):
     assert none is None and torch.equal(out, out2)
 
 
+@pytest.mark.parametrize("n_h", [64, 128])
+def test_extend_shares_of_very_unequal_sequences(n_h):
+    """One long sequence among empty and short ones: some CTAs' shares hold
+    several units, some none of their chunks."""
+    g = _gen(43)
+    lens = [0, 1, 9000, 64, 63, 0, 130, 2, 65] + [1] * 15
+    counts = [1] * len(lens)
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 8, 64, "mxfp4")
+    q = _randn(g, len(lens), n_h, D)
+    out, lse = K.gqa_extend(c, bt, _i32(lens), 9000, q)
+    _check(out, lse, _attend_ref(c, bt, lens, counts, q))
+    assert K.device_error() == 0
+
+
 @pytest.mark.parametrize("counts,n_h", [([3], 8), ([30], 8), ([120], 8)])
 def test_extend_nan_and_infinite_queries_stay_in_their_rows(counts, n_h):
     g = _gen(41)
