@@ -159,9 +159,11 @@ kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
  *   lse       device fp32 [rows][n_h] or NULL
  *   workspace at least kvd_extend_workspace_size() bytes, 256-byte aligned
  *             (NULL when that is 0); see "Workspace" in kvd.h
- * Rows from row_start[batch] on are left as they were. A sequence whose
- * row_start entries descend (or follow a descent), pass q->rows or are more
- * than max_rows apart is skipped and flagged KVD_DEVERR_LEN. Scores and sums
+ * Rows from row_start[batch] on are left as they were. A row list is followed
+ * up to its first descent; the sequence whose entries descend and all behind
+ * it are skipped (their rows are left as they were), and so is a sequence
+ * that starts below 0, passes q->rows or has more than max_rows rows; each is
+ * flagged KVD_DEVERR_LEN and the others' rows are right. Scores and sums
  * in fp32; the queries enter the first product as f16 with a power-of-two
  * scale per (row, head), the probabilities enter the second as f16. A query
  * that is not finite stays in its own (row, head). The writing calls store

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
   WorkPartition &wp = *reinterpret_cast<WorkPartition *>(smem + C::WP_OFF);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
   uint64_t *empty = full + C::NS;
-  __shared__ int s_len_err;
+  __shared__ int s_len_err, s_list_end;
   __shared__ volatile int s_abort, s_issued, s_producer_done;
 
   const int G = p.n_h / p.n_kv;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
     s_producer_done = 0;
   }
   __syncthreads();
-  build_rows_partition(wp, p, &s_len_err, CH, n_units, p.gap);
+  build_rows_partition(wp, p, &s_len_err, &s_list_end, CH, n_units, p.gap);
   const int total = wp.total;
   const int P = p.whole_units ? (int)gridDim.x
                               : min((int)gridDim.x, max(total, 1));
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
   // the rows that see nothing (spread over the CTAs by sequence), and the
   // flags of bad lengths and row lists
   for (int b = c; b < p.batch; b += gridDim.x) {
-    const int n = seq_rows(p, b);
+    const int n = b < s_list_end ? seq_rows(p, b) : 0;
     if (tid == 0 && p.row_start && n == 0 &&
         p.row_start[b] != p.row_start[b + 1])
       report(p.err, DEVERR_LEN);
@@ -646,12 +646,12 @@ __global__ void __launch_bounds__(kRowMergeThreads, 8)
     merge_few_kernel(const __grid_constant__ ExtendParams p, int n_units,
                      int hp, int chunk, int slots) {
   __shared__ WorkPartitionT<NB> wp;
-  __shared__ int s_len_err;
+  __shared__ int s_len_err, s_list_end;
   pdl_trigger();
   // the lengths and row lists are read before the launch before completes:
   // it does not write them, and it lets this one start only after its own
   // predecessor has completed
-  build_rows_partition(wp, p, &s_len_err, chunk, n_units, p.gap);
+  build_rows_partition(wp, p, &s_len_err, &s_list_end, chunk, n_units, p.gap);
   pdl_wait();
   const int total = wp.total;
   if (total == 0) return;

@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *pvdone = pfull + 4;  // [tile]
   uint64_t *qfull = pvdone + 2;
   uint64_t *odone = qfull + 1;
+  // [0] tensor memory's address, [1] first_descent, [2 ..] s_blk
   int *flags = reinterpret_cast<int *>(smem + C::FLAG_OFF);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(flags);
   // this CTA's sequence, its block of it, and the sequence's Seq
@@ -228,37 +229,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int want = item / p.n_kv;
   if (tid == 0) s_blk[0] = -1;
   {
-    int cnt[2], sum = 0;
+    int cnt[2], sum, x, end = p.batch;
     Seq sq[2];
+    while (true) {
+      bool broken = false;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int b = 2 * tid + j;
-      cnt[j] = 0;
-      sq[j] = Seq{0, 0, 0};
-      if (b < p.batch) sq[j] = seq_at(p, b);
-    }
+      for (int j = 0; j < 2; ++j) {
+        const int b = 2 * tid + j;
+        sq[j] = Seq{0, 0, 0};
+        if (b < p.batch) {
+          sq[j] = seq_at(p, b);
+          broken |= b < end && descends(p, b);
+        }
+        if (b >= end) sq[j].n = 0;
+      }
+      sum = 0;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int b = 2 * tid + j;
-      if (b < p.batch) {
+      for (int j = 0; j < 2; ++j) {
+        const int b = 2 * tid + j;
         cnt[j] = (int)(((long)sq[j].n * G + C::ROWS - 1) / C::ROWS);
-        if (blockIdx.x == 0 && blockIdx.y == 0) {
+        if (b < p.batch && blockIdx.x == 0 && blockIdx.y == 0) {
           if (sq[j].n == 0 && p.row_start &&
               p.row_start[b] != p.row_start[b + 1])
             report(p.err, DEVERR_LEN);
           if (p.seq_lens[b] > p.max_seq_len) report(p.err, DEVERR_LEN);
         }
+        sum += cnt[j];
       }
-      sum += cnt[j];
-    }
-    int x = sum;
+      x = sum;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += y;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      if (lane == 31) s_scan[warp] = x;
+      if (!__syncthreads_or(broken)) break;
+      end = first_descent(p, flags + 1);
     }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
     int before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
@@ -908,27 +915,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Parts of output row `at`, 0 where no sequence has it. Reads what the launch
-// before does not write.
-__device__ __forceinline__ int merge_parts(const ExtendParams &p, long at) {
+// Parts of output row `at` (the same for the warp's lanes), 0 where no
+// sequence has it. Reads what the launch before does not write. The row's
+// sequence is looked for 32 at a time, up to the list's first descent: a
+// bisection would lose rows of a list that descends later on.
+__device__ __forceinline__ int merge_parts(const ExtendParams &p, long at,
+                                           int lane) {
   if (at >= (long)p.rows * p.n_h) return 0;
   const int row = (int)at / p.n_h, hh = (int)at - row * p.n_h;  // below 2^31
   const int G = p.n_h / p.n_kv;
   int b = row, r0 = row;
   if (p.row_start) {
-    int lo = 0, hi = p.batch - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.row_start[mid] <= row)
-        lo = mid;
-      else
-        hi = mid - 1;
+    b = -1;
+    for (int i0 = 0; i0 < p.batch && b < 0; i0 += 32) {
+      int x = 0, y = 0;  // an empty sequence past the batch
+      if (i0 + lane < p.batch)
+        x = p.row_start[i0 + lane], y = p.row_start[i0 + lane + 1];
+      const int has = __ffs(__ballot_sync(0xffffffffu, x <= row && row < y));
+      const int down = __ffs(__ballot_sync(0xffffffffu, y < x));
+      if (down && (!has || down < has)) return 0;
+      if (has) {
+        b = i0 + has - 1;
+        r0 = __shfl_sync(0xffffffffu, x, has - 1);
+      }
     }
-    b = lo;
-    r0 = p.row_start[b];
+    if (b < 0) return 0;
   }
   const Seq q = seq_at(p, b);
-  if (row < r0 || row >= r0 + q.n) return 0;  // no sequence's row
+  if (row >= r0 + q.n) return 0;  // the sequence was skipped
   const Block k =
       block_at(p, q, ((row - r0) * G + hh % G) / p.block_rows, G);
   int c0, c1;
@@ -948,7 +962,7 @@ __global__ void __launch_bounds__(kRowMergeThreads)
   const int lane = threadIdx.x & 31;
   const long at =
       (long)blockIdx.x * (kRowMergeThreads / 32) + (threadIdx.x >> 5);
-  const int parts = merge_parts(p, at);
+  const int parts = merge_parts(p, at, lane);
   pdl_wait();
   if (parts <= 1) return;  // written whole, or no sequence's row
   const long n = (long)p.rows * p.n_h;

@@ -50,21 +50,40 @@ __device__ __forceinline__ int row_exponent(uint32_t amax) {
 // ---------------------------------------------------------------------------
 // sequences with several new rows (kvd_gqa_extend)
 // ---------------------------------------------------------------------------
-// New rows of sequence b; 0 for a row list that is not one.
+// A row list is followed up to its first descent: the sequences before it
+// hold disjoint rows whatever the entries are, those from there on could hold
+// another's and are taken to have none.
+
+// New rows of sequence b, which lies before the first descent; 0 where its
+// own entries do not fit the call.
 __device__ __forceinline__ int seq_rows(const ExtendParams &p, int b) {
   if (!p.row_start) return 1;
-  // (three loads at once; a branch between them would chain their latencies)
-  const int rp = p.row_start[max(b - 1, 0)];
   const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
-  // after a descent the rows may be another sequence's
   const bool bad = (r0 < 0) | (r1 < r0) | (r1 > p.rows) |
-                   ((long)r1 - r0 > p.max_rows) | (rp > r0);
+                   ((long)r1 - r0 > p.max_rows);
   return bad ? 0 : r1 - r0;
 }
 
-// First position the rows of sequence b attend to (its visible length is T):
-// the first row's window reaches lowest. A sequence without rows attends to
-// nothing.
+__device__ __forceinline__ bool descends(const ExtendParams &p, int b) {
+  return p.row_start && p.row_start[b + 1] < p.row_start[b];
+}
+
+// The first sequence whose entries descend (the batch if none do), by all
+// threads of the block through the shared word `at`. Lists that descend are
+// the exception: kernels look for any descent on the way (descends) and come
+// here when there is one.
+__device__ __forceinline__ int first_descent(const ExtendParams &p, int *at) {
+  if (threadIdx.x == 0) *at = p.batch;
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x)
+    if (descends(p, b)) atomicMin(at, b);
+  __syncthreads();
+  return *at;
+}
+
+// First position the rows of sequence b (before the first descent) attend to
+// (its visible length is T): the first row's window reaches lowest. A sequence
+// without rows attends to nothing.
 __device__ __forceinline__ int rows_lo(const ExtendParams &p, int b, int T) {
   const int n = seq_rows(p, b);
   if (n == 0) return T;
@@ -83,20 +102,22 @@ __device__ __forceinline__ int rows_first(const ExtendParams &p, int b, int T,
 // build_partition (stream_k.cuh) for these sequences: `units` units each of
 // the chunks of `chunk` positions that the sequence's rows see and of `gap`
 // empty ones behind them, which stand for what a change of units costs the
-// CTA that makes it. Every thread of the block calls it; it ends with a
-// barrier.
+// CTA that makes it. Sequences from the list's first descent, which
+// *list_end receives, have no chunks. Every thread of the block calls it; it
+// ends with a barrier.
 template <int NB>
 __device__ __forceinline__ void build_rows_partition(WorkPartitionT<NB> &wp,
                                                      const ExtendParams &p,
                                                      int *len_error,
-                                                     int chunk, int units,
-                                                     int gap) {
+                                                     int *list_end, int chunk,
+                                                     int units, int gap) {
   const int tid = threadIdx.x, nthreads = blockDim.x;
   __shared__ int warp_tot[32];
   // a run of consecutive sequences a thread, then a scan over the threads
   const int per = (p.batch + nthreads - 1) / nthreads;
   const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
   int local = 0;
+  bool broken = false;
   for (int b = b0; b < b1; ++b) {
     int T = p.seq_lens[b];
     if (T > p.max_seq_len) {
@@ -109,6 +130,7 @@ __device__ __forceinline__ void build_rows_partition(WorkPartitionT<NB> &wp,
     wp.len[b] = T;
     wp.nch[b] = rows > 0 ? (rows + chunk - 1) / chunk + gap : 0;
     local += wp.nch[b] * units;
+    broken |= descends(p, b);
   }
   const int lane = tid & 31, warp = tid >> 5, nwarps = (nthreads + 31) >> 5;
   int x = local;
@@ -118,7 +140,7 @@ __device__ __forceinline__ void build_rows_partition(WorkPartitionT<NB> &wp,
     if (lane >= off) x += y;
   }
   if (lane == 31) warp_tot[warp] = x;
-  __syncthreads();
+  const int any_broken = __syncthreads_or(broken);
   int before = 0, total = 0;
   for (int w = 0; w < nwarps; ++w) {
     if (w < warp) before += warp_tot[w];
@@ -133,8 +155,22 @@ __device__ __forceinline__ void build_rows_partition(WorkPartitionT<NB> &wp,
     wp.units = units;
     wp.total = total;
     wp.pre[p.batch] = total;
+    *list_end = p.batch;
   }
   __syncthreads();
+  if (any_broken) {
+    const int end = first_descent(p, list_end);
+    if (tid == 0) {
+      int at = 0;
+      for (int b = 0; b < p.batch; ++b) {
+        if (b >= end) wp.nch[b] = 0;
+        wp.pre[b] = at;
+        at += wp.nch[b] * units;
+      }
+      wp.total = wp.pre[p.batch] = at;
+    }
+    __syncthreads();
+  }
 }
 
 }  // namespace kvd

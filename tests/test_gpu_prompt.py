@@ -829,3 +829,63 @@ def test_offsets_past_32_bits():
     want, _ = K.rope(plan, pos, x)
     K.rope(plan, pos, rows, q_out=rows)
     assert torch.equal(rows, want)
+
+
+# ---------------------------------------------------------------------------
+# row lists that are none
+# ---------------------------------------------------------------------------
+# lists in units of n rows for four sequences, of 4 n rows in all, and the
+# sequences that are attended: those before the first descent whose own
+# entries fit
+BAD_LISTS = [
+    ([0, 1, 0, 0, 1], [0]),          # the last would take the first's rows
+    ([0, 1, 2, 1, 2], [0, 1]),
+    ([1, 0, 1, 2, 3], []),
+    ([0, 1, 9, 3, 4], [0]),          # past the rows, then a descent
+    ([-1, 1, 2, 3, 4], [1, 2, 3]),
+    ([0, 1, 2, 3, 5], [0, 1, 2]),
+    ([0, 2, 3, 3, 4], [1, 3]),       # two units where one is the bound
+]
+
+
+@pytest.mark.parametrize("units,good", BAD_LISTS)
+@pytest.mark.parametrize("n,lens", [
+    (1, [200, 90, 300, 70]), (2, [7000, 900, 5000, 64]),
+    (4, [200, 90, 300, 70]), (5, [9000, 1000, 2500, 300]),
+    (40, [9000, 1000, 2500, 300]), (70, [900, 80, 200, 300])])
+def test_extend_follows_a_list_to_its_first_descent(units, good, n, lens):
+    g = _gen(53)
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 1, 64, "mxfp4")
+    q = _randn(g, 4 * n, 8, D)
+    out = torch.full((4 * n, 8, D), 9.0, dtype=BF, device="cuda")
+    lse = torch.full((4 * n, 8), 9.0, device="cuda")
+    K.gqa_extend(c, bt, _i32(lens), max(lens), q, _i32([u * n for u in units]),
+                 n, out=out, lse=lse)
+    assert K.device_error() == K.DEVERR_LEN
+    rest = torch.ones(4 * n, dtype=torch.bool, device="cuda")
+    for b in good:
+        r = slice(units[b] * n, units[b + 1] * n)
+        if r.stop > r.start:
+            _check(out[r], lse[r], _attend_ref(
+                c, bt[b:b + 1], lens[b:b + 1], [r.stop - r.start], q[r]))
+        rest[r] = False
+    assert bool((out[rest] == 9).all()) and bool((lse[rest] == 9).all())
+
+
+def test_extend_finds_the_rows_of_many_sequences():
+    """A merge launch over more than 32 sequences, empty ones and padding
+    among them."""
+    g = _gen(57)
+    counts = [0, 3] * 20 + [0] * 30 + [5, 0, 4]
+    lens = [90 * i % 1700 + 5 for i in range(len(counts))]
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 1, 64, "mxfp4")
+    rows = sum(counts)
+    q = _randn(g, rows + 2, 8, D)
+    out = torch.full((rows + 2, 8, D), 9.0, dtype=BF, device="cuda")
+    _, lse = K.gqa_extend(c, bt, _i32(lens), max(lens), q, _starts(counts), 5,
+                          out=out)
+    _check(out, lse, _attend_ref(c, bt, lens, counts, q))
+    assert bool((out[rows:] == 9).all())
+    assert K.device_error() == 0
