@@ -87,7 +87,9 @@ typedef enum kvd_status {
 #define KVD_DEVERR_TIMEOUT 4 /* a bounded wait on a copy gave up               */
 #define KVD_DEVERR_INDEX 8   /* a top-k index >= that sequence's length        */
 #define KVD_DEVERR_LEN 16    /* a sequence length above the block table, or
-                                above the max_seq_len the call was given      */
+                                above the max_seq_len the call was given, or
+                                a row list that does not fit its call
+                                (kvd_prompt.h)                                */
 
 typedef enum kvd_dtype {
   KVD_BF16 = 0,     /* 2-byte bfloat16 elements                              */

@@ -28,6 +28,12 @@ extern "C" {
  * are passed where they lie. Rows `row_start[b] .. row_start[b + 1] - 1`
  * (device int32 [batch + 1], ascending) belong to sequence b; rows from
  * row_start[batch] on are padding: not read, and left as they were.
+ * A sequence that starts below 0 or ends past `rows` is skipped, as if its
+ * rows were padding, and KVD_DEVERR_LEN is set. So it is by a list that
+ * descends somewhere: kvd_kv_write and kvd_kv_read then do nothing (with more
+ * than 2,048 sequences they go on, and which sequence a row is taken for is
+ * unspecified); kvd_gqa_extend skips the sequence whose entries descend and
+ * all behind it.
  */
 typedef struct kvd_rows {
   void *data;
@@ -111,7 +117,7 @@ kvd_status kvd_rope(const kvd_rope_plan *plan, const int32_t *positions,
  * kvd_rope; KVD_ERR_UNSUPPORTED when a head of keys does not fit in shared
  * memory (head_dim above 4096 with rope). A position outside the block
  * table or a bad block id skips that row and sets KVD_DEVERR_POS /
- * KVD_DEVERR_BLOCK.
+ * KVD_DEVERR_BLOCK; for row lists see kvd_rows.
  */
 kvd_status kvd_kv_write(const kvd_cache *cache, const int32_t *block_table,
                         int32_t max_blocks_per_seq, const int32_t *start,
@@ -129,7 +135,7 @@ kvd_status kvd_kv_write(const kvd_cache *cache, const int32_t *block_table,
  *   k_out, v_out rows x n_kv; either may be NULL. 16-byte aligned, strides
  *                multiples of 8
  * Errors as kvd_kv_write. A row whose position or block id is out of range
- * is flagged and left as it was.
+ * is flagged and left as it was; for row lists see kvd_rows.
  */
 kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
                        int32_t max_blocks_per_seq, const int32_t *start,
@@ -159,11 +165,9 @@ kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
  *   lse       device fp32 [rows][n_h] or NULL
  *   workspace at least kvd_extend_workspace_size() bytes, 256-byte aligned
  *             (NULL when that is 0); see "Workspace" in kvd.h
- * Rows from row_start[batch] on are left as they were. A row list is followed
- * up to its first descent; the sequence whose entries descend and all behind
- * it are skipped (their rows are left as they were), and so is a sequence
- * that starts below 0, passes q->rows or has more than max_rows rows; each is
- * flagged KVD_DEVERR_LEN and the others' rows are right. Scores and sums
+ * Rows from row_start[batch] on, and those of sequences that are skipped (see
+ * kvd_rows), are left as they were. A sequence of more than max_rows rows is
+ * skipped as well and flagged KVD_DEVERR_LEN. Scores and sums
  * in fp32; the queries enter the first product as f16 with a power-of-two
  * scale per (row, head), the probabilities enter the second as f16. A query
  * that is not finite stays in its own (row, head). The writing calls store

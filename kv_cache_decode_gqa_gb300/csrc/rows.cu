@@ -123,25 +123,61 @@ __device__ __forceinline__ int seq_of_row(const int32_t *row_start, int batch,
   return r >= row_start[lo] && r < row_start[lo + 1] ? lo : -1;
 }
 
-constexpr long kPadding = -2;  // a row that no sequence owns
-constexpr long kNoSlot = -1;   // a row whose slot is out of range (flagged)
+constexpr long kPadding = -1;   // a row that no sequence owns
+constexpr long kBadPos = -2;    // a position outside the block table
+constexpr long kBadBlock = -3;  // a block id out of range
 
-// First element row of ragged row r's slot (head 0), or one of the above.
+// First element row of ragged row r's slot (head 0), or one of the above. A
+// sequence that starts below 0 or ends past the rows owns none.
 __device__ __forceinline__ long slot_of_row(const RowsParams &p, int r) {
   const int b = seq_of_row(p.row_start, p.batch, r);
   if (b < 0) return kPadding;
-  const long pos = (long)p.start[b] + (r - p.row_start[b]);
-  if (pos < 0 || pos >= (long)p.max_blocks * p.block_size) {
-    report(p.err, DEVERR_POS);
-    return kNoSlot;
-  }
+  const int first = p.row_start[b];
+  if (first < 0 || p.row_start[b + 1] > p.rows) return kPadding;
+  const long pos = (long)p.start[b] + (r - first);
+  if (pos < 0 || pos >= (long)p.max_blocks * p.block_size) return kBadPos;
   const int blk =
       p.block_table[(long)b * p.max_blocks + (int)(pos / p.block_size)];
-  if (blk < 0 || blk >= p.num_blocks) {
-    report(p.err, DEVERR_BLOCK);
-    return kNoSlot;
-  }
+  if (blk < 0 || blk >= p.num_blocks) return kBadBlock;
   return (long)blk * p.n_kv * p.block_size + (int)(pos % p.block_size);
+}
+
+// Row lists up to this long are gone through by every CTA (warps 1 to 7, in up
+// to 10 rounds of loads, beside the first warp's bisections: nothing on the
+// clock), longer ones a share by each: 65,535 entries would cost a CTA more
+// than its rows.
+constexpr int kListChecked = 2048;
+
+// Whether this thread finds that the list descends, which makes bisections
+// meaningless: the call then does nothing. (A second search, for what lies
+// before the descent, costs good lists too: 40 registers in read_kernel instead
+// of 32, 96 to 106 us; as another turn of one loop, 112 to 113.5 us for the
+// turned fp8 write.) Bad entries are flagged once, or by the CTA whose share
+// they are in. The caller's __syncthreads_or shares the answer and the slots.
+__device__ __forceinline__ bool list_descends(const RowsParams &p) {
+  const bool all = p.batch <= kListChecked;
+  const bool flag = !all || (blockIdx.x == 0 && blockIdx.y == 0);
+  bool broken = false;
+  int b = (int)threadIdx.x - 32, step = kThreads - 32;
+  if (b < 0) return false;
+  if (!all) {  // (65,536 CTAs are enough for every list)
+    b = blockIdx.y == 0 && blockIdx.x < 65536u ? b + (int)blockIdx.x * step
+                                               : p.batch;
+    step *= (int)min(gridDim.x, 65536u);
+  }
+#pragma unroll 1
+  for (; b < p.batch; b += step) {
+    const int x = p.row_start[b], y = p.row_start[b + 1];
+    broken |= y < x;
+    if (flag && x != y && (y < x || x < 0 || y > p.rows))
+      report(p.err, DEVERR_LEN);
+  }
+  return broken && all;
+}
+
+__device__ __forceinline__ void report_slot(const RowsParams &p, long slot) {
+  if (slot < kPadding)
+    report(p.err, slot == kBadPos ? DEVERR_POS : DEVERR_BLOCK);
 }
 
 // Threads per row-head: the pieces of one, rounded up to a power of two.
@@ -259,7 +295,11 @@ __global__ void __launch_bounds__(kThreads, 5)
       smem + (rp.on ? (size_t)p.tile * rp.half * 8 + 15 & ~(size_t)15 : 0));
   pdl_trigger();
   pdl_wait();
-  if (WRITE && tid < nr) s_slot[tid] = slot_of_row(p, r0 + tid);
+  bool broken = false;
+  if constexpr (WRITE) {
+    if (tid < nr) s_slot[tid] = slot_of_row(p, r0 + tid);
+    broken = list_descends(p);
+  }
   if (rp.on) {
     for (int i = tid; i < nr * rp.half; i += kThreads) {
       const int r = i / rp.half, pr = i - r * rp.half;
@@ -272,7 +312,12 @@ __global__ void __launch_bounds__(kThreads, 5)
       cs[i] = turn(rp.turns[pr], pos, rp.inverse);
     }
   }
-  __syncthreads();
+  if constexpr (WRITE) {
+    if (__syncthreads_or(broken)) return;
+    if (tid < nr) report_slot(p, s_slot[tid]);
+  } else {
+    __syncthreads();
+  }
   if (rp.on) {
     const int d = p.d;
     const int nrot = VEC ? (rp.adjacent ? rp.half / 4 : rp.half / 8)
@@ -386,7 +431,8 @@ __global__ void __launch_bounds__(kThreads)
   pdl_trigger();
   pdl_wait();
   if (tid < nr) s_slot[tid] = slot_of_row(p, r0 + tid);
-  __syncthreads();
+  if (__syncthreads_or(list_descends(p))) return;
+  if (tid < nr) report_slot(p, s_slot[tid]);
   constexpr int W = DT == DT_MXFP4 ? 16 : 8;
   const int pieces = p.d / W;
   const int L = lanes_for(pieces);
@@ -428,15 +474,23 @@ __global__ void __launch_bounds__(kThreads)
           *reinterpret_cast<uint4 *>(dst + c * 8) =
               make_uint4(o[0], o[1], o[2], o[3]);
         } else {
-          const uint2 u = *reinterpret_cast<const uint2 *>(src + c * 8);
-          const uint32_t g = src[p.d / 2 + c];
-          const float s = f16lo(e4m3x2_to_f16x2((uint16_t)g));
-          uint32_t o[2][4];
-          mxfp4_to_bf16(u.x, s, o[0]);
-          mxfp4_to_bf16(u.y, s, o[1]);
-          uint4 *q = reinterpret_cast<uint4 *>(dst + c * 16);
-          q[0] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-          q[1] = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+          // Words c and c + 8 of the row's 16, so that each store of the lanes
+          // fills whole sectors. (Words 2 c and 2 c + 1: 16-byte stores 32
+          // bytes apart, of which L2 merges what the compiler happens to put
+          // side by side: 24 to 40 million sectors written, 97 to 112 us.)
+          uint32_t u[2], g[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            u[j] = *reinterpret_cast<const uint32_t *>(src + 4 * c + 32 * j);
+            g[j] = src[64 + (c >> 1) + 4 * j];
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t o[4];
+            mxfp4_to_bf16(u[j], f16lo(e4m3x2_to_f16x2((uint16_t)g[j])), o);
+            reinterpret_cast<uint4 *>(dst)[c + 8 * j] =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
         }
       }
     }

@@ -889,3 +889,95 @@ def test_extend_finds_the_rows_of_many_sequences():
     _check(out, lse, _attend_ref(c, bt, lens, counts, q))
     assert bool((out[rows:] == 9).all())
     assert K.device_error() == 0
+
+
+# the same for writes and reads, which do nothing where a list descends
+WRITE_LISTS = [(u, [] if any(b < a for a, b in zip(u, u[1:])) else good)
+               for u, good in BAD_LISTS[:6]] + [([0, 5, 5, 5, 5], []),
+                                                ([-3, -1, 1, 2, 4], [2, 3])]
+
+
+@pytest.mark.parametrize("units,good", WRITE_LISTS)
+@pytest.mark.parametrize("dtype,n,rotate", [
+    ("mxfp4", 1, False), ("bf16", 7, True), ("fp8", 33, False),
+    ("mxfp4", 200, True)])
+def test_write_and_read_flag_bad_lists(units, good, dtype, n, rotate):
+    g = _gen(59)
+    n_kv, bs, starts = 2, 16, [3, 0, 40, 16]
+    bt, blocks = _table(g, [s + 9 * n for s in starts], bs)
+    a = _cache(g, blocks, n_kv, bs, dtype)
+    b = _clone(a)
+    k, v = _randn(g, 4 * n, n_kv, D), _randn(g, 4 * n, n_kv, D)
+    rs = _i32([u * n for u in units])
+    rope, kw = K.rope_plan(D), {}
+    if rotate:
+        pos = torch.arange(4 * n, dtype=torch.int32, device="cuda")
+        q = _randn(g, 4 * n, 4, D)
+        turned, _ = K.rope(rope, pos, q)
+        kw = dict(rope=rope, positions=pos)
+        got = dict(kw, q=q, q_out=torch.full_like(q, 9.0))
+    out = K.kv_write(a, bt, _i32(starts), rs, k, v,
+                     **(got if rotate else {}))
+    assert K.device_error() == K.DEVERR_LEN
+    ko, vo = K.kv_read(a, bt, _i32(starts), rs, 4 * n,
+                       *(torch.full_like(k, 9.0) for _ in range(2)))
+    assert K.device_error() == K.DEVERR_LEN
+    # each good sequence by itself
+    rest = torch.ones(4 * n, dtype=torch.bool, device="cuda")
+    for s in good:
+        r = slice(units[s] * n, units[s + 1] * n)
+        one = (b, bt[s:s + 1].contiguous(), _i32([starts[s]]),
+               _starts([r.stop - r.start]))
+        if rotate:
+            kw["positions"] = pos[r].contiguous()
+            assert torch.equal(out[r], turned[r])
+        K.kv_write(*one, k[r], v[r], **kw)
+        for x, y in zip(K.kv_read(*one, r.stop - r.start), (ko, vo)):
+            assert torch.equal(x, y[r])
+        rest[r] = False
+    assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+    for x in (ko, vo) + ((out,) if rotate else ()):
+        assert bool((x[rest] == 9).all())
+    assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("batch", [257, 2048, 2049, 5000])
+def test_write_and_read_of_many_sequences(batch):
+    """Lists that every CTA checks as a whole and lists that it checks a share
+    of: one token of most sequences, three or none of some."""
+    g = _gen(batch)
+    n_kv, bs = 1, 4
+    counts = [3 if i % 7 == 2 else 0 if i % 11 == 5 else 1
+              for i in range(batch)]
+    rows = sum(counts)
+    bt = torch.randperm(batch, generator=g, device="cuda").to(
+        torch.int32)[:, None].contiguous()
+    c = _cache(g, batch, n_kv, bs, "bf16")
+    want = c.k.clone(), c.v.clone()
+    start = torch.randint(0, 2, (batch,), generator=g, device="cuda")
+    k, v = _randn(g, rows + 1, n_kv, D), _randn(g, rows + 1, n_kv, D)
+    rs = _starts(counts)
+    seq = torch.repeat_interleave(torch.arange(batch, device="cuda"),
+                                  torch.tensor(counts, device="cuda"))
+    at = start[seq] + torch.arange(rows, device="cuda") - rs.long()[seq]
+    for t, x in zip(want, (k, v)):
+        t[bt[seq, 0].long(), :, at] = x[:rows]
+    args = (c, bt, start.to(torch.int32))
+    K.kv_write(*args, rs, k, v)
+    assert torch.equal(c.k, want[0]) and torch.equal(c.v, want[1])
+    ko, vo = K.kv_read(*args, rs, rows)
+    assert torch.equal(ko, k[:rows]) and torch.equal(vo, v[:rows])
+    assert K.device_error() == 0
+    # a descent or an end past the rows, anywhere, is flagged
+    for i, x in ((batch - 1, 0), (batch // 2, rows), (batch, rows + 2),
+                 (1, -1)):
+        bad = rs.clone()
+        bad[i] = x
+        K.kv_write(*args, bad, k, v)
+        assert K.device_error() & K.DEVERR_LEN
+        ko = torch.full_like(k, 9.0)
+        K.kv_read(*args, bad, rows + 1, k_out=ko)
+        assert K.device_error() & K.DEVERR_LEN
+        if batch <= 2048 and i != batch:
+            assert bool((ko == 9).all())
+            assert torch.equal(c.k, want[0]) and torch.equal(c.v, want[1])
