@@ -169,7 +169,9 @@ kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
  * kvd_rows), are left as they were. A sequence of more than max_rows rows is
  * skipped as well and flagged KVD_DEVERR_LEN. Scores and sums
  * in fp32; the queries enter the first product as f16 with a power-of-two
- * scale per (row, head), the probabilities enter the second as f16. A query
+ * scale per (row, head), the probabilities enter the second as f16 with the
+ * largest at 2^7 or above: each is rounded by 2^-11, and n of them that are
+ * 2^-32 of the largest or less lose up to n 2^-32 of the weight. A query
  * that is not finite stays in its own (row, head). The writing calls store
  * finite groups only; where a caller's own bytes hold a NaN scale of V, rows
  * of the same sequence that do not see the position may become NaN as well.

@@ -37,9 +37,12 @@
 // except for elements 2^-29 of the largest and below, and is undone in the
 // fp32 softmax scale. Scores, references and sums are fp32. Exponentials are
 // taken against a reference per pair that moves only when a score passes it
-// by 2^8 (then the accumulators are rescaled, and only then are maxima
-// shared between lanes): they stay below 2^8 and the largest is at least 1,
-// so f16 rounds them by 2^-11, 1/8 of the bf16 output's rounding.
+// by 2^(7 + 8) (then the accumulators are rescaled, the reference set 2^7 below
+// the maximum, and only then are maxima shared between lanes): they stay below
+// 2^15 and the largest is at least 2^7. f16 rounds them by 2^-11, 1/8 of the
+// bf16 output's rounding, and drops those 2^-32 of the largest and below (a
+// million of them hold 2^-12 of the weight; with the reference at the maximum
+// it was 2^-25, and 3%).
 //
 // Work is split as in the other dense decode kernels (stream_k.cuh): one CTA
 // per SM with an equal share of all chunks (and of p.gap empty ones a unit
@@ -57,7 +60,8 @@ namespace {
 constexpr int kD = 128;
 constexpr int kRow = 72;  // bytes of a cached row
 constexpr int kConsBar = 1;    // named barrier of the consumers
-constexpr float kSlack = 8.f;  // log2 units a reference may lag by
+constexpr float kHead = 7.f;   // log2 units a reference lies below the maximum
+constexpr float kSlack = 8.f;  // and may lag by
 
 // HP kv heads and CH positions a chunk, RT tiles of 8 pairs, W warps.
 template <int HP, int CH, int RT, int W>
@@ -535,21 +539,21 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
             }
         }
         // exponents against the references; a first score, or one past its
-        // reference by kSlack, moves them
+        // reference by kHead + kSlack, moves them
         float t[RT][4];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             t[r][q] = fmaf(sc[r][q], sl[r][q & 1], -ref[r][q & 1]);
-            grow |= t[r][q] > (none[r][q & 1] ? -INFINITY : kSlack);
+            grow |= t[r][q] > (none[r][q & 1] ? -INFINITY : kHead + kSlack);
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              float m = fmaxf(sc[r][q], sc[r][2 + q]) * sl[r][q];
+              float m = fmaxf(sc[r][q], sc[r][2 + q]) * sl[r][q] - kHead;
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));

@@ -39,12 +39,13 @@
 // 6% longer; a third K tile in the place of an unused second tile: 4% slower
 // for the few rows, for the ring of raw rows shrinks.)
 //
-// The softmax keeps a reference maximum per pair and moves it only when a
-// chunk exceeds it by more than 2^8 (the accumulator is rescaled then, in
-// tensor memory): P stays below 2^8, exact enough in f16, and the final
-// division by the sum (fp32, of the same exponentials) takes the reference
-// out again. Queries are scaled by a power of two per (row, head) into f16
-// (see extend_few.cu).
+// The softmax keeps a reference per pair, 2^7 below a maximum, and moves it
+// only when a chunk exceeds that maximum by more than 2^8 (the accumulator is
+// rescaled then, in tensor memory): P stays below 2^15 and its largest is at
+// least 2^7, so that f16 drops only what is 2^-32 of it and below (see
+// extend_few.cu), and the final division by the sum (fp32, of the same
+// exponentials) takes the reference out again. Queries are scaled by a power
+// of two per (row, head) into f16 (see extend_few.cu).
 //
 // Warp roles (640 threads, one CTA per SM; registers are moved from the
 // launch's 96 a thread, 61,440, to 128 for the softmax and 72 for the others,
@@ -75,7 +76,8 @@ constexpr int kRaw = kN * kRow;      // raw K (or V) rows of a chunk
 constexpr int kThreads = 640;
 constexpr int kWiden0 = 8, kLoadWarp = 16, kMmaWarp = 17;
 constexpr int kSoftBar = 1;
-constexpr float kSlack = 8.f;        // log2 units the reference may lag by
+constexpr float kHead = 7.f;         // log2 units it lies below the maximum
+constexpr float kSlack = 8.f;        // and may lag by
 
 // CTAS = 1 or 2 CTAs share a block's chunks (2: a cta_group::2 pair).
 // Shared memory: Q tiles, K ring, V ring (2 each), raw ring.
@@ -490,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[g] = max3(mx[g], __uint_as_float(y[i]),
                          __uint_as_float(y[i + 1]));
         }
-        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl;
+        const float top =
+            fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl - kHead;
         const bool grow = top > ref + kSlack;  // from -inf: any score
         if (__any_sync(0xffffffffu, grow)) {
           const float al = grow ? ex2(ref - top) : 1.f;

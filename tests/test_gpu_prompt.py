@@ -981,3 +981,40 @@ def test_write_and_read_of_many_sequences(batch):
         if batch <= 2048 and i != batch:
             assert bool((ko == 9).all())
             assert torch.equal(c.k, want[0]) and torch.equal(c.v, want[1])
+
+
+# ---------------------------------------------------------------------------
+# a flat tail behind one dominant key
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,n_h", [(1, 8), (1, 16), (2, 8), (5, 8), (20, 8),
+                                      (40, 8), (60, 12)])
+def test_extend_keeps_a_flat_tail(rows, n_h):
+    """Position 0 scores 18.7 above every other one (2^-27 of its weight each)
+    and its value is 0, so the outputs are the tail alone: 4,095 positions of
+    one value. With one CTA for all no part has a reference of its own.
+    f16 rounds a probability below its normal range by 2^-25, and the largest
+    is 2^7 or more, so the tail's error is 2^-32 a position, not 2^-25."""
+    g = _gen(141)
+    T = 4096
+    bt, blocks = _table(g, [T], 64)
+    c = _cache(g, blocks, 1, 64, "mxfp4")
+
+    def row(x):
+        bits = np.array([[x] * D], dtype=np.float32).view(np.uint32) >> 16
+        return torch.from_numpy(oracle.mxfp4_encode_rows(
+            bits.astype(np.uint16))).cuda()
+    c.k[:], c.v[:] = row(0.0), row(1.0)
+    c.k[int(bt[0, 0]), :, 0] = row(1.0)
+    c.v[int(bt[0, 0]), :, 0] = row(0.0)
+    q = torch.full((rows, n_h, D), 1.6, device="cuda").to(BF)
+    K.set_tuning(decode_ctas=1)
+    try:
+        out, lse = K.gqa_extend(c, bt, _i32([T]), T, q, _starts([rows]), rows)
+    finally:
+        K.set_tuning()
+    o, l, tol, ltol = _attend_ref(c, bt, [T], [rows], q)
+    v = oracle.mxfp4_rows_to_f64(c.v[int(bt[0, 0]), 0, 1:2].cpu().numpy(), D)
+    tol = tol - (2.0 ** -25 - 2.0 ** -32) * (T - 1) * float(v[0, 0])
+    assert float(tol.max()) < 0.05 * float(o.min())
+    _check(out, lse, (o, l, tol, ltol))
+    assert K.device_error() == 0
