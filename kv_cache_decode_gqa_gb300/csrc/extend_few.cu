@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
   auto pair_range = [&](int b, int j, int &lo_, int &hi_) {
     const int t = j / G, pos = T - un + t;
     const int s_b = p.win_start ? max(p.win_start[b], 0) : 0;
-    lo_ = p.window > 0 ? max(s_b, pos + 1 - p.window) : s_b;
+    lo_ = p.window > 0 ? max(s_b, window_lo(p, pos)) : s_b;
     hi_ = t < un ? max(pos + 1, 0) : 0;
   };
 

@@ -175,7 +175,7 @@ __device__ __forceinline__ Block block_at(const ExtendParams &p, const Seq &q,
   k.f0 = mb * p.block_rows;
   k.f1 = min(k.f0 + p.block_rows, q.n * G);
   const int first = q.T - q.n + k.f0 / G, last = q.T - q.n + (k.f1 - 1) / G;
-  k.lo = p.window > 0 ? max(q.s, first + 1 - p.window) : q.s;
+  k.lo = p.window > 0 ? max(q.s, window_lo(p, first)) : q.s;
   k.hi = max(last + 1, 0);
   return k;
 }
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = q.T - q.n + f / G;
       vhi = max(pos + 1, 0);
       vlo = q.s;
-      if (p.window > 0) vlo = max(vlo, pos + 1 - p.window);
+      if (p.window > 0) vlo = max(vlo, window_lo(p, pos));
     }
     // ---- the pair's query, scaled into f16 (tile t, or both halves' one)
     float sl;

@@ -81,6 +81,12 @@ __device__ __forceinline__ int first_descent(const ExtendParams &p, int *at) {
   return *at;
 }
 
+// First position that the window of a row at position `pos` (negative: a row
+// before the first position) reaches, or some value below 0. Any window fits.
+__device__ __forceinline__ int window_lo(const ExtendParams &p, int pos) {
+  return max(pos + 1, 0) - p.window;
+}
+
 // First position the rows of sequence b (before the first descent) attend to
 // (its visible length is T): the first row's window reaches lowest. A sequence
 // without rows attends to nothing.
@@ -88,7 +94,7 @@ __device__ __forceinline__ int rows_lo(const ExtendParams &p, int b, int T) {
   const int n = seq_rows(p, b);
   if (n == 0) return T;
   int lo = p.win_start ? p.win_start[b] : 0;
-  if (p.window > 0) lo = max(lo, T - n + 1 - p.window);
+  if (p.window > 0) lo = max(lo, window_lo(p, T - n));
   return min(max(lo, 0), T);
 }
 

@@ -1018,3 +1018,19 @@ def test_extend_keeps_a_flat_tail(rows, n_h):
     assert float(tol.max()) < 0.05 * float(o.min())
     _check(out, lse, (o, l, tol, ltol))
     assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 8, 1])
+@pytest.mark.parametrize("counts,lens,n_h", [
+    ([6, 1], [2, 3], 2), ([20, 5], [10, 0], 8), ([60, 9], [50, 70], 8),
+    ([300, 40], [30, 40], 4)])
+def test_extend_windows_of_any_size_with_rows_before_position_0(counts, lens,
+                                                                n_h, window):
+    g = _gen(151)
+    bt, blocks = _table(g, lens, 16)
+    c = _cache(g, blocks, 1, 16, "mxfp4")
+    q = _randn(g, sum(counts), n_h, D)
+    out, lse = K.gqa_extend(c, bt, _i32(lens), max(lens), q, _starts(counts),
+                            max(counts), window=window)
+    _check(out, lse, _attend_ref(c, bt, lens, counts, q, window))
+    assert K.device_error() == 0
