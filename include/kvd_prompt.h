@@ -114,8 +114,8 @@ kvd_status kvd_rope(const kvd_rope_plan *plan, const int32_t *positions,
  *   rope         NULL, or the plan; positions and axis_stride as kvd_rope
  *   q, q_out     only with rope: as kvd_rope, or both NULL
  * No two rows may name the same slot. Errors: those of kvd_kv_append and of
- * kvd_rope; KVD_ERR_UNSUPPORTED when a head of keys does not fit in shared
- * memory (head_dim above 4096 with rope). A position outside the block
+ * kvd_rope; KVD_ERR_UNSUPPORTED when a head of keys and its angles do not fit
+ * in shared memory (with rope: 2 head_dim + 4 d_rot above 204,784 bytes). A position outside the block
  * table or a bad block id skips that row and sets KVD_DEVERR_POS /
  * KVD_DEVERR_BLOCK; for row lists see kvd_rows.
  */

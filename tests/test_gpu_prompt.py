@@ -1034,3 +1034,29 @@ def test_extend_windows_of_any_size_with_rows_before_position_0(counts, lens,
                             max(counts), window=window)
     _check(out, lse, _attend_ref(c, bt, lens, counts, q, window))
     assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("d,d_rot,n_kv", [(2056, 1024, 3), (32768, 1024, 2),
+                                          (100344, 1024, 1), (4104, 64, 9)])
+def test_write_rotates_wide_heads(d, d_rot, n_kv):
+    """Heads that take one key head's shared memory past 40 and 48 KB, up to
+    the limit."""
+    g = _gen(161)
+    rows, bs = 5, 4
+    bt, blocks = _table(g, [rows], bs)
+    a = _cache(g, blocks, n_kv, bs, "bf16", d=d)
+    b = _clone(a)
+    k, v = _randn(g, rows, n_kv, d), _randn(g, rows, n_kv, d)
+    plan = K.rope_plan(d_rot)
+    pos = torch.arange(7, 7 + rows, dtype=torch.int32, device="cuda")
+    wk, _ = K.rope(plan, pos, k)
+    K.kv_write(b, bt, _i32([0]), _starts([rows]), wk, v)
+    K.kv_write(a, bt, _i32([0]), _starts([rows]), k, v, rope=plan,
+               positions=pos)
+    assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+    freqs = [10000.0 ** (-2.0 * i / d_rot) for i in range(d_rot // 2)]
+    ref, mag = _rope_ref(k, freqs, [0] * (d_rot // 2), pos[None], "half",
+                         d_rot, False)
+    tol = HALF_BF16 * ref.abs() + 2.0 ** -19 * mag
+    assert bool(((wk.cpu().double() - ref).abs() <= tol).all())
+    assert K.device_error() == 0

@@ -285,3 +285,13 @@ def test_calls_take_a_stream_keyword():
     for f in (K.rope, K.kv_write, K.kv_read, K.gqa_extend):
         assert "stream" in inspect.signature(f).parameters
         assert f.__doc__
+
+
+def test_write_rotates_heads_that_fit_in_shared_memory(lib):
+    """2 head_dim + 4 d_rot bytes up to 204,784 (nothing to do: no rows)."""
+    for d_rot, most in ((128, 102136), (1024, 100344)):
+        assert 2 * most + 4 * d_rot == 204784
+        for d, want in ((most, 0), (most + 8, 3)):
+            e = _rows(rows=0, head_stride=d, row_stride=8 * d)
+            assert _write(lib, _cache(dtype=0, head_dim=d), k=e, v=e,
+                          plan=_plan(d_rot=d_rot), pos=FAKE) == want
