@@ -642,29 +642,39 @@ def kv_read(cache, block_table, start, row_start, rows, k_out=None,
 
 
 def extend_workspace_size(cache, block_table, seq_lens, max_seq_len, rows,
-                          n_h, max_rows=1, window=0):
-    """Workspace bytes of a gqa_extend call (kvd_extend_workspace_size)."""
+                          n_h, max_rows=None, window=0):
+    """Workspace bytes of a gqa_extend call (kvd_extend_workspace_size) with
+    these arguments; without ``max_rows``, enough for a call without it, with
+    row_start or not."""
     import torch
     c = cache.struct()
     s = _seqs(block_table, seq_lens, max_seq_len, window=window)
-    out = ctypes.c_size_t(0)
+    rows = int(rows)
+    bounds = [int(max_rows)] if max_rows is not None else [rows]
+    if max_rows is None and rows == s.batch:
+        bounds.append(1)
+    most = 0
     with torch.cuda.device(block_table.device):
-        check(lib().kvd_extend_workspace_size(
-            ctypes.byref(c), ctypes.byref(s), int(rows), int(max_rows), n_h,
-            ctypes.byref(out)))
-    return out.value
+        for bound in bounds:
+            out = ctypes.c_size_t(0)
+            check(lib().kvd_extend_workspace_size(
+                ctypes.byref(c), ctypes.byref(s), rows, bound, n_h,
+                ctypes.byref(out)))
+            most = max(most, out.value)
+    return most
 
 
 @_in_context
 def gqa_extend(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
-               max_rows=1, scale=None, out=None, lse=None, workspace=None,
+               max_rows=None, scale=None, out=None, lse=None, workspace=None,
                want_lse=True, window=0, window_start=None):
     """Attention of new tokens over an MXFP4 cache that holds them: q
     [rows][n_h][head_dim] bf16 (contiguous vectors) -> (out [rows][n_h]
     [head_dim] bf16, lse [rows][n_h] fp32). Rows row_start[b] ..
     row_start[b + 1] - 1 (int32 [batch + 1]) are the last positions of
-    sequence b, at most ``max_rows`` of them; without row_start row b is
-    sequence b's one new token. Each row attends to the positions up to its
+    sequence b, at most ``max_rows`` of them (it chooses the kernel: the
+    smallest bound is the fastest; None: all rows, which fits any list);
+    without row_start row b is sequence b's one new token. Each row attends to the positions up to its
     own, within ``window`` and from ``window_start`` if given. Rows of new
     outputs that no sequence owns are not initialised."""
     import torch
@@ -672,7 +682,10 @@ def gqa_extend(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
     qs = _rows3(q, "q", width=d)
     c = cache.struct()
     seqs = _seqs(block_table, seq_lens, max_seq_len, 0, window, window_start)
-    rows, n_h, max_rows = qs.rows, qs.heads, int(max_rows)
+    rows, n_h = qs.rows, qs.heads
+    if max_rows is None:
+        max_rows = 1 if row_start is None else rows
+    max_rows = int(max_rows)
     if row_start is not None:
         _need(row_start, "row_start", torch.int32, seqs.batch + 1)
     if out is not None:

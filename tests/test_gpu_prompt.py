@@ -1060,3 +1060,28 @@ def test_write_rotates_wide_heads(d, d_rot, n_kv):
     tol = HALF_BF16 * ref.abs() + 2.0 ** -19 * mag
     assert bool(((wk.cpu().double() - ref).abs() <= tol).all())
     assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("counts", [[1, 1, 1], [2, 1, 0], [4, 9, 1],
+                                    [60, 1, 30]])
+def test_extend_without_a_bound_on_the_rows(counts):
+    """A row list without max_rows: every row is attended, in the workspace
+    that extend_workspace_size gives without it."""
+    g = _gen(171)
+    lens = [900, 64, 3000]
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 1, 64, "mxfp4")
+    rows = sum(counts)
+    q = _randn(g, rows, 8, D)
+    ref = _attend_ref(c, bt, lens, counts, q)
+    args = (c, bt, _i32(lens), max(lens))
+    ws = torch.empty(K.extend_workspace_size(*args, rows, 8),
+                     dtype=torch.uint8, device="cuda")
+    for kw in ({}, dict(workspace=ws)):
+        out = torch.full((rows, 8, D), 9.0, dtype=BF, device="cuda")
+        _, lse = K.gqa_extend(*args, q, _starts(counts), out=out, **kw)
+        assert K.device_error() == 0
+        _check(out, lse, ref)
+    if rows == 3 and max(counts) == 1:      # and without a list
+        out, lse = K.gqa_extend(*args, q, workspace=ws)
+        _check(out, lse, ref)
