@@ -161,7 +161,8 @@ kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
  *             of 8; head h reads KV head h / (n_h / n_kv)
  *   scale     softmax scale; <= 0 selects 1/sqrt(head_dim)
  *   out       device bf16 [rows][n_h][head_dim], 16-byte aligned; must not
- *             overlap q
+ *             overlap q (else KVD_ERR_SHAPE: parts of a row block read q while
+ *             others write)
  *   lse       device fp32 [rows][n_h] or NULL
  *   workspace at least kvd_extend_workspace_size() bytes, 256-byte aligned
  *             (NULL when that is 0); see "Workspace" in kvd.h

@@ -675,8 +675,9 @@ def gqa_extend(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
     sequence b, at most ``max_rows`` of them (it chooses the kernel: the
     smallest bound is the fastest; None: all rows, which fits any list);
     without row_start row b is sequence b's one new token. Each row attends to the positions up to its
-    own, within ``window`` and from ``window_start`` if given. Rows of new
-    outputs that no sequence owns are not initialised."""
+    own, within ``window`` and from ``window_start`` if given. ``out`` must not
+    overlap q. Rows of new outputs that no sequence owns are not
+    initialised."""
     import torch
     d = cache.head_dim
     qs = _rows3(q, "q", width=d)

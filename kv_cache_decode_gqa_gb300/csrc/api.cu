@@ -958,6 +958,26 @@ kvd_status check_rows(const kvd_rows *r, int d, bool out, const char *what,
   return KVD_OK;
 }
 
+// Whether any vector of r (d wide) has bytes in [p, p + bytes). Vectors are
+// gone through only where the span of all of them meets that range.
+bool rows_meet(const kvd_rows *r, int d, const void *p, size_t bytes) {
+  const uintptr_t base = reinterpret_cast<uintptr_t>(r->data);
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + bytes;
+  const auto meet = [&](uintptr_t at, int64_t last) {  // to element last + d
+    return at < hi && at + 2 * (uintptr_t)(last + d) > lo;
+  };
+  const int64_t rs = r->row_stride, hs = r->head_stride;
+  const int64_t heads = (r->heads - 1) * hs;
+  if (!meet(base, (r->rows - 1) * rs + heads)) return false;
+  for (int32_t i = 0; i < r->rows; ++i) {
+    const uintptr_t row = base + 2 * (uintptr_t)(i * rs);
+    if (!meet(row, heads)) continue;
+    for (int32_t h = 0; h < r->heads; ++h)
+      if (meet(row + 2 * (uintptr_t)(h * hs), 0)) return true;
+  }
+  return false;
+}
+
 bool rows_aligned16(const kvd_rows *r) {
   return aligned(r->data, 16) && r->row_stride % 8 == 0 &&
          r->head_stride % 8 == 0;
@@ -1421,6 +1441,9 @@ kvd_status kvd_gqa_extend(const kvd_cache *cache, const kvd_seqs *seqs,
                 "q's strides multiples of 8");
   if (seqs->batch == 0 || q->rows == 0 || max_rows == 0) return ok();
   if (!out) return fail(KVD_ERR_NULL, "gqa_extend: out required");
+  if (rows_meet(q, cache->head_dim, out,
+                (size_t)q->rows * q->heads * cache->head_dim * 2))
+    return fail(KVD_ERR_SHAPE, "gqa_extend: out overlaps q");
   const DeviceInfo *d = nullptr;
   st = device_info(&d);
   if (st != KVD_OK) return st;

@@ -1085,3 +1085,28 @@ def test_extend_without_a_bound_on_the_rows(counts):
     if rows == 3 and max(counts) == 1:      # and without a list
         out, lse = K.gqa_extend(*args, q, workspace=ws)
         _check(out, lse, ref)
+
+
+def test_extend_outputs_beside_the_queries():
+    """Outputs in the gaps of strided queries are no overlap; in place is
+    refused and leaves the queries alone."""
+    g = _gen(181)
+    lens, n_h = [70, 40], 8
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 1, 64, "mxfp4")
+    arena = _randn(g, 9, n_h, D)
+    args = (c, bt, _i32(lens), max(lens))
+    q = arena[1:9:6]                                    # rows 1 and 7
+    want, wl = K.gqa_extend(*args, q.contiguous())
+    for at in (2, 5):
+        out, lse = K.gqa_extend(*args, q, out=arena[at:at + 2])
+        assert torch.equal(arena[at:at + 2], want) and torch.equal(lse, wl)
+    before = arena.clone()
+    for at in (0, 1, 6, 7):
+        with pytest.raises(K.KvdError, match="overlaps"):
+            K.gqa_extend(*args, q, out=arena[at:at + 2])
+    apart = arena[:2].transpose(0, 1).contiguous().transpose(0, 1)
+    with pytest.raises(K.KvdError, match="overlaps"):
+        K.gqa_extend(*args, apart, out=apart.transpose(0, 1).view(
+            2, n_h, D))
+    assert torch.equal(arena, before)

@@ -295,3 +295,18 @@ def test_write_rotates_heads_that_fit_in_shared_memory(lib):
             e = _rows(rows=0, head_stride=d, row_stride=8 * d)
             assert _write(lib, _cache(dtype=0, head_dim=d), k=e, v=e,
                           plan=_plan(d_rot=d_rot), pos=FAKE) == want
+
+
+def test_extend_refuses_outputs_over_the_queries(lib):
+    """Six rows of 64 heads: in place, and a few bytes shared at either end;
+    strided queries of which one vector is met."""
+    n = 6 * 64 * 128 * 2
+    at = FAKE + 0x400000                                # where _rows() lie
+    row = 64 * 128
+    wide = _rows(64, rows=2, row_stride=8 * row)
+    apart = _rows(64, rows=1, head_stride=128 * 65)
+    for q, out in ((_rows(64), at), (_rows(64), at + n - 16),
+                   (_rows(64), at - n + 16), (wide, at + 2 * 7 * row),
+                   (wide, at + 2 * 8 * row), (apart, at + 2 * 128 + 16),
+                   (apart, at + 2 * 128 * 65 * 63)):
+        assert _extend(lib, q=q, out=out) == 2 and _says(lib, "overlaps")
