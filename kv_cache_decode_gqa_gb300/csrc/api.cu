@@ -1136,7 +1136,7 @@ ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
                              s->max_seq_len, sms);
     pl.f = f;
     const long units = (long)s->batch * (c->n_kv / f.hp);
-    long unit_chunks = (s->max_seq_len + f.chunk - 1) / f.chunk;
+    long unit_chunks = ((long)s->max_seq_len + f.chunk - 1) / f.chunk;
     const long chunks = units * unit_chunks;
     if (s->window > 0)
       unit_chunks = std::min<long>(
@@ -1165,7 +1165,7 @@ ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
       (int)((pairs + (long)std::min(s->batch, rows) * (block_rows - 1)) /
             block_rows);
   const int ch = kvd::kExtendChunk;
-  long chunks = (s->max_seq_len + ch - 1) / ch;
+  long chunks = ((long)s->max_seq_len + ch - 1) / ch;
   if (s->window > 0)
     chunks = std::min<long>(
         chunks, ((long)s->window + block_rows / g + ch) / ch + 2);

@@ -1110,3 +1110,24 @@ def test_extend_outputs_beside_the_queries():
         K.gqa_extend(*args, apart, out=apart.transpose(0, 1).view(
             2, n_h, D))
     assert torch.equal(arena, before)
+
+
+@pytest.mark.parametrize("rows", [1, 20, 60])
+def test_extend_with_the_largest_length_bound(rows):
+    """max_seq_len of 2^31 - 1 plans like one a few chunks below it, and the
+    call is right."""
+    g = _gen(191)
+    bs, T = 2 ** 20, 5000
+    k, v = (torch.zeros((1, 1, bs, 72), dtype=torch.uint8, device="cuda")
+            for _ in range(2))
+    small = _cache(g, 1, 1, 8192, "mxfp4")
+    k[:, :, :8192], v[:, :, :8192] = small.k, small.v
+    c = K.PagedCache(k, v, bs, 1, D, "mxfp4")
+    bt = torch.zeros((1, 2048), dtype=torch.int32, device="cuda")
+    top = 2 ** 31 - 1
+    assert K.extend_workspace_size(c, bt, _i32([T]), top, rows, 8, rows) == \
+        K.extend_workspace_size(c, bt, _i32([T]), top - 4096, rows, 8, rows) > 0
+    q = _randn(g, rows, 8, D)
+    out, lse = K.gqa_extend(c, bt, _i32([T]), top, q, _starts([rows]), rows)
+    _check(out, lse, _attend_ref(small, _i32([[0]]), [T], [rows], q))
+    assert K.device_error() == 0
