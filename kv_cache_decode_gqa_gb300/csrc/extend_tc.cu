@@ -379,11 +379,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_all = [&](uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
   };
-  // Arrivals that the MMA warp (CTA 0's in a pair) waits for, and commits
-  // that the roles of every CTA wait for.
+  // Arrivals that the MMA warps (CTA 0's in a pair) wait for, and commits that
+  // the roles of every CTA wait for. CTA 1's tiles in shared memory (Q, K, V)
+  // are released at cluster scope, ahead of their use: 434 to 439 us for the
+  // prompts, 699 to 701 for the chunk. P, on the way from one product to the
+  // next, lies in tensor memory and needs the threads' order only (at cluster
+  // scope as well: 537 and 970 us; relayed by CTA 1's own MMA warps: 477 and
+  // 842; without pairs: 475 and 792. By a release in CTA 0, which needs none
+  // either: 451 and 726).
   auto arrive_mma = [&](uint64_t *bar) {
+    if (PAIR && rank != 0)
+      mbar_arrive_remote(cluster_saddr(bar, 0));
+    else
+      mbar_arrive(bar);
+  };
+  auto arrive_p = [&](uint64_t *bar) {
     if constexpr (PAIR)
-      mbar_arrive_remote_cta(cluster_saddr(bar, 0));
+      mbar_arrive_remote_relaxed(cluster_saddr(bar, 0));
     else
       mbar_arrive(bar);
   };
@@ -550,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_mma(&pfull[2 * t + buf]);
+      if (lane == 0) arrive_p(&pfull[2 * t + buf]);
     }
     // ---- epilogue --------------------------------------------------------
     const bool ok = wait_all(odone, 0);
@@ -822,12 +834,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool done = bar == nullptr;
           int i = 0;
           for (; i < (1 << 24); ++i) {
-            done = done || mbar_test_wait(bar, par);
+            done = done || mbar_test_scope<PAIR>(bar, par);
             if (__all_sync(0xffffffffu, done)) break;
           }
           if (i == (1 << 24)) return false;
         }
-        return wait_all(b0, p0);
+        return __all_sync(0xffffffffu, mbar_wait_scope<PAIR>(b0, p0));
       };
       // One warp a tile: a wait costs 300 cycles and more here even when its
       // phase is over (the shared memory pipe is busy with the tiles), and

@@ -7,14 +7,37 @@
 
 namespace kvd {
 
-// One arrival on the mbarrier at `addr` in another CTA of the cluster (or
-// this one, from cluster_saddr) with release semantics at CTA scope only: for
-// arrivals that publish data of this SM (its shared memory after a proxy fence, its tensor
-// memory after a wait) to work that the other CTA's thread starts on this SM.
-// 100 ns one way where the cluster-scope release took 360 (idle SM).
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr)
-               : "memory");
+// One arrival on the mbarrier at `addr` in another CTA of the cluster (or this
+// one, from cluster_saddr) that orders no memory: for arrivals that publish
+// tensor memory, whose accesses tcgen05.wait and tcgen05.fence order with any
+// synchronisation of the threads. mbar_arrive_remote is for shared memory.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t addr) {
+  asm volatile(
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+      : "memory");
+}
+
+// mbar_test_wait and mbar_wait; CLUSTER: with acquire semantics at cluster
+// scope, for barriers that other CTAs of the cluster arrive on.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_test_scope(uint64_t *bar,
+                                                uint32_t parity) {
+  if constexpr (!CLUSTER) return mbar_test_wait(bar, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;"
+      "\n\tselp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_wait_scope(uint64_t *bar,
+                                                uint32_t parity) {
+  if constexpr (!CLUSTER) return mbar_wait(bar, parity);
+  return mbar_test_scope<true>(bar, parity) || mbar_wait_cluster(bar, parity);
 }
 
 // The eight E2M1 codes of a word (first code in the low nibble) to four f16
