@@ -185,11 +185,13 @@ typedef struct kvd_cache {
  * position, seq_lens[b] - 1, may be written by that kernel (a kv_append of
  * this step), or by kvd_gqa_append_decode itself. That holds in a decode
  * step, where older rows were appended by earlier steps; it does not hold
- * right after kvd_copy_blocks, which writes older rows. kvd_gqa_decode,
- * kvd_gqa_append_decode and kvd_indexer_topk may then start copying those
- * rows while that kernel finishes (the query rows, and everything written,
- * still wait for it); the CUDA-core decode kernel (query groups of 1, 2 or
- * 4) and the indexer's scores do. Other calls ignore the flag.
+ * right after kvd_copy_blocks, which writes older rows, nor after a
+ * kvd_kv_write (kvd_prompt.h) of more than each sequence's newest position.
+ * kvd_gqa_decode, kvd_gqa_append_decode and kvd_indexer_topk may then start
+ * copying those rows while that kernel finishes (the query rows, and
+ * everything written, still wait for it); the CUDA-core decode kernel (query
+ * groups of 1, 2 or 4) and the indexer's scores do. Other calls ignore the
+ * flag.
  */
 #define KVD_SEQS_STABLE 1
 #define KVD_SEQS_PREFIX_READY 2
