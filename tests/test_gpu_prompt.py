@@ -1131,3 +1131,31 @@ def test_extend_with_the_largest_length_bound(rows):
     out, lse = K.gqa_extend(c, bt, _i32([T]), top, q, _starts([rows]), rows)
     _check(out, lse, _attend_ref(small, _i32([[0]]), [T], [rows], q))
     assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("pairing", ["half", "adjacent"])
+def test_rope_angles_at_any_position(pairing):
+    """At positions over the whole int32 range the rotation is the one by
+    position times the plan's 64-bit fraction of a turn, formed in exact
+    integers here; tolerance as in test_rope, whatever the position."""
+    d = 128
+    plan = K.rope_plan(d, theta=500000.0, pairing=pairing)
+    turns = [int(x) % 2 ** 64 for x in plan.turns.tolist()]
+    g = _gen(201)
+    p = [0, 1, -1, 2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, -2 ** 29 - 7,
+         123456789, 16777217, -99999999]
+    x = _randn(g, len(p), 3, d)
+    y, _ = K.rope(plan, _i32([p]), x)
+    frac = np.array([[(t * a % 2 ** 64) / 2.0 ** 64 for t in turns]
+                     for a in p])[:, None]
+    c, s = (torch.from_numpy(f(2 * np.pi * frac)) for f in (np.cos, np.sin))
+    i = torch.arange(d // 2)
+    a, b = (i, i + d // 2) if pairing == "half" else (2 * i, 2 * i + 1)
+    v = x.double().cpu()
+    ref, mag = v.clone(), v.clone()
+    ref[..., a] = v[..., a] * c - v[..., b] * s
+    ref[..., b] = v[..., b] * c + v[..., a] * s
+    mag[..., a] = mag[..., b] = v[..., a].abs() + v[..., b].abs()
+    tol = HALF_BF16 * ref.abs() + 2.0 ** -19 * mag
+    assert bool(((y.cpu().double() - ref).abs() <= tol).all())
+    assert K.device_error() == 0
