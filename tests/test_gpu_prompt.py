@@ -1159,3 +1159,72 @@ def test_rope_angles_at_any_position(pairing):
     tol = HALF_BF16 * ref.abs() + 2.0 ** -19 * mag
     assert bool(((y.cpu().double() - ref).abs() <= tol).all())
     assert K.device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# many sequences, wide groups of single tokens, two calls at once
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("batch,n_h,n_kv,counts,window", [
+    (65, 8, 1, 1, 0), (300, 16, 2, 1, 0), (1024, 16, 1, 1, 0),
+    (1024, 3, 1, 2, 40), (200, 8, 1, 4, 0), (1024, 16, 1, 2, 0),
+    (1000, 40, 1, 1, 0)])
+def test_extend_many_sequences(batch, n_h, n_kv, counts, window):
+    """Up to 1,024 sequences by either kernel, a tenth of them empty, one of
+    them long."""
+    g = _gen(batch + n_h)
+    lens = [0 if i % 10 == 3 else 7 * i % 90 + 1 for i in range(batch)]
+    lens[batch // 2] = 6000
+    n = [0 if i % 9 == 4 else counts for i in range(batch)]
+    if counts == 1:
+        n = [1] * batch
+    bt, blocks = _table(g, lens, 32)
+    c = _cache(g, blocks, n_kv, 32, "mxfp4")
+    q = _randn(g, sum(n), n_h, D)
+    args = (c, bt, _i32(lens), 6000, q)
+    ref = _attend_ref(c, bt, lens, n, q, window)
+    out, lse = K.gqa_extend(*args, _starts(n), counts, window=window)
+    _check(out, lse, ref)
+    if counts == 1:
+        a, b = K.gqa_extend(*args, window=window)
+        assert torch.equal(a, out) and torch.equal(b, lse)
+    assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("group", [17, 24, 100, 128])
+def test_extend_single_tokens_of_wide_groups(group):
+    """One token a sequence without a row list on tcgen05."""
+    g = _gen(211 + group)
+    lens = [5000, 1, 0, 129, 700]
+    bt, blocks = _table(g, lens, 64)
+    c = _cache(g, blocks, 2, 64, "mxfp4")
+    q = _randn(g, 5, 2 * group, D)
+    for window in (0, 60):
+        out, lse = K.gqa_extend(c, bt, _i32(lens), 5000, q, window=window)
+        _check(out, lse, _attend_ref(c, bt, lens, [1] * 5, q, window))
+    assert K.device_error() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Prompts, drafts and single tokens of two models, interleaved on two
+    streams with nothing between them, give each call's own result."""
+    g = _gen(221)
+    jobs = []
+    for counts, n_kv in (([300, 200], 2), ([4, 4], 8), ([1, 1], 8)):
+        for _ in range(2):
+            lens = [9000, 5000]
+            bt, blocks = _table(g, lens, 64)
+            c = _cache(g, blocks, n_kv, 64, "mxfp4")
+            q = _randn(g, sum(counts), 8 * n_kv, D)
+            args = (c, bt, _i32(lens), 9000, q, _starts(counts), max(counts))
+            jobs.append((args, K.gqa_extend(*args)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for i, (args, _) in enumerate(jobs):
+            got.append((i, K.gqa_extend(*args, stream=streams[i & 1])))
+    torch.cuda.synchronize()
+    for i, (out, lse) in got:
+        assert torch.equal(out, jobs[i][1][0])
+        assert torch.equal(lse, jobs[i][1][1])
+    assert K.device_error() == 0
