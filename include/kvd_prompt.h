@@ -115,9 +115,9 @@ kvd_status kvd_rope(const kvd_rope_plan *plan, const int32_t *positions,
  *   q, q_out     only with rope: as kvd_rope, or both NULL
  * No two rows may name the same slot. Errors: those of kvd_kv_append and of
  * kvd_rope; KVD_ERR_UNSUPPORTED when a head of keys and its angles do not fit
- * in shared memory (with rope: 2 head_dim + 4 d_rot above 204,784 bytes). A position outside the block
- * table or a bad block id skips that row and sets KVD_DEVERR_POS /
- * KVD_DEVERR_BLOCK; for row lists see kvd_rows.
+ * in shared memory (with rope: 2 head_dim + 4 d_rot above 204,784 bytes). A
+ * position outside the block table or a bad block id skips that row and sets
+ * KVD_DEVERR_POS / KVD_DEVERR_BLOCK; for row lists see kvd_rows.
  */
 kvd_status kvd_kv_write(const kvd_cache *cache, const int32_t *block_table,
                         int32_t max_blocks_per_seq, const int32_t *start,
@@ -156,7 +156,11 @@ kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
  *   row_start device int32 [batch + 1] (see kvd_rows), or NULL: row b is
  *             the one new token of sequence b
  *   max_rows  host: an upper bound on every n_b, 1 without row_start. It
- *             chooses the kernel and sizes the workspace
+ *             chooses the kernel, for all sequences alike, and sizes the
+ *             workspace. Single tokens beside a long chunk are faster in a
+ *             call of their own (1,021 rows over 32,000 positions and 32 single
+ *             tokens over 8,192, 64 heads: 1,270 us in one call, 1,018 and 76
+ *             in two)
  *   q         rows x n_h, head_dim wide, 16-byte aligned, strides multiples
  *             of 8; head h reads KV head h / (n_h / n_kv)
  *   scale     softmax scale; <= 0 selects 1/sqrt(head_dim)

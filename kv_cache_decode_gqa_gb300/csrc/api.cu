@@ -1113,17 +1113,19 @@ struct ExtendPlan {
 // Few (row, head) pairs a kv head (at most 16): the stream-K kernel with one
 // CTA per SM. Else blocks of 256 pairs a CTA, or of 512 a pair of CTAs where
 // a sequence may have more than 256 (one prompt chunk of 1,021 tokens over
-// 32,000, 56 heads: 802 us with pairs, 856 us without, in four waves). Enough blocks fill
-// the SMs by themselves (two waves and more); fewer are split over the
-// positions. Several sequences are split into 8 / 7 waves of parts, were all
-// as long as max_seq_len: ragged ones then fill about one. (Means over eight
-// draws of lengths, us, for 16 sequences of 4 rows to 16K positions, 6 of 9 to
-// 8K, 4 of 175 to 12K, 3 of 30 to 32K: 105, 36, 198, 99; one wave 115, 39,
-// 198, 101; two waves 106, 46, 209, 109; three 106, 46, 221, 115.) One
-// sequence's blocks are about equally long, and the number of parts whose
-// last wave ends first is taken (the chunk above: 3 waves of halves, 722 us;
-// thirds, in 4.4 waves, 802). A choice by the lengths themselves, on the
-// device, cost every CTA 1 to 4 us.
+// 32,000, 56 heads: 698 us with pairs, 792 without). Blocks that make two waves
+// and more are not split over the positions. Of several sequences, fewer are
+// split into 8 / 7 waves of parts, were all as long as max_seq_len: ragged
+// ones then fill about one, and blocks that already make 8 / 7 waves are left
+// whole. (Means over eight draws of lengths, us, for 16 sequences of 4 rows to
+// 16K positions, 6 of 9 to 8K, 4 of 175 to 12K, 3 of 30 to 32K: 105, 36, 198,
+// 99; one wave 115, 39, 198, 101; two waves 106, 46, 209, 109; three 106, 46,
+// 221, 115. Equally long sequences of 1.2 to 1.5 waves would gain up to 9% from
+// two or three parts: 4 of 200 rows over 12,000 positions 369 and 356, 3 of 250
+// over 16,000 474 and 435.) One sequence's blocks are about equally long, and
+// the number of parts whose last wave ends first is taken (the chunk above: 3
+// waves of halves, 722 us when thirds, in 4.4 waves, took 802). A choice by the
+// lengths themselves, on the device, cost every CTA 1 to 4 us.
 ExtendPlan extend_plan(const kvd_cache *c, const kvd_seqs *s, int rows,
                        int max_rows, int n_h, int sms) {
   ExtendPlan pl;

@@ -26,12 +26,14 @@
 // swizzled tiles that both products read. Raw rows come through a ring of
 // bulk copies, so that the widening never waits for HBM.
 //
-// Measured: 1,021 rows over 32,000 positions, 56 heads of 8 kv heads, in 719
-// us (1,323 TFLOP/s, 68% of cuBLAS's bf16 rate); whole prompts of 7,001 rows
-// in two sequences, 64 heads, in 437 us; 4 rows of each of 16 sequences over
-// 8,700 positions (160 MB) in 102 us. In a less even split (797 us) the first
-// took 627 us without the exponentials, 779 without the widening, 744 without
-// most of the products, 478 with none of them: it is the time from a
+// Measured: 1,021 rows over 32,000 positions, 56 heads of 8 kv heads, in 705
+// us (1,350 TFLOP/s, 70% of cuBLAS's bf16 rate); whole prompts of 7,001 rows
+// in two sequences, 64 heads, in 430 us; 4 rows of each of 16 sequences over
+// 8,700 positions (160 MB) in 102 us (32 pairs: 32 of a tile's 128 lanes, so
+// that one softmax warp of each group does all of its exponentials and three
+// quarters of the products are padding). In a less even split (797 us) the
+// first took 627 us without the exponentials, 779 without the widening, 744
+// without most of the products, 478 with none of them: it is the time from a
 // product's end to the softmax and from P back to the next product that is
 // left, one after the other in each of a tile's two buffers. (Softmax groups
 // that take turns on named barriers: 850 us; one S buffer of 128 positions a
@@ -381,12 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // Arrivals that the MMA warps (CTA 0's in a pair) wait for, and commits that
   // the roles of every CTA wait for. CTA 1's tiles in shared memory (Q, K, V)
-  // are released at cluster scope, ahead of their use: 434 to 439 us for the
-  // prompts, 699 to 701 for the chunk. P, on the way from one product to the
-  // next, lies in tensor memory and needs the threads' order only (at cluster
-  // scope as well: 537 and 970 us; relayed by CTA 1's own MMA warps: 477 and
-  // 842; without pairs: 475 and 792. By a release in CTA 0, which needs none
-  // either: 451 and 726).
+  // are released at cluster scope, ahead of their use: 434 to 440 us for the
+  // prompts (in a graph), 697 to 699 for the chunk. P, on the way from one
+  // product to the next, lies in tensor memory and needs the threads' order
+  // only (released at cluster scope as well: 537 and 970 us; relayed by CTA
+  // 1's own MMA warps: 477 and 842; without pairs: 475 and 792; released in
+  // CTA 0, which needs none either: 451 and 726).
   auto arrive_mma = [&](uint64_t *bar) {
     if (PAIR && rank != 0)
       mbar_arrive_remote(cluster_saddr(bar, 0));

@@ -15,17 +15,21 @@
 // over the CTA's threads and is 4% of a row's time at 72 heads. Measured:
 // 16,384 rows of 72 heads turned in 102 us (604 MB, 5.9 TB/s; the same in
 // CTAs of 128 or 512 threads or six an SM: slower, up to 131 us); 12,007 rows
-// of 64 heads turned and of 8 + 8 heads turned and stored in E4M3, then read
-// back, in 114 us (541 MB); 110,003 rows of 8 + 8 heads read from 4 bits in
-// 97 us (577 MB, 6.0 TB/s). The loads of a thread's next 16 bytes are issued
+// of 64 heads turned and of 8 + 8 heads turned and stored, in E4M3 in 90 us
+// (467 MB, 5.2 TB/s), in 4 bits in 86 us; 110,003 rows of 8 + 8 heads read
+// from 4 bits in 96 us (577 MB, 6.0 TB/s), from E4M3 in 133 us (5.1 TB/s), from
+// bf16 in 143 us (6.3 TB/s). The loads of a thread's next 16 bytes are issued
 // before it finishes these (106 us without, for the first figure).
 //
 // Write: with a rotation the turned keys pass through shared memory as bf16
 // (the rounding kvd_rope would make), then every row is encoded exactly as
 // kv_append encodes it. The MXFP4 encoder divides by one reciprocal per
-// 16-channel group instead of 16 exact divisions (mxfp4_group): the write of
-// 30,011 rows of 8 + 8 heads takes 40 us (157 MB, 3.9 TB/s: the encoder's
-// instructions, about 100 a group, bind it there, not HBM).
+// 16-channel group instead of 16 exact divisions (mxfp4_group). Rows without a
+// rotation do not reach the copy rate: 30,011 rows of 8 + 8 heads take 41 us in
+// 4 bits (157 MB, 3.8 TB/s), 53 in E4M3 and 56 in bf16. In 4 bits the kernel
+// issues 260 instructions a group on 62% of its slots (addresses are formed
+// anew for each group), and waits longest for the group's own loads, which
+// nothing issues ahead.
 #include <algorithm>
 
 #include "prompt_common.cuh"
