@@ -572,7 +572,9 @@ def kv_write(cache, block_table, start, row_start, k_new, v_new=None,
     start[b] .. of sequence b. With ``rope`` (a RopePlan) and ``positions``
     the keys are rotated on the way, and so is q [rows][n_h][head_dim] if
     given: returns q_out (None without q; q_out=q rotates in place). Rows of
-    a new q_out that no sequence owns are not initialised."""
+    a new q_out that no sequence owns are not initialised. With a row_start
+    that descends nothing is done; it is flagged, as is a sequence that the
+    rows do not hold (device_error(): DEVERR_LEN; so for the other calls)."""
     c = cache.struct()
     B = _ragged(cache, block_table, start, row_start)
     ks = _rows3(k_new, "k_new", cache.n_kv, cache.head_dim)

@@ -27,7 +27,7 @@
 // 16-channel group instead of 16 exact divisions (mxfp4_group). Rows without a
 // rotation do not reach the copy rate: 30,011 rows of 8 + 8 heads take 41 us in
 // 4 bits (157 MB, 3.8 TB/s), 53 in E4M3 and 56 in bf16. In 4 bits the kernel
-// issues 260 instructions a group on 62% of its slots (addresses are formed
+// issues 260 instructions a group on 64% of its slots (addresses are formed
 // anew for each group), and waits longest for the group's own loads, which
 // nothing issues ahead.
 #include <algorithm>
