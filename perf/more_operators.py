@@ -262,9 +262,10 @@ def _prepare_keep(s, case, g, h):
     s["path"], s["n_keep"] = _i32(paths), _i32(keep)
     if own:
         import kv_cache_decode_gqa_gb300 as K
-        s["caches"] = [K.PagedCache(s["k"][i], s["v"][i], case["block"],
-                                    case["n_kv"], case["d"], case["dtype"])
-                       for i in range(case["layers"])]
+        s["caches"] = K.CacheList(
+            K.PagedCache(s["k"][i], s["v"][i], case["block"], case["n_kv"],
+                         case["d"], case["dtype"])
+            for i in range(case["layers"]))
     return s
 
 
