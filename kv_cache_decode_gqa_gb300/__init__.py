@@ -27,6 +27,8 @@ __all__ = ["PagedCache", "kv_append", "gqa_decode", "mla_decode",
            "sparse_decode", "workspace_size",
            "RopePlan", "rope_plan", "rope", "kv_write", "kv_read",
            "gqa_extend", "extend_workspace_size",
+           "tree_plan", "gqa_tree", "gqa_cross", "attend_workspace_size",
+           "CacheList", "kv_keep",
            "bytes_per_token", "device_error", "launch_count", "set_tuning",
            "KvdError",
            "OP_GQA_DECODE", "OP_MLA_DECODE", "OP_INDEXER_TOPK",
@@ -723,6 +725,218 @@ def gqa_extend(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
             None if lse is None else lse.data_ptr(),
             None if workspace is None else workspace.data_ptr(), nbytes, s))
         return out, lse
+    return dev, launch
+
+
+# ---------------------------------------------------------------------------
+# drafted trees and cross attention (include/kvd_tree.h)
+# ---------------------------------------------------------------------------
+TREE_NODES = 256     # KVD_TREE_NODES
+
+
+def _words(max_rows):
+    return (max_rows + 31) // 32
+
+
+@_in_context
+def tree_plan(parents, start, row_start, max_rows, window=0, masks=None,
+              positions=None):
+    """The trees of a step: parents int32 [rows], node row_start[b] + i of
+    sequence b hanging below node parents[row] < i of its sequence (-1: below
+    the context, start[b] positions long). Returns (masks int32 [rows]
+    [ceil(max_rows / 32)]: bits of a node and its ancestors, positions int32
+    [rows]: start[b] + depth). ``max_rows``: a bound on the nodes of a tree, at
+    most TREE_NODES. ``window``: ancestors that many levels up and more are
+    left out. Rows of new outputs that no sequence owns are not
+    initialised."""
+    import torch
+    _need(parents, "parents", torch.int32)
+    _need(start, "start", torch.int32)
+    B = start.numel()
+    _need(row_start, "row_start", torch.int32, B + 1)
+    rows, max_rows = parents.numel(), int(max_rows)
+    words = _words(max_rows)
+    if masks is not None:
+        _need(masks, "masks", torch.int32, rows * words)
+    if positions is not None:
+        _need(positions, "positions", torch.int32, rows)
+    dev = _one_device(parents, start, row_start, masks, positions)
+
+    def launch(s, masks=masks, positions=positions):
+        if masks is None:
+            masks = torch.empty((rows, words), dtype=torch.int32, device=dev)
+        if positions is None:
+            positions = torch.empty(rows, dtype=torch.int32, device=dev)
+        check(lib().kvd_tree_plan(
+            parents.data_ptr(), start.data_ptr(), row_start.data_ptr(), B,
+            rows, max_rows, int(window), masks.data_ptr(),
+            positions.data_ptr(), s))
+        return masks, positions
+    return dev, launch
+
+
+def attend_workspace_size(cache, block_table, seq_lens, max_seq_len, rows,
+                          n_h, max_rows=None, row_list=True):
+    """Workspace bytes of a gqa_tree or gqa_cross call with these arguments
+    (kvd_attend_workspace_size); ``row_list=False``: a gqa_cross call without
+    row_start."""
+    import torch
+    c = cache.struct()
+    s = _seqs(block_table, seq_lens, max_seq_len)
+    rows = int(rows)
+    if max_rows is None:
+        max_rows = rows if row_list else 1
+    out = ctypes.c_size_t(0)
+    with torch.cuda.device(block_table.device):
+        check(lib().kvd_attend_workspace_size(
+            ctypes.byref(c), ctypes.byref(s), rows, int(max_rows), n_h,
+            1 if row_list else 0, ctypes.byref(out)))
+    return out.value
+
+
+def _attend(call, extra, cache, seqs, tensors, q, row_start, max_rows, scale,
+            out, lse, workspace, want_lse):
+    """What gqa_tree and gqa_cross share: `call` the name of the function,
+    `extra` its arguments between q and the scale."""
+    import torch
+    d = cache.head_dim
+    qs = _rows3(q, "q", width=d)
+    c = cache.struct()
+    rows, n_h = qs.rows, qs.heads
+    if row_start is not None:
+        _need(row_start, "row_start", torch.int32, seqs.batch + 1)
+    if out is not None:
+        _need(out, "out", torch.bfloat16, rows * n_h * d)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, rows * n_h)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+    dev = _one_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale,
+                      row_start, out, lse, workspace, *tensors)
+
+    def launch(s, out=out, lse=lse, workspace=workspace):
+        L = lib()
+        if out is None:
+            out = torch.empty((rows, n_h, d), dtype=torch.bfloat16,
+                              device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty((rows, n_h), dtype=torch.float32, device=dev)
+        if workspace is not None:
+            nbytes = workspace.numel()
+        else:
+            need = ctypes.c_size_t(0)
+            check(L.kvd_attend_workspace_size(
+                c, seqs, rows, max_rows, n_h, 0 if row_start is None else 1,
+                need))
+            nbytes = need.value
+            if nbytes:
+                # every partial a call keeps here is written before it is read
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        check(getattr(L, call)(
+            c, seqs, None if row_start is None else row_start.data_ptr(),
+            max_rows, qs, *extra, float(scale or 0.0), out.data_ptr(),
+            None if lse is None else lse.data_ptr(),
+            None if workspace is None else workspace.data_ptr(), nbytes, s))
+        return out, lse
+    return dev, launch
+
+
+@_in_context
+def gqa_tree(cache, block_table, seq_lens, max_seq_len, q, row_start,
+             max_rows, masks, positions=None, scale=None, out=None, lse=None,
+             workspace=None, want_lse=True, window=0, window_start=None):
+    """Attention of drafted nodes over a cache that holds them: q [rows][n_h]
+    [head_dim] bf16 (contiguous vectors) -> (out [rows][n_h][head_dim] bf16,
+    lse [rows][n_h] fp32). Rows row_start[b] .. row_start[b + 1] - 1 (int32
+    [batch + 1]) are the last positions of sequence b, at most ``max_rows`` (up
+    to TREE_NODES). Each sees the positions before them and the nodes whose
+    bits its ``masks`` (int32 [rows][ceil(max_rows / 32)], from tree_plan or
+    any other) have set. ``window`` bounds the context from the row's
+    ``positions`` (int32 [rows], tree_plan) back, ``window_start`` from the
+    front. ``out`` must not overlap q. Rows of new outputs that no sequence owns
+    are not initialised."""
+    import torch
+    seqs = _seqs(block_table, seq_lens, max_seq_len, 0, window, window_start)
+    rows, max_rows = q.shape[0], int(max_rows)
+    if row_start is None:
+        raise ValueError("gqa_tree needs row_start")
+    _need(masks, "masks", torch.int32, rows * _words(max_rows))
+    if positions is not None:
+        _need(positions, "positions", torch.int32, rows)
+    elif window:
+        raise ValueError("a window needs positions")
+    return _attend("kvd_gqa_tree",
+                   (masks.data_ptr(),
+                    None if positions is None else positions.data_ptr()),
+                   cache, seqs, (block_table, seq_lens, window_start, masks,
+                                 positions),
+                   q, row_start, max_rows, scale, out, lse, workspace,
+                   want_lse)
+
+
+@_in_context
+def gqa_cross(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
+              max_rows=None, scale=None, out=None, lse=None, workspace=None,
+              want_lse=True, first=None):
+    """Cross attention: q [rows][n_h][head_dim] bf16 (contiguous vectors) ->
+    (out, lse) as gqa_tree, every row of sequence b over all its states, the
+    cached positions [first[b], seq_lens[b]) (``first``: int32 [batch], None:
+    from 0). Rows row_start[b] .. row_start[b + 1] - 1 belong to sequence b, at
+    most ``max_rows`` of them (None: all rows, which fits any list); without
+    row_start row b is sequence b's one row."""
+    seqs = _seqs(block_table, seq_lens, max_seq_len, 0, 0, first)
+    if max_rows is None:
+        max_rows = 1 if row_start is None else q.shape[0]
+    return _attend("kvd_gqa_cross", (), cache, seqs,
+                   (block_table, seq_lens, first), q, row_start,
+                   int(max_rows), scale, out, lse, workspace, want_lse)
+
+
+class CacheList:
+    """The caches of a model's layers (PagedCache objects of one shape and
+    type) as kv_keep takes them, checked once; the model keeps it. It holds the
+    caches' tensors: make a new one when a layer gets others."""
+
+    def __init__(self, caches):
+        self.caches = tuple(caches)
+        if not self.caches:
+            raise ValueError("a CacheList needs a cache")
+        self.structs = (_native.KvdCache * len(self.caches))(
+            *[c.struct() for c in self.caches])
+        tensors = [t for c in self.caches for t in (c.k, c.v)]
+        if len({c.k.data_ptr() for c in self.caches}) != len(self.caches):
+            raise ValueError("a cache is listed twice")
+        self.device = _one_device(*tensors)
+
+
+@_in_context
+def kv_keep(caches, block_table, start, path, n_keep):
+    """Move the accepted nodes' rows of every layer's cache (a CacheList, or
+    PagedCache objects to make one of) behind the context: position start[b] +
+    j takes the row of start[b] + path[b][j], j < n_keep[b]. ``path``: int32
+    [batch][width], ascending node indexes from the root on; ``start``,
+    ``n_keep``: int32 [batch]. The new lengths are start + n_keep."""
+    import torch
+    if not isinstance(caches, CacheList):
+        caches = CacheList([caches] if isinstance(caches, PagedCache)
+                           else caches)
+    _need(block_table, "block_table", torch.int32)
+    _need(path, "path", torch.int32)
+    if block_table.dim() != 2 or path.dim() != 2:
+        raise ValueError("block_table and path must be [batch][...]")
+    B, width = path.shape
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table and path have {block_table.shape[0]} "
+                         f"and {B} sequences")
+    _need(start, "start", torch.int32, B)
+    _need(n_keep, "n_keep", torch.int32, B)
+    dev = _one_device(block_table, start, path, n_keep, caches.caches[0].k)
+
+    def launch(s):
+        check(lib().kvd_kv_keep(
+            caches.structs, len(caches.structs), block_table.data_ptr(),
+            block_table.shape[1], start.data_ptr(), path.data_ptr(), width,
+            n_keep.data_ptr(), B, s))
     return dev, launch
 
 

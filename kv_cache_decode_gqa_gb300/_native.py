@@ -1,4 +1,4 @@
-"""ctypes view of libkvd.so (include/kvd.h) and libkvd_inputs.so.
+"""ctypes view of libkvd.so (include/kvd*.h) and libkvd_inputs.so.
 
 The libraries are built in-tree by build.py (``__graft_entry__.build()``).
 Loading fails loudly if they are missing: there is no other implementation
@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(PKG, "libkvd.so")
 INPUTS_LIB_PATH = os.path.join(PKG, "libkvd_inputs.so")
 HEADER = os.path.join(ROOT, "include", "kvd.h")
 PROMPT_HEADER = os.path.join(ROOT, "include", "kvd_prompt.h")
+TREE_HEADER = os.path.join(ROOT, "include", "kvd_tree.h")
 
 c_void_p = ctypes.c_void_p
 c_int32 = ctypes.c_int32
@@ -121,6 +122,21 @@ _SIGS = {
     "kvd_extend_workspace_size": (c_int32, [_PCACHE, _PSEQS, c_int32, c_int32,
                                             c_int32,
                                             ctypes.POINTER(c_size_t)]),
+    "kvd_tree_plan": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32,
+                                c_int32, c_int32, c_int32, c_void_p,
+                                c_void_p, c_void_p]),
+    "kvd_gqa_tree": (c_int32, [_PCACHE, _PSEQS, c_void_p, c_int32, _PROWS,
+                               c_void_p, c_void_p, c_float, c_void_p,
+                               c_void_p, c_void_p, c_size_t, c_void_p]),
+    "kvd_gqa_cross": (c_int32, [_PCACHE, _PSEQS, c_void_p, c_int32, _PROWS,
+                                c_float, c_void_p, c_void_p, c_void_p,
+                                c_size_t, c_void_p]),
+    "kvd_attend_workspace_size": (c_int32, [_PCACHE, _PSEQS, c_int32, c_int32,
+                                            c_int32, c_int32,
+                                            ctypes.POINTER(c_size_t)]),
+    "kvd_kv_keep": (c_int32, [_PCACHE, c_int32, c_void_p, c_int32, c_void_p,
+                              c_void_p, c_int32, c_void_p, c_int32,
+                              c_void_p]),
     "kvd_workspace_size": (c_int32, [c_int32, _PCACHE, _PSEQS, c_int32,
                                      c_int32, ctypes.POINTER(c_size_t)]),
 }

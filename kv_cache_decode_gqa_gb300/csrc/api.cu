@@ -14,8 +14,10 @@
 
 #include "kvd.h"
 #include "kvd_prompt.h"
+#include "kvd_tree.h"
 #include "kvd_internal.h"
 #include "prompt_internal.h"
+#include "tree_internal.h"
 
 namespace {
 
@@ -1490,6 +1492,246 @@ kvd_status kvd_gqa_extend(const kvd_cache *cache, const kvd_seqs *seqs,
                       ? kvd::launch_extend_few(p, pl.f, s)
                       : kvd::launch_extend_tc(p, pl.blocks, pl.splits, s),
                   "gqa_extend");
+}
+
+}  // extern "C"
+
+// ===========================================================================
+// drafted trees and cross attention (kvd_tree.h)
+// ===========================================================================
+namespace {
+
+// What kvd_gqa_tree, kvd_gqa_cross and their workspace sizing check alike.
+kvd_status check_attend(const kvd_cache *c, const kvd_seqs *s, int rows,
+                        int max_rows, int n_h, bool lists, const char *what) {
+  kvd_status st = check_cache(c, true, what);
+  if (st != KVD_OK) return st;
+  st = check_seqs(s, c, what);
+  if (st != KVD_OK) return st;
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: head_dim %d (64 or 128)", what,
+                c->head_dim);
+  if (c->dtype == KVD_FP8_E4M3 && (!c->k_scale || !c->v_scale))
+    return fail(KVD_ERR_NULL, "%s: fp8 cache needs k_scale and v_scale", what);
+  if (n_h < 1 || n_h % c->n_kv != 0)
+    return fail(KVD_ERR_SHAPE, "%s: n_h (%d) must be a positive multiple of "
+                "n_kv (%d)", what, n_h, c->n_kv);
+  if (n_h / c->n_kv > 128)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: group size %d above 128", what,
+                n_h / c->n_kv);
+  if (s->batch > 1024)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: at most 1024 sequences per call "
+                "(got %d)", what, s->batch);
+  if (rows < 0 || max_rows < 0)
+    return fail(KVD_ERR_SHAPE, "%s: rows and max_rows must be >= 0", what);
+  if (!lists && (rows != s->batch || max_rows != 1))
+    return fail(KVD_ERR_SHAPE, "%s: without row_start there is one row a "
+                "sequence (rows = batch, max_rows = 1)", what);
+  if ((long)rows * n_h >= (1L << 31) || (long)max_rows * n_h >= (1L << 31))
+    return fail(KVD_ERR_SHAPE, "%s: rows x n_h must be below 2^31", what);
+  return KVD_OK;
+}
+
+// The call itself, its masks and positions checked.
+kvd_status attend(const kvd_cache *cache, const kvd_seqs *seqs,
+                  const int32_t *row_start, int32_t max_rows,
+                  const kvd_rows *q, const uint32_t *masks,
+                  const int32_t *positions, float scale, void *out, float *lse,
+                  void *workspace, size_t workspace_bytes, kvd_stream stream,
+                  const char *what) {
+  kvd_status st = check_rows(q, cache->head_dim, false, what, "q");
+  if (st != KVD_OK) return st;
+  if (!rows_aligned16(q) || !aligned(out, 16))
+    return fail(KVD_ERR_SHAPE, "%s: q and out must be 16-byte aligned, q's "
+                "strides multiples of 8", what);
+  if (seqs->batch == 0 || q->rows == 0 || max_rows == 0) return ok();
+  if (!out) return fail(KVD_ERR_NULL, "%s: out required", what);
+  if (rows_meet(q, cache->head_dim, out,
+                (size_t)q->rows * q->heads * cache->head_dim * 2))
+    return fail(KVD_ERR_SHAPE, "%s: out overlaps q", what);
+  const DeviceInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != KVD_OK) return st;
+  kvd::AttendParams p{};
+  p.k = static_cast<const uint8_t *>(cache->k);
+  p.v = static_cast<const uint8_t *>(cache->v);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.block_table = seqs->block_table;
+  p.seq_lens = seqs->seq_lens;
+  p.q = static_cast<const uint16_t *>(q->data);
+  p.q_rs = q->row_stride;
+  p.q_hs = q->head_stride;
+  p.out = static_cast<uint16_t *>(out);
+  p.lse = lse;
+  p.batch = seqs->batch;
+  p.n_h = q->heads;
+  p.n_kv = cache->n_kv;
+  p.dk = p.dv = cache->head_dim;
+  p.dtype = cache->dtype;
+  p.block_size = cache->block_size;
+  p.num_blocks = cache->num_blocks;
+  p.max_blocks = seqs->max_blocks_per_seq;
+  p.max_seq_len = seqs->max_seq_len;
+  p.window = seqs->window;
+  p.win_start = seqs->window_start;
+  p.row_start = row_start;
+  p.max_rows = max_rows;
+  p.rows = q->rows;
+  p.masks = masks;
+  p.words = (max_rows + 31) / 32;
+  p.positions = positions;
+  p.scale_log2 = log2_scale(scale, cache->head_dim);
+  p.err = d->err;
+  return launched(
+      kvd::launch_attend(p, reinterpret_cast<cudaStream_t>(stream)), what);
+}
+
+}  // namespace
+
+extern "C" {
+
+kvd_status kvd_tree_plan(const int32_t *parents, const int32_t *start,
+                         const int32_t *row_start, int32_t batch, int32_t rows,
+                         int32_t max_rows, int32_t window, uint32_t *masks,
+                         int32_t *positions, kvd_stream stream) {
+  if (batch < 0 || rows < 0 || max_rows < 0 || window < 0)
+    return fail(KVD_ERR_SHAPE, "tree_plan: batch, rows, max_rows and window "
+                "must be >= 0");
+  if (max_rows > kvd::kTreeNodes || batch > 1024)
+    return fail(KVD_ERR_UNSUPPORTED, "tree_plan: at most %d nodes a tree and "
+                "1024 sequences", kvd::kTreeNodes);
+  if (batch == 0 || rows == 0 || max_rows == 0) return ok();
+  if (!parents || !start || !row_start || !masks)
+    return fail(KVD_ERR_NULL, "tree_plan: parents, start, row_start and masks "
+                "required");
+  const DeviceInfo *d = nullptr;
+  const kvd_status st = device_info(&d);
+  if (st != KVD_OK) return st;
+  kvd::TreePlanParams p{};
+  p.parents = parents;
+  p.start = start;
+  p.row_start = row_start;
+  p.masks = masks;
+  p.positions = positions;
+  p.batch = batch;
+  p.rows = rows;
+  p.max_rows = max_rows;
+  p.words = (max_rows + 31) / 32;
+  p.window = window;
+  p.err = d->err;
+  return launched(
+      kvd::launch_tree_plan(p, reinterpret_cast<cudaStream_t>(stream)),
+      "tree_plan");
+}
+
+kvd_status kvd_attend_workspace_size(const kvd_cache *cache,
+                                     const kvd_seqs *seqs, int32_t rows,
+                                     int32_t max_rows, int32_t n_h,
+                                     int32_t lists, size_t *bytes) {
+  if (!bytes)
+    return fail(KVD_ERR_NULL, "attend_workspace_size: bytes is NULL");
+  kvd_status st = check_attend(cache, seqs, rows, max_rows, n_h, lists != 0,
+                               "attend_workspace_size");
+  if (st != KVD_OK) return st;
+  *bytes = 0;
+  return ok();
+}
+
+kvd_status kvd_gqa_tree(const kvd_cache *cache, const kvd_seqs *seqs,
+                        const int32_t *row_start, int32_t max_rows,
+                        const kvd_rows *q, const uint32_t *masks,
+                        const int32_t *positions, float scale, void *out,
+                        float *lse, void *workspace, size_t workspace_bytes,
+                        kvd_stream stream) {
+  if (!q) return fail(KVD_ERR_NULL, "gqa_tree: q is NULL");
+  const kvd_status st = check_attend(cache, seqs, q->rows, max_rows, q->heads,
+                                     true, "gqa_tree");
+  if (st != KVD_OK) return st;
+  if (max_rows > kvd::kTreeNodes)
+    return fail(KVD_ERR_UNSUPPORTED, "gqa_tree: at most %d nodes a tree",
+                kvd::kTreeNodes);
+  if (seqs->batch > 0 && q->rows > 0 && max_rows > 0) {
+    if (!row_start || !masks)
+      return fail(KVD_ERR_NULL, "gqa_tree: row_start and masks required");
+    if (seqs->window > 0 && !positions)
+      return fail(KVD_ERR_NULL, "gqa_tree: a window needs positions");
+  }
+  return attend(cache, seqs, row_start, max_rows, q, masks, positions, scale,
+                out, lse, workspace, workspace_bytes, stream, "gqa_tree");
+}
+
+kvd_status kvd_gqa_cross(const kvd_cache *cache, const kvd_seqs *seqs,
+                         const int32_t *row_start, int32_t max_rows,
+                         const kvd_rows *q, float scale, void *out, float *lse,
+                         void *workspace, size_t workspace_bytes,
+                         kvd_stream stream) {
+  if (!q) return fail(KVD_ERR_NULL, "gqa_cross: q is NULL");
+  const kvd_status st = check_attend(cache, seqs, q->rows, max_rows, q->heads,
+                                     row_start != nullptr, "gqa_cross");
+  if (st != KVD_OK) return st;
+  if (seqs->window != 0)
+    return fail(KVD_ERR_UNSUPPORTED, "gqa_cross: no sliding window (rows see "
+                "every state)");
+  return attend(cache, seqs, row_start, max_rows, q, nullptr, nullptr, scale,
+                out, lse, workspace, workspace_bytes, stream, "gqa_cross");
+}
+
+kvd_status kvd_kv_keep(const kvd_cache *caches, int32_t n_caches,
+                       const int32_t *block_table, int32_t max_blocks_per_seq,
+                       const int32_t *start, const int32_t *path,
+                       int32_t width, const int32_t *n_keep, int32_t batch,
+                       kvd_stream stream) {
+  if (n_caches < 0 || batch < 0 || width < 0 || max_blocks_per_seq < 1)
+    return fail(KVD_ERR_SHAPE, "kv_keep: n_caches, batch, width >= 0 and "
+                "max_blocks_per_seq >= 1 required");
+  if (width > kvd::kTreeNodes || batch > 1024)
+    return fail(KVD_ERR_UNSUPPORTED, "kv_keep: paths of at most %d nodes, at "
+                "most 1024 sequences", kvd::kTreeNodes);
+  if (n_caches == 0) return ok();
+  if (!caches) return fail(KVD_ERR_NULL, "kv_keep: caches is NULL");
+  for (int32_t i = 0; i < n_caches; ++i) {
+    const kvd_cache &c = caches[i], &c0 = caches[0];
+    const kvd_status st = check_cache(&c, false, "kv_keep");
+    if (st != KVD_OK) return st;
+    if (c.num_blocks != c0.num_blocks || c.block_size != c0.block_size ||
+        c.n_kv != c0.n_kv || c.head_dim != c0.head_dim ||
+        c.dtype != c0.dtype || !c.v != !c0.v)
+      return fail(KVD_ERR_SHAPE, "kv_keep: cache %d differs from the first in "
+                  "shape or type", i);
+  }
+  if (batch == 0 || width == 0) return ok();
+  if (!block_table || !start || !path || !n_keep)
+    return fail(KVD_ERR_NULL, "kv_keep: block_table, start, path and n_keep "
+                "required");
+  const DeviceInfo *d = nullptr;
+  const kvd_status st = device_info(&d);
+  if (st != KVD_OK) return st;
+  kvd::KeepParams p{};
+  p.block_table = block_table;
+  p.start = start;
+  p.path = path;
+  p.n_keep = n_keep;
+  p.row = kvd::row_bytes(caches[0].head_dim, caches[0].dtype);
+  p.n_kv = caches[0].n_kv;
+  p.batch = batch;
+  p.max_blocks = max_blocks_per_seq;
+  p.block_size = caches[0].block_size;
+  p.num_blocks = caches[0].num_blocks;
+  p.width = width;
+  p.err = d->err;
+  for (int32_t i = 0; i < n_caches; i += kvd::kKeepCaches) {
+    p.tensors = 0;
+    for (int32_t j = i; j < std::min(n_caches, i + kvd::kKeepCaches); ++j) {
+      p.data[p.tensors++] = static_cast<uint8_t *>(caches[j].k);
+      if (caches[j].v)
+        p.data[p.tensors++] = static_cast<uint8_t *>(caches[j].v);
+    }
+    const cudaError_t e =
+        kvd::launch_keep(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return launched(e, "kv_keep");
+  }
+  return ok();
 }
 
 }  // extern "C"

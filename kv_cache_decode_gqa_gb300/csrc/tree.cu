@@ -1,0 +1,147 @@
+// Trees of drafted tokens: their plan (kvd_tree_plan) and the move of their
+// accepted rows (kvd_kv_keep).
+#include "kvd_common.cuh"
+#include "tree_internal.h"
+
+namespace kvd {
+namespace {
+
+constexpr int kPlanThreads = kTreeNodes;
+
+// One CTA a sequence, one thread a node: the thread walks up the parents,
+// which lie in shared memory, and sets a bit of its mask a step. A walk is as
+// long as the node is deep; sums and doubling would save steps in chains of a
+// hundred nodes only.
+__global__ void __launch_bounds__(kPlanThreads)
+    tree_plan_kernel(const __grid_constant__ TreePlanParams p) {
+  __shared__ int16_t up[kTreeNodes];
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.x, i = threadIdx.x;
+  // a descent of the list at or before this sequence
+  bool down = false;
+  for (int j = i; j <= b; j += kPlanThreads)
+    down |= p.row_start[j + 1] < p.row_start[j];
+  const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
+  const bool fits = r0 >= 0 && r1 >= r0 && r1 <= p.rows &&
+                    (long)r1 - r0 <= p.max_rows;
+  if (__syncthreads_or(down) || !fits) {
+    if (i == 0 && r0 != r1) report(p.err, DEVERR_LEN);
+    return;
+  }
+  const int n = r1 - r0;
+  if (i < n) {
+    int a = p.parents[r0 + i];
+    if (a < -1 || a >= i) {
+      report(p.err, DEVERR_INDEX);
+      a = -1;
+    }
+    up[i] = (int16_t)a;
+  }
+  __syncthreads();
+  if (i >= n) return;
+  constexpr int W = kTreeNodes / 32;
+  uint32_t m[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) m[w] = 0;
+  int depth = 0;
+  for (int a = i; a >= 0; a = up[a], ++depth) {
+    if (p.window == 0 || depth < p.window) {
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (a >> 5 == w) m[w] |= 1u << (a & 31);
+    }
+  }
+  const long row = r0 + i;
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    if (w < p.words) p.masks[row * p.words + w] = m[w];
+  if (p.positions)
+    p.positions[row] = (int)((uint32_t)p.start[b] + (uint32_t)(depth - 1));
+}
+
+// Bytes of one access of the move: rows of MXFP4 are multiples of 8.
+constexpr int kKeepThreads = 256;
+
+// A thread moves one piece of 8 bytes of every accepted row of a (cache
+// tensor, sequence, head), eight rows' loads in flight: with an ascending path
+// from 0 up, row j's source path[j] >= j is overwritten by row path[j] at the
+// earliest, so that loads stay ahead of the stores when rows are taken in
+// order.
+__global__ void __launch_bounds__(kKeepThreads)
+    keep_kernel(const __grid_constant__ KeepParams p) {
+  __shared__ long at[kTreeNodes + 1], to[kTreeNodes];
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.y, tid = threadIdx.x;
+  const int n = p.n_keep[b];
+  const bool first = blockIdx.x == 0;
+  if (n < 0 || n > p.width) {
+    if (first && tid == 0) report(p.err, DEVERR_LEN);
+    return;
+  }
+  int bad = 0;
+  const int32_t *path = p.path + (long)b * p.width;
+  auto row_of = [&](long pos) {
+    if (pos < 0 || pos >= (long)p.max_blocks * p.block_size) {
+      bad |= DEVERR_POS;
+      return 0L;
+    }
+    const int blk =
+        p.block_table[(long)b * p.max_blocks + pos / p.block_size];
+    if (blk < 0 || blk >= p.num_blocks) {
+      bad |= DEVERR_BLOCK;
+      return 0L;
+    }
+    return (long)blk * p.n_kv * p.block_size + pos % p.block_size;
+  };
+  if (tid < n) {
+    const int x = path[tid];
+    if (x < 0 || (tid > 0 && path[tid - 1] >= x)) bad |= DEVERR_INDEX;
+    at[tid] = row_of((long)p.start[b] + x);
+    to[tid] = row_of((long)p.start[b] + tid);
+  }
+  if (__syncthreads_or(bad)) {
+    if (first && bad) report(p.err, bad);
+    return;
+  }
+  const int pieces = p.row / 8;
+  const long items = (long)p.tensors * p.n_kv * pieces;
+  for (long x = (long)blockIdx.x * kKeepThreads + tid; x < items;
+       x += (long)gridDim.x * kKeepThreads) {
+    const int c = (int)(x % pieces);
+    const long th = x / pieces;
+    const long head = th % p.n_kv * p.block_size;
+    uint8_t *base = p.data[th / p.n_kv] + c * 8;
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      uint2 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < n)
+          v[j] = *reinterpret_cast<const uint2 *>(
+              base + (at[j0 + j] + head) * p.row);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < n && at[j0 + j] != to[j0 + j])
+          *reinterpret_cast<uint2 *>(base + (to[j0 + j] + head) * p.row) =
+              v[j];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s) {
+  return launch_pdl(tree_plan_kernel, dim3(p.batch), dim3(kPlanThreads), 0, s,
+                    1, p);
+}
+
+cudaError_t launch_keep(const KeepParams &p, cudaStream_t s) {
+  const long items = (long)p.tensors * p.n_kv * (p.row / 8);
+  const long blocks = (items + kKeepThreads - 1) / kKeepThreads;
+  return launch_pdl(keep_kernel,
+                    dim3((unsigned)(blocks < 4096 ? blocks : 4096), p.batch),
+                    dim3(kKeepThreads), 0, s, 1, p);
+}
+
+}  // namespace kvd
