@@ -22,7 +22,8 @@ LIB_SOURCES = ["api.cu", "append.cu", "decode_simt.cu", "noalloc.cu",
                "decode_mma.cu", "decode_wide.cu", "decode_latent_tc.cu",
                "decode_gather_tc.cu",
                "indexer.cu", "block_pool.cu", "rows.cu", "extend_few.cu",
-               "extend_tc.cu", "tree.cu", "attend.cu"]
+               "extend_tc.cu", "tree.cu", "attend.cu",
+               "attend_widen.cu"]
 INPUTS_SOURCES = ["inputs_fill.cu"]
 LIB = os.path.join(PKG, "libkvd.so")
 INPUTS_LIB = os.path.join(PKG, "libkvd_inputs.so")

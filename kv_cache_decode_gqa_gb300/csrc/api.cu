@@ -1529,7 +1529,20 @@ kvd_status check_attend(const kvd_cache *c, const kvd_seqs *s, int rows,
                 "sequence (rows = batch, max_rows = 1)", what);
   if ((long)rows * n_h >= (1L << 31) || (long)max_rows * n_h >= (1L << 31))
     return fail(KVD_ERR_SHAPE, "%s: rows x n_h must be below 2^31", what);
+  if (s->max_seq_len > INT32_MAX - 255)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: max_seq_len above 2^31 - 256", what);
+  if (c->dtype == KVD_BF16 &&
+      (double)c->num_blocks * c->n_kv * c->block_size >= 2147483648.0)
+    return fail(KVD_ERR_UNSUPPORTED, "%s: bf16 caches of 2^31 rows (blocks x "
+                "heads x slots) and more", what);
   return KVD_OK;
+}
+
+kvd::AttendPlan attend_plan_of(const kvd_cache *c, const kvd_seqs *s, int rows,
+                               int max_rows, int n_h, int sms) {
+  const int forced = g_decode_ctas.load(std::memory_order_relaxed);
+  return kvd::attend_plan(c->n_kv, n_h / c->n_kv, c->head_dim, s->batch, rows,
+                          max_rows, s->max_seq_len, forced > 0 ? forced : sms);
 }
 
 // The call itself, its masks and positions checked.
@@ -1552,7 +1565,18 @@ kvd_status attend(const kvd_cache *cache, const kvd_seqs *seqs,
   const DeviceInfo *d = nullptr;
   st = device_info(&d);
   if (st != KVD_OK) return st;
+  const kvd::AttendPlan pl = attend_plan_of(cache, seqs, q->rows, max_rows,
+                                            q->heads, d->sms);
+  Plan need;
+  need.ws_bytes = pl.ws_bytes;
+  st = check_ws(need, workspace, workspace_bytes, what);
+  if (st != KVD_OK) return st;
   kvd::AttendParams p{};
+  p.n_splits = pl.ctas;
+  p.block_rows = pl.pairs;
+  p.ws_o = static_cast<float *>(workspace);
+  p.ws_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                       pl.ws_o_bytes);
   p.k = static_cast<const uint8_t *>(cache->k);
   p.v = static_cast<const uint8_t *>(cache->v);
   p.k_scale = cache->k_scale;
@@ -1635,6 +1659,11 @@ kvd_status kvd_attend_workspace_size(const kvd_cache *cache,
                                "attend_workspace_size");
   if (st != KVD_OK) return st;
   *bytes = 0;
+  if (rows == 0 || max_rows == 0 || seqs->batch == 0) return ok();
+  const DeviceInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != KVD_OK) return st;
+  *bytes = attend_plan_of(cache, seqs, rows, max_rows, n_h, d->sms).ws_bytes;
   return ok();
 }
 

@@ -1,141 +1,141 @@
 // Attention of several rows a sequence that is not causal (kvd_gqa_tree,
-// kvd_gqa_cross): one warp a (row, query head), its lanes over the channels,
-// the running maximum and sum of a softmax in fp32.
-#include <cmath>
-
-#include "prompt_common.cuh"
-#include "tree_internal.h"
+// kvd_gqa_cross): the launches, and the merge of the units that CTAs share.
+#include "attend_tc.cuh"
 
 namespace kvd {
 namespace {
 
-constexpr int kAttendThreads = 256;
+// Log-sum-exp merge of the units that several CTAs of the launch before share:
+// a lane a float4 of an output row, up to 8 parts' loads in flight. A CTA is
+// small enough to sit beside one of that launch, so that the work is scanned
+// and the rows' parts are found while it still runs (it lets this one start
+// only after its own predecessor has completed).
+constexpr int kAttendMergeThreads = 256;
 
-// This lane's channels [E lane, E lane + E) of a cached row.
-template <int DT, int D>
-__device__ __forceinline__ void load_channels(const uint8_t *cache, long row,
-                                              int lane, float (&x)[D / 32]) {
-  constexpr int E = D / 32;
-  const uint8_t *src = cache + row * row_bytes(D, DT);
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int c = lane * E + e;
-    if constexpr (DT == DT_BF16) {
-      x[e] = __uint_as_float(
-          (uint32_t)reinterpret_cast<const uint16_t *>(src)[c] << 16);
-    } else if constexpr (DT == DT_FP8) {
-      x[e] = f16lo(e4m3x2_to_f16x2(src[c]));
-    } else {
-      const uint32_t codes = src[c / 2];
-      const float s = f16lo(e4m3x2_to_f16x2(src[D / 2 + c / 16]));
-      const uint32_t y = e2m1x2_to_f16x2(codes);
-      x[e] = (c & 1 ? f16hi(y) : f16lo(y)) * s;
-    }
-  }
-}
-
-template <int DT, int D>
-__global__ void __launch_bounds__(kAttendThreads)
-    attend_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int E = D / 32;
+template <int D, int NB>
+__global__ void __launch_bounds__(kAttendMergeThreads)
+    attend_merge_kernel(const __grid_constant__ AttendParams p) {
+  __shared__ long scratch[33], pre[NB];
   pdl_trigger();
+  const int G = p.n_h / p.n_kv, tid = threadIdx.x;
+  long before, total;
+  int end;
+  scan_work(p, G, scratch, false, before, total, end);
+  const int per = (p.batch + kAttendMergeThreads - 1) / kAttendMergeThreads;
+  for (int b = tid * per; b < min(tid * per + per, p.batch); ++b) {
+    pre[b] = before;
+    if (b < end) before += seq_chunks(p, seq_at(p, b, G));
+  }
+  __syncthreads();
+  const int P = (int)min((long)p.n_splits, total);
+  constexpr int LANES = D / 4;  // of a row
+  const long at = (long)blockIdx.x * (kAttendMergeThreads / LANES) +
+                  tid / LANES;
+  const int e4 = tid % LANES;
+  int parts = 0, first = 0, ri = 0;
+  if (at < (long)p.rows * p.n_h) {
+    const int row = (int)(at / p.n_h), head = (int)(at - (long)row * p.n_h);
+    int b = 0;
+    Seq q{};
+    for (; b < end; ++b) {
+      const int r0 = p.row_start ? p.row_start[b] : b;
+      const int r1 = p.row_start ? p.row_start[b + 1] : b + 1;
+      if (row >= r0 && row < r1) {
+        q = seq_at(p, b, G);
+        break;
+      }
+    }
+    if (q.n > 0 && q.nch > 0) {
+      const int f = (row - q.r0) * G + head % G, m = f / kUnit;
+      ri = f - m * kUnit;
+      const long u =
+          pre[b] + ((long)(head / G) * q.blocks + m) * q.nch;
+      first = share_of(u, total, P);
+      parts = share_of(u + q.nch - 1, total, P) - first + 1;
+    }
+  }
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long item =
-      (long)blockIdx.x * (kAttendThreads / 32) + (threadIdx.x >> 5);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    bool down = false;
-    for (int b = 0; b < p.batch; ++b) {
-      down |= descends(p, b);
-      const int n = down ? 0 : seq_rows(p, b);
-      if (p.row_start && n == 0 && p.row_start[b] != p.row_start[b + 1])
-        report(p.err, DEVERR_LEN);
-      if (p.seq_lens[b] > p.max_seq_len ||
-          (p.masks && min(max(p.seq_lens[b], 0), p.max_seq_len) < n))
-        report(p.err, DEVERR_LEN);
-    }
-  }
-  if (item >= (long)p.rows * p.n_h) return;
-  const int row = (int)(item / p.n_h), h = (int)(item % p.n_h);
-  int b = 0, r0 = 0;
-  for (;; ++b) {
-    if (b == p.batch || descends(p, b)) return;
-    const int n = seq_rows(p, b);
-    r0 = p.row_start ? p.row_start[b] : b;
-    if (row >= r0 && row < r0 + n) break;
-  }
-  const int T = min(max(p.seq_lens[b], 0), p.max_seq_len);
-  const int ctx = p.masks ? T - seq_rows(p, b) : T;
-  if (ctx < 0) return;
-  int lo = p.win_start ? max(p.win_start[b], 0) : 0;
-  if (p.masks && p.window > 0)
-    lo = max(lo, max(p.positions[row], -1) + 1 - p.window);
-  const int G = p.n_h / p.n_kv, kvh = h / G;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __uint_as_float(
-        (uint32_t)p.q[row * p.q_rs + h * p.q_hs + lane * E + e] << 16);
-    o[e] = 0.f;
-  }
-  const float scale =
-      p.scale_log2 * (DT == DT_FP8 ? p.k_scale[kvh] : 1.f);
-  for (int pos = min(lo, ctx); pos < T; ++pos) {
-    if (pos >= ctx) {
-      const int j = pos - ctx;
-      if (!(p.masks[(long)row * p.words + j / 32] >> (j & 31) & 1)) continue;
-    }
-    int blk = p.block_table[(long)b * p.max_blocks + pos / p.block_size];
-    if (blk < 0 || blk >= p.num_blocks) {
-      report(p.err, DEVERR_BLOCK);
-      blk = 0;
-    }
-    const long at =
-        ((long)blk * p.n_kv + kvh) * p.block_size + pos % p.block_size;
-    float x[E], s = 0.f;
-    load_channels<DT, D>(p.k, at, lane, x);
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], x[e], s);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-      s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= scale;
-    const float top = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - top);
-    const float w = top == -INFINITY ? 0.f : exp2f(s - top);
-    m = top;
-    l = fmaf(l, f, w);
-    load_channels<DT, D>(p.v, at, lane, x);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[e], o[e] * f);
-  }
-  const float inv =
-      l == 0.f ? 0.f : (DT == DT_FP8 ? p.v_scale[kvh] : 1.f) / l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) p.out[item * D + lane * E + e] = f2bf(o[e] * inv);
-  if (lane == 0 && p.lse)
-    p.lse[item] =
-        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  if (parts <= 1) return;  // written whole, or no sequence's row
+  float M, W;
+  float4 acc;
+  quad_merge<1>(p.ws_lse, p.ws_o, p.block_rows, D, ri, ri * LANES + e4, parts,
+                [&](int i) { return (long)(first + i) * 2 + (i == 0); }, M, W,
+                acc);
+  const float iw = W == 0.f ? 0.f : 1.f / W;
+  uint2 packed;
+  packed.x = pack_bf16x2(acc.x * iw, acc.y * iw);
+  packed.y = pack_bf16x2(acc.z * iw, acc.w * iw);
+  reinterpret_cast<uint2 *>(p.out + at * D)[e4] = packed;
+  if (e4 == 0 && p.lse) p.lse[at] = W == 0.f ? -INFINITY : M + logf(W);
 }
 
-template <int DT, int D>
-cudaError_t launch_t(const AttendParams &p, cudaStream_t s) {
-  const long per = kAttendThreads / 32;
-  const long items = (long)p.rows * p.n_h;
-  return launch_pdl(attend_kernel<DT, D>,
-                    dim3((unsigned)((items + per - 1) / per)),
-                    dim3(kAttendThreads), 0, s, 1, p);
+template <int D>
+cudaError_t launch_merge(const AttendParams &p, cudaStream_t s) {
+  const long rows = (long)p.rows * p.n_h;
+  const long per = kAttendMergeThreads / (D / 4);
+  const dim3 grid((unsigned)((rows + per - 1) / per));
+  return launch_pdl(p.batch <= kMergeSmallBatch
+                        ? attend_merge_kernel<D, kMergeSmallBatch>
+                        : attend_merge_kernel<D, kMaxDecodeBatch>,
+                    grid, dim3(kAttendMergeThreads), 0, s, 1, p);
+}
+
+// A bf16 cache as [column half][row][64 columns], in swizzled boxes of `box`
+// rows (of all columns where box is 64).
+bool cache_map(CUtensorMap *map, const uint8_t *data, const AttendParams &p,
+               int box) {
+  const auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t d = p.dk;
+  const cuuint64_t dims[3] = {
+      64, (cuuint64_t)p.num_blocks * p.n_kv * p.block_size, d / 64};
+  const cuuint64_t strides[2] = {2 * d, 128};
+  const cuuint32_t boxes[3] = {64, (cuuint32_t)box,
+                               (cuuint32_t)(box == 64 ? d / 64 : 1)};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                const_cast<uint8_t *>(data), dims, strides, boxes, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
+AttendPlan attend_plan(int n_kv, int g, int d, int batch, int rows,
+                       int max_rows, int max_seq_len, int ctas) {
+  AttendPlan pl;
+  pl.pairs = (int)std::min((long)max_rows * g, (long)kUnit);
+  const long units =
+      (long)n_kv * (((long)rows * g + (long)std::min(batch, rows) * (kUnit - 1)) /
+                    kUnit);
+  const long chunks = units * (((long)max_seq_len + kN - 1) / kN);
+  pl.ctas = (int)std::max(1L, std::min((long)ctas, chunks));
+  if (pl.ctas > 1) {
+    const size_t slots = (size_t)pl.ctas * 2 * pl.pairs;
+    pl.ws_o_bytes = (slots * d * 4 + 255) / 256 * 256;
+    pl.ws_bytes = pl.ws_o_bytes + (slots * 4 + 255) / 256 * 256;
+  }
+  return pl;
+}
+
 cudaError_t launch_attend(const AttendParams &p, cudaStream_t s) {
-  if (p.dtype == DT_MXFP4) return launch_t<DT_MXFP4, 128>(p, s);
-  if (p.dtype == DT_FP8)
-    return p.dk == 128 ? launch_t<DT_FP8, 128>(p, s)
-                       : launch_t<DT_FP8, 64>(p, s);
-  return p.dk == 128 ? launch_t<DT_BF16, 128>(p, s)
-                     : launch_t<DT_BF16, 64>(p, s);
+  TcParams tp{};
+  tp.p = p;
+  cudaError_t e;
+  if (p.dtype == DT_BF16) {
+    // boxes of rows that lie within a block and within half a chunk
+    tp.box = std::min(64, p.block_size & -p.block_size);
+    if (!cache_map(&tp.tmk, p.k, p, tp.box) ||
+        !cache_map(&tp.tmv, p.v, p, tp.box))
+      return cudaErrorNotSupported;
+    e = p.dk == 128 ? launch_attend_t<DT_BF16, 128, 2>(tp, s)
+                    : launch_attend_t<DT_BF16, 64, 2>(tp, s);
+  } else {
+    e = launch_attend_widen(tp, p.block_rows <= kM, s);
+  }
+  if (e != cudaSuccess || p.n_splits <= 1) return e;
+  return p.dk == 128 ? launch_merge<128>(p, s) : launch_merge<64>(p, s);
 }
 
 }  // namespace kvd

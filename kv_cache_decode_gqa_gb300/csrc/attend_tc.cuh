@@ -1,0 +1,1208 @@
+// Attention of several rows a sequence that is not causal, on the
+// 5th-generation tensor cores (kvd_gqa_tree, kvd_gqa_cross).
+//
+// The (row, head) pairs of a kv head are numbered row-major, pair f = row *
+// G + head, so any group size G fills the MMA's M. A unit is a block of up to
+// 256 pairs -- two M = 128 tiles -- of one sequence and kv head against all
+// the positions that its sequence attends to, in chunks of 128:
+//   S = Q K^T   (A = Q in shared memory, B = K chunk, K-major)
+//   O += P V    (A = P in tensor memory, over S; B = V chunk, MN-major)
+// A tile's S lies in two buffers of 64 positions: while the softmax (a thread
+// a pair) turns one into P, the tensor core does PV of the other and the
+// scores that follow it. A unit of at most 128 pairs has one tile; then both
+// halves work for it, on even and odd chunks, and their states are merged at
+// its end.
+#pragma once
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "prompt_common.cuh"
+#include "tcgen05_pair.cuh"
+#include "tmap.h"
+#include "tree_internal.h"
+
+namespace kvd {
+
+struct TcParams {
+  AttendParams p;
+  CUtensorMap tmk, tmv;  // bf16 caches: [column half][row][64 columns]
+  int box;               // rows of their boxes: 1 .. 64, a power of two
+};
+
+namespace {
+
+constexpr int kM = 128;         // pairs per tile
+constexpr int kUnit = 256;      // pairs per unit, at most
+constexpr int kN = 128;         // positions per chunk
+constexpr int kS = 64;          // positions per product (half a chunk)
+constexpr int kSoftBar = 1;
+
+// DT, D: the cache's type and head width. QS: slots for tiles of queries (1:
+// every unit of the launch has one tile).
+template <int DT, int D, int QS>
+struct ACfg {
+  static constexpr bool WIDEN = DT != DT_BF16;
+  static constexpr int TILE = 128 * D * 2;    // 128 rows of 16 bits
+  static constexpr int HALF = TILE / 2;       // 64 positions of a chunk
+  static constexpr int COLS = 64 * 128;       // 64 rows x 64 columns
+  static constexpr int RAW = kN * row_bytes(D, DT);  // cached rows of a chunk
+  // warps 0-7: softmax; then (WIDEN) 8-11 K and queries, 12-15 V, 16 copies,
+  // 17, 18 MMA issue; or 8-11 queries, 12 copies, 13 the ends of V, 14, 15 MMA
+  static constexpr int kLoad = WIDEN ? 16 : 12;
+  static constexpr int kMma = WIDEN ? 17 : 14;
+  static constexpr int THREADS = WIDEN ? 640 : 512;
+  // K and V tiles in alternation, then (WIDEN) raw K and V rows
+  static constexpr int FIXED = (2 + QS) * kM * 4 + 768;
+  static constexpr int ROOM = 227 * 1024 - FIXED - QS * TILE;
+  static constexpr int NS =
+      WIDEN ? 4 : (ROOM / TILE > 12 ? 12 : ROOM / TILE);
+  static constexpr int NR_FIT = WIDEN ? (ROOM - NS * TILE) / RAW : 0;
+  static constexpr int NR = NR_FIT > 12 ? 12 : NR_FIT & ~1;
+  static constexpr int Q_OFF = 0;
+  static constexpr int KV_OFF = QS * TILE;
+  static constexpr int RAW_OFF = KV_OFF + NS * TILE;
+  static constexpr int F_OFF = RAW_OFF + NR * RAW;  // float [2][128]
+  static constexpr int SL_OFF = F_OFF + 2 * kM * 4;  // float [QS][128]
+  static constexpr int BAR_OFF = SL_OFF + QS * kM * 4;
+  static constexpr int BARS = 3 * NS + 2 * NR + 2 * QS + 13;
+  static constexpr int FLAG_OFF = BAR_OFF + BARS * 8;
+  static constexpr int SMEM = FLAG_OFF + 64;
+  static_assert(NS >= 4 && (!WIDEN || NR >= 2) && SMEM <= 227 * 1024,
+                "shared memory");
+  static_assert(RAW % 128 == 0 && FLAG_OFF % 8 == 0, "alignment");
+};
+
+// 16-byte piece c (0..7) of row r (0..63) in a 128-byte-swizzled 64-column
+// tile.
+__device__ __forceinline__ uint32_t sw128(int r, int c) {
+  return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Packed pairs of fp32 values, one instruction for both.
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b,
+                                              uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The largest of three, NaN only if all are.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// the work: every chunk of every unit, in the order (sequence, kv head, block
+// of pairs, chunk); the CTAs take equal consecutive ranges
+// ---------------------------------------------------------------------------
+// What a sequence's units are computed from.
+struct Seq {
+  int r0, n;    // its rows (n = 0: skipped, or none)
+  int T, ctx;   // positions, and those before the tree (cross: all)
+  int lo;       // first position that a row attends to
+  int c0, nch;  // first chunk, chunks
+  int blocks;   // blocks of pairs
+};
+
+__device__ __forceinline__ Seq seq_at(const AttendParams &p, int b, int G) {
+  Seq q;
+  q.r0 = p.row_start ? p.row_start[b] : b;
+  q.n = seq_rows(p, b);
+  q.T = min(max(p.seq_lens[b], 0), p.max_seq_len);
+  q.ctx = q.T;
+  q.lo = p.win_start ? max(p.win_start[b], 0) : 0;
+  if (p.masks) {
+    q.ctx = q.T - q.n;
+    if (q.ctx < 0) q.n = 0;
+    if (p.window > 0) q.lo = max(q.lo, max(q.ctx, 0) - (p.window - 1));
+    q.lo = min(q.lo, max(q.ctx, 0));
+  }
+  q.c0 = q.lo / kN;
+  q.nch = q.n > 0 && q.lo < q.T ? (q.T + kN - 1) / kN - q.c0 : 0;
+  q.blocks = (int)(((long)q.n * G + kUnit - 1) / kUnit);
+  return q;
+}
+
+__device__ __forceinline__ long seq_chunks(const AttendParams &p,
+                                           const Seq &q) {
+  return (long)p.n_kv * q.blocks * q.nch;
+}
+
+// Exclusive prefix sums of the sequences' chunks over the block's threads:
+// thread t has the sequences [t per, t per + per), per = ceil(batch /
+// blockDim). `end`: the list's first descent (or the batch). `scratch` int64
+// [32] and one int behind it. With `flag` the block reports what does not fit.
+// Ends with a barrier.
+__device__ __forceinline__ void scan_work(const AttendParams &p, int G,
+                                          long *scratch, bool flag, long &before,
+                                          long &total, int &end) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  const int per = (p.batch + nt - 1) / nt;
+  const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+  end = p.batch;
+  while (true) {
+    bool broken = false;
+    long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      broken |= b < end && descends(p, b);
+      if (b < end) sum += seq_chunks(p, seq_at(p, b, G));
+    }
+    long x = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    const int any = __syncthreads_or(broken);
+    before = x - sum;
+    total = 0;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) before += scratch[w];
+      total += scratch[w];
+    }
+    if (!any) break;
+    end = first_descent(p, reinterpret_cast<int *>(scratch + 32));
+  }
+  if (flag) {
+    for (int b = b0; b < b1; ++b) {
+      const bool rows = p.row_start && p.row_start[b] != p.row_start[b + 1];
+      if ((rows && (b >= end || seq_at(p, b, G).n == 0)) ||
+          p.seq_lens[b] > p.max_seq_len)
+        report(p.err, DEVERR_LEN);
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ long share_lo(int c, long total, int P) {
+  return total / P * c + total % P * c / P;
+}
+// The CTA whose share holds chunk x.
+__device__ __forceinline__ int share_of(long x, long total, int P) {
+  int c = (int)((double)x / (double)total * P);
+  c = min(max(c, 0), P - 1);
+  while (c > 0 && x < share_lo(c, total, P)) --c;
+  while (c < P - 1 && x >= share_lo(c + 1, total, P)) ++c;
+  return c;
+}
+
+// A CTA's run of chunks of one unit.
+struct Seg {
+  Seq q;
+  int b, h, m;     // sequence, kv head, block of pairs
+  int f0, np;      // its first pair, pairs
+  int k0, k1;      // chunks of the unit, [k0, k1) of q.nch
+  long left;       // chunks of the range from this segment on
+  bool two;        // two tiles
+  __device__ __forceinline__ int nch() const { return k1 - k0; }
+  __device__ __forceinline__ bool whole() const {
+    return k0 == 0 && k1 == q.nch;
+  }
+  // chunks that tile t takes part in, two steps each
+  __device__ __forceinline__ int steps(int t) const {
+    return two ? 2 * nch() : (nch() - t + 1) & ~1;
+  }
+  __device__ __forceinline__ int tiles() const { return two ? 2 : 1; }
+};
+
+// Step v of tile t: half v & 1 of a chunk of the segment.
+__device__ __forceinline__ int chunk_of(const Seg &s, int t, int v) {
+  return s.two ? v >> 1 : (v & ~1) + t;
+}
+
+__device__ __forceinline__ void seg_unit(const AttendParams &p, Seg &s,
+                                         int G) {
+  s.f0 = s.m * kUnit;
+  s.np = min(s.q.n * G - s.f0, kUnit);
+  s.two = s.np > kM;
+  s.k1 = (int)min((long)s.q.nch, s.k0 + s.left);
+}
+
+// The segment at chunk `off` of sequence b's.
+__device__ __forceinline__ Seg seg_first(const AttendParams &p, int b,
+                                         long off, long left, int G) {
+  Seg s;
+  s.b = b;
+  s.q = seq_at(p, b, G);
+  s.left = left;
+  const long unit = off / s.q.nch;
+  s.k0 = (int)(off - unit * s.q.nch);
+  s.h = (int)(unit / s.q.blocks);
+  s.m = (int)(unit - (long)s.h * s.q.blocks);
+  seg_unit(p, s, G);
+  return s;
+}
+
+// On to the next segment; false at the range's end.
+__device__ __forceinline__ bool seg_next(const AttendParams &p, Seg &s,
+                                         int G) {
+  s.left -= s.nch();
+  if (s.left <= 0) return false;
+  s.k0 = 0;
+  if (++s.m == s.q.blocks) {
+    s.m = 0;
+    if (++s.h == p.n_kv) {
+      s.h = 0;
+      do {
+        s.q = seq_at(p, ++s.b, G);
+      } while (seq_chunks(p, s.q) == 0);
+    }
+  }
+  seg_unit(p, s, G);
+  return true;
+}
+
+// Bits of the 32 positions from p0 on that a row sees: [lo, ctx), and the
+// nodes of its mask (`words` words at `mask`, n nodes from position ctx on).
+__device__ __forceinline__ uint32_t seen_bits(int p0, int lo, int ctx, int n,
+                                              const uint32_t *mask,
+                                              int words) {
+  const int a = min(max(lo - p0, 0), 32), z = min(max(ctx - p0, 0), 32);
+  uint32_t bits = 0;
+  if (a < z) bits = (0xffffffffu >> (32 - (z - a))) << a;
+  const int j = p0 - ctx;  // the first position's node
+  if (mask && j > -32 && j < n) {
+    const int w = j >> 5;
+    const uint32_t x = w >= 0 ? mask[w] : 0u;
+    const uint32_t y = w + 1 < words ? mask[w + 1] : 0u;
+    uint32_t m = __funnelshift_r(x, y, j & 31);
+    if (n - j < 32) m &= (1u << (n - j)) - 1u;  // nodes from n on
+    bits |= m;
+  }
+  return bits;
+}
+
+template <int DT, int D, int QS>
+__global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
+    attend_tc_kernel(const __grid_constant__ TcParams tp) {
+  using C = ACfg<DT, D, QS>;
+  constexpr bool WIDEN = C::WIDEN;
+  constexpr int NS = C::NS, NR = C::NR;
+  // log2 units that a reference lies below the maximum, and may lag by: f16
+  // probabilities stay below 2^15 and the largest is at least 2^7, so that f16
+  // drops only what is 2^-32 of it; bf16 has fp32's range
+  constexpr float kHead = WIDEN ? 7.f : 0.f;
+  constexpr float kSlack = 8.f;
+  // tensor memory: two score buffers of 64 columns a tile, then the outputs
+  constexpr uint32_t kColS = 0, kColO = 256;
+  const AttendParams &p = tp.p;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float *fs = reinterpret_cast<float *>(smem + C::F_OFF);
+  float *qsl = reinterpret_cast<float *>(smem + C::SL_OFF);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+  uint64_t *empty = full + NS;
+  uint64_t *land = empty + NS;  // bf16: a V tile whose ends are not filled
+  uint64_t *rawfull = land + NS;
+  uint64_t *rawempty = rawfull + NR;
+  uint64_t *qfull = rawempty + NR;
+  uint64_t *qempty = qfull + QS;
+  uint64_t *sfull = qempty + QS;  // [tile][buffer]
+  uint64_t *pfull = sfull + 4;    // [tile][buffer]
+  uint64_t *pvdone = pfull + 4;   // [tile]
+  uint64_t *odone = pvdone + 2;   // [tile]: a unit's last product
+  uint64_t *drain = odone + 2;
+  int *flags = reinterpret_cast<int *>(smem + C::FLAG_OFF);
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(flags);
+  int *s_b = flags + 1;
+  long *s_off = reinterpret_cast<long *>(flags + 2);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.n_h / p.n_kv;
+
+  pdl_wait();
+  pdl_trigger();  // after the wait: the merge launch never overlaps this
+                  // launch's predecessor
+  // ---- this CTA's share ------------------------------------------------
+  long lo, hi;
+  {
+    long before, total;
+    int end;
+    scan_work(p, G, reinterpret_cast<long *>(smem), blockIdx.x == 0, before,
+              total, end);
+    // rows that see nothing
+    for (int b = blockIdx.x; b < end; b += gridDim.x) {
+      const Seq q = seq_at(p, b, G);
+      if (q.n == 0 || q.nch > 0) continue;
+      for (long i = tid; i < (long)q.n * p.n_h * (D / 8); i += C::THREADS)
+        reinterpret_cast<uint4 *>(p.out + (long)q.r0 * p.n_h * D)[i] =
+            make_uint4(0, 0, 0, 0);
+      if (p.lse)
+        for (long i = tid; i < (long)q.n * p.n_h; i += C::THREADS)
+          p.lse[(long)q.r0 * p.n_h + i] = -INFINITY;
+    }
+    const int P = (int)min((long)gridDim.x, total);
+    const int c = blockIdx.x;
+    if (c >= P) return;
+    lo = share_lo(c, total, P);
+    hi = share_lo(c + 1, total, P);
+    const int per = (p.batch + C::THREADS - 1) / C::THREADS;
+    for (int b = tid * per; b < min(tid * per + per, end); ++b) {
+      const long n = seq_chunks(p, seq_at(p, b, G));
+      if (lo >= before && lo < before + n) {
+        *s_b = b;
+        *s_off = lo - before;
+      }
+      before += n;
+    }
+  }
+  // the swizzled tiles assume 1 KB atoms (every CTA sees the same layout)
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (tid == 0) report(p.err, DEVERR_TIMEOUT);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], WIDEN ? 4 : 1);
+      mbar_init(&empty[i], 2);  // both MMA warps
+      mbar_init(&land[i], 1);
+    }
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(&rawfull[i], 1);
+      mbar_init(&rawempty[i], 4);
+    }
+    for (int i = 0; i < QS; ++i) {
+      mbar_init(&qfull[i], 4);
+      // a commit of either MMA warp (and the softmax warps have the scales)
+      mbar_init(&qempty[i], WIDEN ? 10 : 2);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+    }
+    mbar_init(&pvdone[0], 1);
+    mbar_init(&pvdone[1], 1);
+    mbar_init(&odone[0], 1);
+    mbar_init(&odone[1], 1);
+    mbar_init(drain, 2);
+    fence_mbar_init();
+  }
+  if (warp == C::kMma) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *s_tmem;
+  Seg sg = seg_first(p, *s_b, *s_off, hi - lo, G);
+  // Every wait is bounded. A role whose wait runs out goes on without waiting
+  // and without touching what it waited for; the others follow when their own
+  // waits run out.
+  auto give_up = [&]() {
+    if (lane == 0) report(p.err, DEVERR_TIMEOUT);
+  };
+  auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  };
+  // Uses of the query slots, in order: a unit's tiles one after the other.
+  auto q_slot = [&](int use) { return use % QS; };
+  auto q_par = [&](int use) { return (uint32_t)(use / QS & 1); };
+
+  // A tile of queries by 128 threads, a pair each (WIDEN: scaled into f16).
+  auto load_queries = [&](const Seg &s, int t, int use, int r) {
+    const int ri = t * kM + r;
+    const bool live = ri < s.np;
+    const int f = s.f0 + ri;
+    uint8_t *qt = smem + C::Q_OFF + q_slot(use) * C::TILE;
+    const uint16_t *src = p.q + (long)(s.q.r0 + f / G) * p.q_rs +
+                          ((long)s.h * G + f % G) * p.q_hs;
+    auto at = [&](int c) {
+      return live ? reinterpret_cast<const uint4 *>(src)[c]
+                  : make_uint4(0, 0, 0, 0);
+    };
+    // 64 rows of 64 columns lie 8 KB apart, columns from 64 on behind all rows
+    auto put = [&](int c, const uint4 &w) {
+      *reinterpret_cast<uint4 *>(qt + ((c >> 3) * 2 + (r >> 6)) * C::COLS +
+                                 sw128(r & 63, c & 7)) = w;
+    };
+    if constexpr (!WIDEN) {
+      uint4 x[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) x[c] = at(c);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) put(c, x[c]);
+    } else {
+      // twice over the row, with few registers: its largest magnitude first
+      uint32_t m = 0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D / 8; c0 += 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = at(c0 + c);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          m = __vmaxu2(m,
+                       __vmaxu2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu));
+          m = __vmaxu2(m,
+                       __vmaxu2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu));
+        }
+      }
+      m = max(m & 0xffffu, m >> 16);
+      const int e = row_exponent(m);
+      const float sc = __uint_as_float((uint32_t)e << 23);
+      const float ks = DT == DT_FP8 ? p.k_scale[s.h] : 1.f;
+      qsl[q_slot(use) * kM + r] = fmaxf(
+          p.scale_log2 * ks * exp2f((float)(127 - e)), 1.17549435e-38f);
+#pragma unroll 1
+      for (int c0 = 0; c0 < D / 8; c0 += 4) {
+        uint4 x[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = at(c0 + c);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          put(c0 + c,
+              make_uint4(pack_f16x2(bf16lo(x[c].x) * sc, bf16hi(x[c].x) * sc),
+                         pack_f16x2(bf16lo(x[c].y) * sc, bf16hi(x[c].y) * sc),
+                         pack_f16x2(bf16lo(x[c].z) * sc, bf16hi(x[c].z) * sc),
+                         pack_f16x2(bf16lo(x[c].w) * sc,
+                                    bf16hi(x[c].w) * sc)));
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&qfull[q_slot(use)]);
+  };
+
+  if (warp < 8) {
+    // ======================= softmax ======================================
+    if constexpr (WIDEN) reg_inc<128>();
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // pair of the tile
+    const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+    int use = 0;              // query slots used so far
+    int gv = 0, units = 0;    // steps and units of this tile so far
+    bool ok = true;
+    while (true) {
+      const bool two = sg.two;
+      const int ri = two ? t * kM + r : r;  // pair of the unit
+      const bool live = ri < sg.np;
+      const int f = sg.f0 + ri;
+      const int row = live ? sg.q.r0 + f / G : 0;
+      // what the pair sees (one that does not exist: everything, so that its
+      // warp masks nothing for it; its query is 0 and nothing of it is stored)
+      int vlo = 0, vctx = INT_MAX;
+      const uint32_t *mask = nullptr;
+      if (live) {
+        vlo = p.win_start ? max(p.win_start[sg.b], 0) : 0;
+        vctx = sg.q.ctx;
+        if (p.masks) {
+          mask = p.masks + (long)row * p.words;
+          if (p.window > 0)
+            vlo = max(vlo, max(p.positions[row], vctx) - (p.window - 1));
+        }
+      }
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      float sl = p.scale_log2;
+      if constexpr (WIDEN) {
+        // (the other tile's slot is released here too)
+        for (int i = 0; i < sg.tiles(); ++i) {
+          if (ok && !wait_all(&qfull[q_slot(use + i)], q_par(use + i))) {
+            give_up();
+            ok = false;
+          }
+        }
+        const int u = use + (two ? t : 0);
+        sl = qsl[q_slot(u) * kM + r];
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&qempty[q_slot(use)]);
+          if (two) mbar_arrive(&qempty[q_slot(use + 1)]);
+        }
+      }
+      use += sg.tiles();
+      float ref = -INFINITY, l = 0.f;
+      const uint64_t sl2 = pack_f32x2(sl, sl);
+      const int nv = sg.steps(t);
+      for (int v = 0; ok && v < nv; ++v) {
+        const int buf = v & 1, g = gv + v;
+        const int pos0 =
+            (sg.q.c0 + sg.k0 + chunk_of(sg, t, v)) * kN + buf * kS;
+        if (!wait_all(&sfull[2 * t + buf], (g >> 1) & 1)) {
+          give_up();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (warp_live) {
+          uint32_t x[2][32];
+          const uint32_t ts = tl + kColS + 128 * t + kS * buf;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, x[i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) tmem_wait_ld(x[i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int p0 = pos0 + 32 * i;
+            // 32 columns that some pair of the warp sees in part
+            if (__any_sync(0xffffffffu, p0 < vlo || p0 > vctx - 32)) {
+              const uint32_t bits =
+                  live ? seen_bits(p0, vlo, vctx, sg.q.n, mask, p.words)
+                       : 0xffffffffu;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(bits >> j & 1)) x[i][j] = 0xff800000u;  // -inf
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t *y = &x[i >> 1][16 * (i & 1)];
+            mx[i] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+#pragma unroll
+            for (int j = 2; j < 16; j += 2)
+              mx[i] = max3(mx[i], __uint_as_float(y[j]),
+                           __uint_as_float(y[j + 1]));
+          }
+          const float top =
+              fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl - kHead;
+          const bool grow = top > ref + kSlack;  // from -inf: any score
+          if (__any_sync(0xffffffffu, grow)) {
+            const float al = grow ? ex2(ref - top) : 1.f;
+            if (grow) ref = top;
+            l *= al;
+            if (v > 0) {
+              // the tile's last product into O has to be over (this step's
+              // scores followed the one before it)
+              if (!wait_all(&pvdone[t], (g - 1) & 1)) {
+                give_up();
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                uint32_t o[16];
+                const uint32_t to = tl + kColO + D * t + 16 * i;
+                tmem_ld16(to, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+                tmem_st16(to, o);
+              }
+            }
+          }
+          const float mu = ref == -INFINITY ? 0.f : ref;
+          const uint64_t mu2 = pack_f32x2(-mu, -mu);
+          uint64_t ls[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float e0, e1;
+              unpack_f32x2(
+                  fma_f32x2(pack_f32x2(__uint_as_float(x[i][2 * j]),
+                                       __uint_as_float(x[i][2 * j + 1])),
+                            sl2, mu2),
+                  e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              ls[j & 1] = add_f32x2(ls[j & 1], pack_f32x2(e0, e1));
+              pk[j] = WIDEN ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+            }
+            tmem_st16(ts + 16 * i, pk);
+          }
+          {
+            float a0, a1;
+            unpack_f32x2(add_f32x2(ls[0], ls[1]), a0, a1);
+            l += a0 + a1;
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[2 * t + buf]);
+      }
+      // ---- epilogue ------------------------------------------------------
+      gv += nv;
+      if (nv > 0) {
+        if (ok && !wait_all(&odone[t], units & 1)) {
+          give_up();
+          ok = false;
+        }
+        ++units;
+      }
+      tc_fence_after();
+      // the outputs' factors (of the tile's sums, and of tile 1's in one-tile
+      // units) and the log-sum-exp
+      float w0, w1 = 0.f, lse;
+      auto finish = [&](float M, float L) {
+        lse = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        return L == 0.f ? 0.f : DT == DT_FP8 ? p.v_scale[sg.h] / L : 1.f / L;
+      };
+      if (two) {
+        w0 = finish(ref, l);
+      } else {
+        // the halves' states of pair r, joined by tile 0's thread
+        if (t == 1) fs[r] = ref, fs[kM + r] = l;
+        tc_fence_before();
+        named_sync(kSoftBar, 2 * kM);
+        tc_fence_after();
+        if (t == 0) {
+          const float rb = fs[r], M = fmaxf(ref, rb);
+          const float mu = M == -INFINITY ? 0.f : M;
+          w0 = ex2(ref - mu);
+          w1 = ex2(rb - mu);
+          const float inv = finish(M, l * w0 + fs[kM + r] * w1);
+          w0 *= inv, w1 *= inv;
+          fs[r] = w0, fs[kM + r] = w1;
+        }
+        named_sync(kSoftBar, 2 * kM);
+        if (t == 1) w0 = fs[r], w1 = fs[kM + r];
+      }
+      // two tiles: all columns of the tile's pair; one: the halves write half
+      // of them each
+      const int ncol = two ? D : D / 2;
+      const int col0 = two ? 0 : t * (D / 2);
+      const uint32_t ta = tl + kColO + (two ? D * t : 0) + col0;
+      const bool second = !two && sg.nch() > 1;
+      const bool whole = sg.whole();
+      const long at = (long)row * p.n_h + (long)sg.h * G + f % G;
+      const long part = ((long)blockIdx.x * 2 + (sg.k0 > 0 ? 0 : 1)) *
+                            p.block_rows + ri;
+      if (warp_live && ok) {
+#pragma unroll 1
+        for (int g = 0; g < ncol; g += 32) {
+          uint32_t o[32];
+          tmem_ld32(ta + g, o);
+          tmem_wait_ld(o);
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            y[i] = __uint_as_float(o[i]) * w0;
+          if (second) {
+            tmem_ld32(ta + D + g, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              y[i] = fmaf(__uint_as_float(o[i]), w1, y[i]);
+          }
+          if (live) {
+            if (whole) {
+              uint4 *dst =
+                  reinterpret_cast<uint4 *>(p.out + at * D + col0 + g);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]),
+                                    pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                    pack_bf16x2(y[8 * i + 4], y[8 * i + 5]),
+                                    pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+            } else {
+              float4 *dst =
+                  reinterpret_cast<float4 *>(p.ws_o + part * D + col0 + g);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2],
+                                     y[4 * i + 3]);
+            }
+          }
+        }
+        if (live && (two || t == 0)) {
+          if (!whole)
+            p.ws_lse[part] = lse;
+          else if (p.lse)
+            p.lse[at] = lse;
+        }
+      }
+      tc_fence_before();
+      // (the next unit's products into O and its states wait for both halves'
+      // reads)
+      if (!two) named_sync(kSoftBar, 2 * kM);
+      if (!seg_next(p, sg, G)) break;
+    }
+  } else if (WIDEN && warp < 16) {
+    // ======================= queries, widening ============================
+    if constexpr (WIDEN) {
+      reg_dec<72>();
+      const int r = tid & 127;  // row of the chunk
+      const bool is_v = warp >= 12;
+      int use = 0, gc = 0;
+      bool ok = true;
+      // K rows are raw units 0, 2, 4, ..., V rows 1, 3, 5, ...
+      int rs = is_v, rph = 0;
+      do {
+        if (!is_v) {
+          for (int t = 0; t < sg.tiles(); ++t, ++use) {
+            if (ok && !wait_all(&qempty[q_slot(use)], q_par(use) ^ 1)) {
+              give_up();
+              ok = false;
+            }
+            if (ok) load_queries(sg, t, use, r);
+          }
+        }
+        for (int i = 0; ok && i < sg.nch(); ++i, ++gc) {
+          if (!wait_all(&rawfull[rs], rph)) {
+            give_up();
+            ok = false;
+            break;
+          }
+          const uint8_t *src =
+              smem + C::RAW_OFF + rs * C::RAW + r * row_bytes(D, DT);
+          const int pos = (sg.q.c0 + sg.k0 + i) * kN + r;
+          // a row that was not copied, or that no pair sees: zeros, so that 0
+          // times it stays 0
+          const bool dead = pos < sg.q.lo || pos >= sg.q.T;
+          const int u = 2 * gc + is_v, st = u % NS;
+          uint8_t *dst = smem + C::KV_OFF + st * C::TILE + (r >> 6) * C::HALF;
+          constexpr int PIECES = D / 16;  // of 16 channels
+          auto put = [&](int g, const uint32_t (&y)[8]) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int c = 2 * g + q;
+              *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::COLS +
+                                         sw128(r & 63, c & 7)) =
+                  make_uint4(y[4 * q], y[4 * q + 1], y[4 * q + 2],
+                             y[4 * q + 3]);
+            }
+          };
+          // raw codes to registers, then the slot is free
+          if constexpr (DT == DT_MXFP4) {
+            uint2 w[PIECES];
+            uint32_t sw[PIECES / 4];
+#pragma unroll
+            for (int g = 0; g < PIECES; ++g)
+              w[g] = *reinterpret_cast<const uint2 *>(src + 8 * g);
+#pragma unroll
+            for (int g = 0; g < PIECES / 4; ++g)
+              sw[g] =
+                  *reinterpret_cast<const uint32_t *>(src + D / 2 + 4 * g);
+            if (dead) {
+#pragma unroll
+              for (int g = 0; g < PIECES; ++g) w[g] = make_uint2(0, 0);
+#pragma unroll
+              for (int g = 0; g < PIECES / 4; ++g) sw[g] = 0;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rawempty[rs]);
+            if (!wait_all(&empty[st], (u / NS & 1) ^ 1)) {
+              give_up();
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int g = 0; g < PIECES; ++g) {
+              const uint32_t sp = e4m3x2_to_f16x2(
+                  (uint16_t)(sw[g >> 2] >> (16 * ((g >> 1) & 1))));
+              const uint32_t s2 = prmt(sp, 0, (g & 1) ? 0x3232 : 0x1010);
+              uint32_t y[8], z[4];
+              e2m1x8_to_f16(w[g].x, z);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = mul_f16x2(z[j], s2);
+              e2m1x8_to_f16(w[g].y, z);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[4 + j] = mul_f16x2(z[j], s2);
+              put(g, y);
+            }
+          } else {
+            // rows are a power of two apart: each reads its pieces in an
+            // order of its own, so that eight rows meet all the banks
+            const int turn = D == 128 ? r & 7 : (r >> 1) & 3;
+            uint4 w[PIECES];
+#pragma unroll
+            for (int g = 0; g < PIECES; ++g) {
+              w[g] = *reinterpret_cast<const uint4 *>(src + 16 * (g ^ turn));
+              if (dead) w[g] = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rawempty[rs]);
+            if (!wait_all(&empty[st], (u / NS & 1) ^ 1)) {
+              give_up();
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int g = 0; g < PIECES; ++g) {
+              const uint32_t cw[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y[2 * j] = e4m3x2_to_f16x2((uint16_t)cw[j]);
+                y[2 * j + 1] = e4m3x2_to_f16x2((uint16_t)(cw[j] >> 16));
+              }
+              put(g ^ turn, y);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[st]);
+          if ((rs += 2) >= NR) rs -= NR, rph ^= 1;
+        }
+      } while (seg_next(p, sg, G));
+    }
+  } else if (!WIDEN && warp < 12) {
+    // ======================= queries ======================================
+    int use = 0;
+    bool ok = true;
+    do {
+      for (int t = 0; t < sg.tiles(); ++t, ++use) {
+        if (ok && !wait_all(&qempty[q_slot(use)], q_par(use) ^ 1)) {
+          give_up();
+          ok = false;
+        }
+        if (ok) load_queries(sg, t, use, tid & 127);
+      }
+    } while (seg_next(p, sg, G));
+  } else {
+    if constexpr (WIDEN) reg_dec<72>();
+    const int bs = p.block_size;
+    auto block_of = [&](int b, int lb) {
+      int pb = p.block_table[(long)b * p.max_blocks + lb];
+      if (pb < 0 || pb >= p.num_blocks) {
+        report(p.err, DEVERR_BLOCK);
+        pb = 0;  // read a valid block; the result is flagged as wrong
+      }
+      return pb;
+    };
+    if (warp == C::kLoad) {
+      // ===================== copies =======================================
+      // Pieces of a chunk: boxes of tp.box rows (bf16), or what it has of a
+      // block. Chunks are looked up 32 / L at a time: lane l takes piece l % L
+      // of chunk l / L of the batch (L: pieces a chunk may have, a power of
+      // two), and later issues that piece's copies. L = 32 and more pieces: a
+      // lane looks further ones up when it issues.
+      int L = 1;
+      if constexpr (!WIDEN) {
+        L = min(32, kN / tp.box);
+      } else {
+        while (L < 32 && L < (bs % kN == 0   ? 1
+                              : kN % bs == 0 ? kN / bs
+                                             : kN / bs + 2))
+          L <<= 1;
+      }
+      const int lq = lane & (L - 1), batch = 32 / L;
+      bool go = true;
+      int u = 0;                     // K and V units so far
+      uint32_t via = 0, par = 0;     // slots on their way through `land`, and
+                                     // its parities, a bit a slot
+      do {
+        const int c0 = sg.q.c0 + sg.k0, c1 = sg.q.c0 + sg.k1;
+        for (int cb = c0; go && cb < c1; cb += batch) {
+          // this lane's piece: positions [x0, x1), at row `at` of the cache
+          const int c = cb + lane / L;
+          int t0 = 0, t1 = 0;
+          auto piece = [&](int i, int &x0, int &x1) -> long {
+            if constexpr (!WIDEN) {
+              x0 = c * kN + i * tp.box;
+              x1 = x0 + tp.box;
+              if (i * tp.box >= kN || x1 <= t0 || x0 >= t1) {
+                x1 = x0;
+                return 0;
+              }
+            } else {
+              const int lb = t0 / bs + i;
+              x0 = max(t0, lb * bs);
+              x1 = min(t1, (lb + 1) * bs);
+              if (x0 >= x1) {
+                x1 = x0;
+                return 0;
+              }
+            }
+            const int lb = x0 / bs;
+            return ((long)block_of(sg.b, lb) * p.n_kv + sg.h) * bs +
+                   (x0 - lb * bs);
+          };
+          int x0 = 0, x1 = 0;
+          long at = 0;
+          if (c < c1) {
+            t0 = max(c * kN, sg.q.lo);
+            t1 = min((c + 1) * kN, sg.q.T);
+            if constexpr (DT == DT_MXFP4) {
+              // (rows of 72 bytes are copied in pairs; block sizes are even)
+              t0 &= ~1;
+              t1 = (t1 + 1) & ~1;
+            }
+            at = piece(lq, x0, x1);
+          }
+          const int cnt = min(batch, c1 - cb);
+          for (int j = 0; go && j < cnt; ++j) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q, ++u) {  // K, V
+              constexpr int RING = WIDEN ? NR : NS;
+              const int s = u % RING;
+              uint64_t *eb = WIDEN ? &rawempty[s] : &empty[s];
+              go = go && wait_all(eb, (u / RING & 1) ^ 1);
+              if (!go) break;
+              // a V tile of which some rows are not attended to goes through
+              // the warp that fills them with zeros
+              bool ends = false;
+              if constexpr (!WIDEN) {
+                const int p0 = (cb + j) * kN;
+                ends = q == 1 && (p0 < sg.q.lo || p0 > sg.q.T - kN);
+                via = (via & ~(1u << s)) | ((uint32_t)ends << s);
+                par ^= (uint32_t)ends << s;
+              }
+              if (lane / L == j) {
+                if constexpr (!WIDEN) {
+                  uint64_t *bar = ends ? &land[s] : &full[s];
+                  const int n = (t1 + tp.box - 1) / tp.box - t0 / tp.box;
+                  if (lq == 0)
+                    mbar_arrive_expect_tx(bar,
+                                          (uint32_t)n * tp.box * D * 2);
+                  uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
+                  const void *map = q ? &tp.tmv : &tp.tmk;
+                  for (int i = lq; i * tp.box < kN; i += L) {
+                    int a0 = x0, a1 = x1;
+                    long row = at;
+                    if (i > lq) row = piece(i, a0, a1);
+                    if (a0 >= a1) continue;
+                    const int o = i * tp.box;  // row of the chunk
+                    uint8_t *dst = tile + (o >> 6) * C::HALF + (o & 63) * 128;
+                    if (tp.box == 64) {
+                      tma_load_3d(dst, map, 0, (int)row, 0, bar);
+                    } else {
+#pragma unroll
+                      for (int z = 0; z < D / 64; ++z)
+                        tma_load_3d(dst + z * C::COLS, map, 0, (int)row, z,
+                                    bar);
+                    }
+                  }
+                } else {
+                  constexpr int ROW = row_bytes(D, DT);
+                  uint8_t *dst = smem + C::RAW_OFF + s * C::RAW;
+                  const uint8_t *src = q ? p.v : p.k;
+                  // (copies may land before the expectation is set: the phase
+                  // ends with that arrival at the earliest)
+                  if (lq == 0)
+                    mbar_arrive_expect_tx(&rawfull[s],
+                                          (uint32_t)(t1 - t0) * ROW);
+                  for (int i = lq;; i += L) {
+                    int a0 = x0, a1 = x1;
+                    long row = at;
+                    if (i > lq) row = piece(i, a0, a1);
+                    if (a0 < a1)
+                      bulk_g2s(dst + (a0 - c * kN) * ROW, src + row * ROW,
+                               (uint32_t)(a1 - a0) * ROW, &rawfull[s]);
+                    if (L < 32 || (t0 / bs + i + L) * bs >= t1) break;
+                  }
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+      } while (seg_next(p, sg, G));
+      if (!go) {
+        give_up();
+        // every copy that was issued has landed before this CTA gives its
+        // shared memory back
+        constexpr int RING = WIDEN ? NR : NS;
+        for (int i = 0; i < RING && i < u; ++i) {
+          const int x = u - 1 - i;
+          if constexpr (WIDEN) {
+            mbar_wait(&rawfull[x % RING], (x / RING) & 1);
+          } else {
+            const int s = x % RING;
+            if (via >> s & 1)
+              mbar_wait(&land[s], (par >> s & 1) ^ 1);
+            else
+              mbar_wait(&full[s], (x / RING) & 1);
+          }
+        }
+      }
+    } else if (!WIDEN && warp == C::kLoad + 1) {
+      // ===================== ends of V ====================================
+      // Rows of a chunk that no pair attends to are zeros, so that 0 times
+      // them stays 0: the copies left them as they were, or brought in what
+      // lies beside the sequence.
+      int u = 1;
+      uint32_t par = 0;  // parities of `land`, a bit a slot
+      bool ok = true;
+      do {
+        for (int k = sg.k0; ok && k < sg.k1; ++k, u += 2) {
+          const int pos0 = (sg.q.c0 + k) * kN;
+          const int a = max(sg.q.lo - pos0, 0);
+          const int z = min(sg.q.T - pos0, kN);
+          if (z - a == kN) continue;
+          const int s = u % NS;
+          if (!wait_all(&land[s], par >> s & 1)) {
+            give_up();
+            ok = false;
+            break;
+          }
+          par ^= 1u << s;
+          uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
+          // 16-byte pieces of the rows [0, a) and [z, 128)
+          constexpr int PC = D / 8;
+          const int rows = kN - (z - a);
+          for (int i = lane; i < rows * PC; i += 32) {
+            int r = i / PC;
+            const int c = i - r * PC;
+            if (r >= a) r += z - a;
+            *reinterpret_cast<uint4 *>(tile + (r >> 6) * C::HALF +
+                                       (c >> 3) * C::COLS + (r & 63) * 128 +
+                                       (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+        }
+      } while (seg_next(p, sg, G));
+    } else if (warp == C::kMma || warp == C::kMma + 1) {
+      // ===================== MMA issue ====================================
+      constexpr uint32_t idS = WIDEN ? umma_idesc_f16(kM, kS, false)
+                                     : umma_idesc_bf16(kM, kS, false);
+      constexpr uint32_t idO = WIDEN ? umma_idesc_f16(kM, D, true)
+                                     : umma_idesc_bf16(kM, D, true);
+      const uint32_t q0 = smem_u32(smem + C::Q_OFF);
+      const uint32_t kv0 = smem_u32(smem + C::KV_OFF);
+      // A step's barriers: V's, complete by then as a rule, is polled; then P's
+      // (or Q's), by a suspending wait, which leaves the issue slots to the
+      // softmax warps.
+      auto poll = [&](uint64_t *bar, uint32_t par) {
+        for (int i = 0; i < (1 << 24); ++i)
+          if (__all_sync(0xffffffffu, mbar_test_wait(bar, par))) return true;
+        return false;
+      };
+      // One warp a tile; each touches its own tensor memory only. Both see every
+      // K and V tile arrive, in their order (a barrier's phases must not pass
+      // unseen), and both let go of it: after the products that read it, or at
+      // once where the other tile's do.
+      const int t = warp - C::kMma;
+      int use = 0, gc = 0, gv = 0, seen = 0;
+      bool ok = true;
+      do {
+        const int nv = sg.steps(t), two = sg.two;
+        const int qu = use + (two ? t : 0);
+        const uint32_t qa = q0 + q_slot(qu) * C::TILE;
+        auto unit_of = [&](int v, int is_v) {
+          return 2 * (gc + chunk_of(sg, t, v)) + is_v;
+        };
+        // waits for the tiles up to unit u
+        auto need = [&](int u) {
+          for (; seen <= u; ++seen) {
+            const int st = seen % NS;
+            if (!poll(&full[st], seen / NS & 1)) return false;
+            if (!two && (((seen >> 1) - gc) & 1) != t) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&empty[st]);
+            }
+          }
+          return true;
+        };
+        // scores of step v, whose K tile is there
+        auto issue_s = [&](int v) {
+          const int st = unit_of(v, 0) % NS, buf = v & 1;
+          const uint64_t a = umma_desc_sw128(qa, 16, 1024);
+          const uint64_t bk =
+              umma_desc_sw128(kv0 + st * C::TILE + buf * C::HALF, 16, 1024);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t step = (ks & 3) * 32;
+            umma_ss_elect(tbase + kColS + 128 * t + kS * buf,
+                          a + (((ks >> 2) * 2 * C::COLS + step) >> 4),
+                          bk + (((ks >> 2) * C::COLS + step) >> 4), idS,
+                          ks > 0 ? 1u : 0u);
+          }
+          umma_commit_elect(&sfull[2 * t + buf]);
+          if (buf == 1) umma_commit_elect(&empty[st]);  // the chunk's last step
+        };
+        // both tiles' query slots are seen and let go of by both warps
+        for (int i = 0; ok && i < sg.tiles(); ++i)
+          ok = wait_all(&qfull[q_slot(use + i)], q_par(use + i));
+        // two steps of scores ahead; then per step the product with V and the
+        // scores of the step after next, into the buffer P just left
+        if (ok && nv > 0) {
+          ok = need(unit_of(0, 0));
+          tc_fence_after();
+          if (ok) {
+            issue_s(0);
+            issue_s(1);
+          }
+        }
+        for (int v = 0; ok && v < nv; ++v) {
+          const int buf = v & 1, u = unit_of(v, 1), st = u % NS;
+          if (v == nv - 2) {
+            // the unit's scores are all issued: its queries are free
+            for (int i = 0; i < sg.tiles(); ++i)
+              umma_commit_elect(&qempty[q_slot(use + i)]);
+          }
+          ok = need(u) &&
+               wait_all(&pfull[2 * t + buf], ((gv + v) >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bv = umma_desc_sw128(
+              kv0 + st * C::TILE + buf * C::HALF, C::COLS, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kS / 16; ++kk)
+            umma_ts_elect(tbase + kColO + D * t,
+                          tbase + kColS + 128 * t + kS * buf + kk * 8,
+                          bv + (uint64_t)((kk * 2048) >> 4), idO,
+                          (v > 0 || kk > 0) ? 1u : 0u);
+          umma_commit_elect(&pvdone[t]);
+          if (buf == 1) umma_commit_elect(&empty[st]);
+          if (v == nv - 1) umma_commit_elect(&odone[t]);
+          if (v + 2 < nv) {
+            ok = need(unit_of(v + 2, 0));
+            tc_fence_after();
+            if (ok) issue_s(v + 2);
+          }
+        }
+        if (ok && nv == 0)
+          for (int i = 0; i < sg.tiles(); ++i)
+            umma_commit_elect(&qempty[q_slot(use + i)]);
+        // the other tile's last ones too
+        ok = ok && need(2 * (gc + sg.nch()) - 1);
+        use += sg.tiles();
+        gc += sg.nch();
+        gv += nv;
+      } while (ok && seg_next(p, sg, G));
+      if (!ok) give_up();
+      // every MMA issued has completed before the dealloc
+      umma_commit_elect(drain);
+      mbar_wait(drain, 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();  // every read of tensor memory is done
+  if (warp == C::kMma) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int DT, int D, int QS>
+cudaError_t launch_attend_t(const TcParams &tp, cudaStream_t s) {
+  using C = ACfg<DT, D, QS>;
+  static bool done[64] = {};
+  auto kern = attend_tc_kernel<DT, D, QS>;
+  const cudaError_t e = set_smem_once(kern, C::SMEM, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(tp.p.n_splits), dim3(C::THREADS), C::SMEM, s, 1,
+                    tp);
+}
+
+}  // namespace
+
+// Caches whose rows are widened (attend_widen.cu); `one`: no unit of the
+// launch has two tiles.
+cudaError_t launch_attend_widen(const TcParams &tp, bool one, cudaStream_t s);
+
+}  // namespace kvd

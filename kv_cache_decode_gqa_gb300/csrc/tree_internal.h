@@ -19,7 +19,8 @@ struct TreePlanParams {
 };
 
 // kvd_gqa_tree (masks set) and kvd_gqa_cross (masks null). The ExtendParams
-// fields it uses keep their meaning.
+// fields it uses keep their meaning; n_splits are the CTAs, block_rows the
+// pairs that a partial result has room for.
 struct AttendParams : ExtendParams {
   const uint32_t *masks;     // [rows][words]: nodes a row sees
   const int32_t *positions;  // [rows], with a window
@@ -37,6 +38,14 @@ struct KeepParams {
 };
 
 cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s);
+// The CTAs of a call (at most `ctas`), with equal shares of its chunks, and
+// their partial results: two a CTA, of `pairs` (row, head) pairs each.
+struct AttendPlan {
+  int ctas = 1, pairs = 0;
+  size_t ws_o_bytes = 0, ws_bytes = 0;
+};
+AttendPlan attend_plan(int n_kv, int g, int d, int batch, int rows,
+                       int max_rows, int max_seq_len, int ctas);
 cudaError_t launch_attend(const AttendParams &p, cudaStream_t s);
 cudaError_t launch_keep(const KeepParams &p, cudaStream_t s);
 

@@ -96,6 +96,9 @@ def test_attention_validation(lib, call):
     assert call(lib, _cache(), _seqs(batch=1025)) == 3
     assert call(lib, _cache(), _seqs(batch=-1)) == 2
     assert call(lib, _cache(), _seqs(max_seq_len=1025)) == 4
+    assert call(lib, _cache(), _seqs(max_blocks_per_seq=2 ** 26,
+                                     max_seq_len=2 ** 31 - 1)) == 3
+    assert call(lib, _cache(num_blocks=2 ** 22)) == 3  # 2^31 rows
     assert call(lib, _cache(), _seqs(flags=4)) == 2
     assert call(lib, _cache(), _seqs(window=-1)) == 2
     assert call(lib, q=_rows(60)) == 2                 # not a multiple
