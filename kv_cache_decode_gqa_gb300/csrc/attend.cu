@@ -18,13 +18,17 @@ __global__ void __launch_bounds__(kAttendMergeThreads)
   __shared__ long scratch[33], pre[NB];
   pdl_trigger();
   const int G = p.n_h / p.n_kv, tid = threadIdx.x;
+  constexpr int SPT = (NB + kAttendMergeThreads - 1) / kAttendMergeThreads;
+  Seq sq[SPT];
   long before, total;
   int end;
-  scan_work(p, G, scratch, false, before, total, end);
+  scan_work(p, G, scratch, sq, before, total, end);
   const int per = (p.batch + kAttendMergeThreads - 1) / kAttendMergeThreads;
-  for (int b = tid * per; b < min(tid * per + per, p.batch); ++b) {
-    pre[b] = before;
-    if (b < end) before += seq_chunks(p, seq_at(p, b, G));
+#pragma unroll
+  for (int j = 0; j < SPT; ++j) {
+    if (j >= per || tid * per + j >= p.batch) continue;
+    pre[tid * per + j] = before;
+    before += seq_chunks(p, sq[j]);
   }
   __syncthreads();
   const int P = (int)min((long)p.n_splits, total);

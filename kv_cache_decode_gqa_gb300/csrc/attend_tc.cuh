@@ -37,7 +37,8 @@ constexpr int kM = 128;         // pairs per tile
 constexpr int kUnit = 256;      // pairs per unit, at most
 constexpr int kN = 128;         // positions per chunk
 constexpr int kS = 64;          // positions per product (half a chunk)
-constexpr int kSoftBar = 1;
+constexpr int kSoftBar = 9;     // the softmax warps (1-8: two of them)
+constexpr int kSeqs = 12;       // sequences of a CTA's range kept at hand
 
 // DT, D: the cache's type and head width. QS: slots for tiles of queries (1:
 // every unit of the launch has one tile).
@@ -48,13 +49,14 @@ struct ACfg {
   static constexpr int HALF = TILE / 2;       // 64 positions of a chunk
   static constexpr int COLS = 64 * 128;       // 64 rows x 64 columns
   static constexpr int RAW = kN * row_bytes(D, DT);  // cached rows of a chunk
-  // warps 0-7: softmax; then (WIDEN) 8-11 K and queries, 12-15 V, 16 copies,
-  // 17, 18 MMA issue; or 8-11 queries, 12 copies, 13 the ends of V, 14, 15 MMA
-  static constexpr int kLoad = WIDEN ? 16 : 12;
-  static constexpr int kMma = WIDEN ? 17 : 14;
-  static constexpr int THREADS = WIDEN ? 640 : 512;
+  // warps 0-15: softmax; then (WIDEN) 16-19 K and queries, 20-23 V, 24 copies,
+  // 25, 26 MMA issue; or 16-19 queries, 20 copies, 21 the ends of V, 22, 23 MMA
+  static constexpr int kLoad = WIDEN ? 24 : 20;
+  static constexpr int kMma = WIDEN ? 25 : 22;
+  static constexpr int THREADS = WIDEN ? 896 : 768;
   // K and V tiles in alternation, then (WIDEN) raw K and V rows
-  static constexpr int FIXED = (2 + QS) * kM * 4 + 768;
+  static constexpr int SCALES = WIDEN ? QS : 0;
+  static constexpr int FIXED = (2 + SCALES) * kM * 4 + 896;
   static constexpr int ROOM = 227 * 1024 - FIXED - QS * TILE;
   static constexpr int NS =
       WIDEN ? 4 : (ROOM / TILE > 12 ? 12 : ROOM / TILE);
@@ -64,11 +66,12 @@ struct ACfg {
   static constexpr int KV_OFF = QS * TILE;
   static constexpr int RAW_OFF = KV_OFF + NS * TILE;
   static constexpr int F_OFF = RAW_OFF + NR * RAW;  // float [2][128]
-  static constexpr int SL_OFF = F_OFF + 2 * kM * 4;  // float [QS][128]
-  static constexpr int BAR_OFF = SL_OFF + QS * kM * 4;
+  static constexpr int SL_OFF = F_OFF + 2 * kM * 4;  // float [SCALES][128]
+  static constexpr int BAR_OFF = SL_OFF + SCALES * kM * 4;
   static constexpr int BARS = 3 * NS + 2 * NR + 2 * QS + 13;
   static constexpr int FLAG_OFF = BAR_OFF + BARS * 8;
-  static constexpr int SMEM = FLAG_OFF + 64;
+  static constexpr int SEQ_OFF = FLAG_OFF + 32;  // Seq [kSeqs]
+  static constexpr int SMEM = SEQ_OFF + kSeqs * 32;
   static_assert(NS >= 4 && (!WIDEN || NR >= 2) && SMEM <= 227 * 1024,
                 "shared memory");
   static_assert(RAW % 128 == 0 && FLAG_OFF % 8 == 0, "alignment");
@@ -78,15 +81,6 @@ struct ACfg {
 // tile.
 __device__ __forceinline__ uint32_t sw128(int r, int c) {
   return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
-}
-
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Packed pairs of fp32 values, one instruction for both.
@@ -116,6 +110,50 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// named_sync that says whether any of its threads passes `yes`.
+__device__ __forceinline__ bool named_any(int id, int count, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((uint32_t)yes)
+      : "memory");
+  return r != 0;
+}
+
+// 8 columns of this thread's lane of tensor memory, waited for, and back.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, "
+      "[%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr,
+                                         const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, "
+      "%7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// 32 bytes at once, on a 32-byte boundary.
+__device__ __forceinline__ void st_global_v8(float *dst, const float *y) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                   dst),
+               "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]),
+               "f"(y[5]), "f"(y[6]), "f"(y[7])
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // the work: every chunk of every unit, in the order (sequence, kv head, block
 // of pairs, chunk); the CTAs take equal consecutive ranges
@@ -125,9 +163,12 @@ struct Seq {
   int r0, n;    // its rows (n = 0: skipped, or none)
   int T, ctx;   // positions, and those before the tree (cross: all)
   int lo;       // first position that a row attends to
-  int c0, nch;  // first chunk, chunks
+  int nch;      // chunks
   int blocks;   // blocks of pairs
+  int pad;
+  __device__ __forceinline__ int c0() const { return lo / kN; }
 };
+static_assert(sizeof(Seq) == 32, "shared memory");
 
 __device__ __forceinline__ Seq seq_at(const AttendParams &p, int b, int G) {
   Seq q;
@@ -142,8 +183,7 @@ __device__ __forceinline__ Seq seq_at(const AttendParams &p, int b, int G) {
     if (p.window > 0) q.lo = max(q.lo, max(q.ctx, 0) - (p.window - 1));
     q.lo = min(q.lo, max(q.ctx, 0));
   }
-  q.c0 = q.lo / kN;
-  q.nch = q.n > 0 && q.lo < q.T ? (q.T + kN - 1) / kN - q.c0 : 0;
+  q.nch = q.n > 0 && q.lo < q.T ? (q.T + kN - 1) / kN - q.c0() : 0;
   q.blocks = (int)(((long)q.n * G + kUnit - 1) / kUnit);
   return q;
 }
@@ -154,50 +194,54 @@ __device__ __forceinline__ long seq_chunks(const AttendParams &p,
 }
 
 // Exclusive prefix sums of the sequences' chunks over the block's threads:
-// thread t has the sequences [t per, t per + per), per = ceil(batch /
-// blockDim). `end`: the list's first descent (or the batch). `scratch` int64
-// [32] and one int behind it. With `flag` the block reports what does not fit.
+// thread t has the (at most SPT) sequences [t per, t per + per), per =
+// ceil(batch / blockDim), and keeps them in `q`; those from the list's first
+// descent on, which `end` receives, have no chunks. `scratch`: int64 [33].
 // Ends with a barrier.
+template <int SPT>
 __device__ __forceinline__ void scan_work(const AttendParams &p, int G,
-                                          long *scratch, bool flag, long &before,
-                                          long &total, int &end) {
+                                          long *scratch, Seq (&q)[SPT],
+                                          long &before, long &total,
+                                          int &end) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-  const int per = (p.batch + nt - 1) / nt;
-  const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-  end = p.batch;
-  while (true) {
-    bool broken = false;
-    long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      broken |= b < end && descends(p, b);
-      if (b < end) sum += seq_chunks(p, seq_at(p, b, G));
-    }
-    long x = sum;
+  const int per = (p.batch + nt - 1) / nt, b0 = tid * per;
+  bool broken = false;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += y;
+  for (int j = 0; j < SPT; ++j) {
+    q[j].nch = q[j].n = q[j].blocks = 0;
+    if (j < per && b0 + j < p.batch) {
+      q[j] = seq_at(p, b0 + j, G);
+      broken |= descends(p, b0 + j);
     }
-    if (lane == 31) scratch[warp] = x;
-    const int any = __syncthreads_or(broken);
-    before = x - sum;
-    total = 0;
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) before += scratch[w];
-      total += scratch[w];
-    }
-    if (!any) break;
+  }
+  end = p.batch;
+  if (__syncthreads_or(broken)) {
     end = first_descent(p, reinterpret_cast<int *>(scratch + 32));
+#pragma unroll
+    for (int j = 0; j < SPT; ++j)
+      if (b0 + j >= end) q[j].nch = q[j].n = q[j].blocks = 0;
   }
-  if (flag) {
-    for (int b = b0; b < b1; ++b) {
-      const bool rows = p.row_start && p.row_start[b] != p.row_start[b + 1];
-      if ((rows && (b >= end || seq_at(p, b, G).n == 0)) ||
-          p.seq_lens[b] > p.max_seq_len)
-        report(p.err, DEVERR_LEN);
-    }
+  long sum = 0;
+#pragma unroll
+  for (int j = 0; j < SPT; ++j) sum += seq_chunks(p, q[j]);
+  long x = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
   }
+  if (lane == 31) scratch[warp] = x;
+  __syncthreads();
+  long w = lane < nw ? scratch[lane] : 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long y = __shfl_up_sync(0xffffffffu, w, off);
+    if (lane >= off) w += y;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const long upto = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  before = (warp > 0 ? upto : 0) + x - sum;
   __syncthreads();
 }
 
@@ -213,69 +257,67 @@ __device__ __forceinline__ int share_of(long x, long total, int P) {
   return c;
 }
 
+// Where a role is in its CTA's range. A role's loops keep this much only and
+// look the rest up (Seg) when a unit begins and ends: what registers cannot
+// hold goes to local memory, which beside this much shared memory means L2.
+struct Walk {
+  int b, unit;  // sequence, unit of it (kv head major, blocks of pairs)
+  int k0;       // first chunk of the unit
+  long left;    // chunks from here on
+};
+
 // A CTA's run of chunks of one unit.
 struct Seg {
   Seq q;
-  int b, h, m;     // sequence, kv head, block of pairs
-  int f0, np;      // its first pair, pairs
-  int k0, k1;      // chunks of the unit, [k0, k1) of q.nch
-  long left;       // chunks of the range from this segment on
-  bool two;        // two tiles
-  __device__ __forceinline__ int nch() const { return k1 - k0; }
-  __device__ __forceinline__ bool whole() const {
-    return k0 == 0 && k1 == q.nch;
-  }
+  int h;        // kv head
+  int f0, np;   // first pair, pairs
+  int k0, nch;  // its chunks, [k0, k0 + nch) of q.nch
+  bool two;     // two tiles
+  __device__ __forceinline__ int c0() const { return q.c0() + k0; }
+  __device__ __forceinline__ bool whole() const { return nch == q.nch; }
   // chunks that tile t takes part in, two steps each
   __device__ __forceinline__ int steps(int t) const {
-    return two ? 2 * nch() : (nch() - t + 1) & ~1;
+    return two ? 2 * nch : (nch - t + 1) & ~1;
   }
   __device__ __forceinline__ int tiles() const { return two ? 2 : 1; }
 };
 
-// Step v of tile t: half v & 1 of a chunk of the segment.
-__device__ __forceinline__ int chunk_of(const Seg &s, int t, int v) {
-  return s.two ? v >> 1 : (v & ~1) + t;
+// Step v of tile t: half v & 1 of this chunk of the segment.
+__device__ __forceinline__ int chunk_of(bool two, int t, int v) {
+  return two ? v >> 1 : (v & ~1) + t;
 }
 
-__device__ __forceinline__ void seg_unit(const AttendParams &p, Seg &s,
-                                         int G) {
-  s.f0 = s.m * kUnit;
+// Sequence b of the range; `near`: b0 .. b0 + kSeqs - 1.
+__device__ __forceinline__ Seq seq_near(const AttendParams &p, int b, int G,
+                                        const Seq *near, int b0) {
+  return b - b0 < kSeqs ? near[b - b0] : seq_at(p, b, G);
+}
+
+__device__ __forceinline__ Seg seg_at(const AttendParams &p, const Walk &w,
+                                      int G, const Seq *near, int b0) {
+  Seg s;
+  s.q = seq_near(p, w.b, G, near, b0);
+  s.h = w.unit / s.q.blocks;
+  s.f0 = (w.unit - s.h * s.q.blocks) * kUnit;
   s.np = min(s.q.n * G - s.f0, kUnit);
   s.two = s.np > kM;
-  s.k1 = (int)min((long)s.q.nch, s.k0 + s.left);
-}
-
-// The segment at chunk `off` of sequence b's.
-__device__ __forceinline__ Seg seg_first(const AttendParams &p, int b,
-                                         long off, long left, int G) {
-  Seg s;
-  s.b = b;
-  s.q = seq_at(p, b, G);
-  s.left = left;
-  const long unit = off / s.q.nch;
-  s.k0 = (int)(off - unit * s.q.nch);
-  s.h = (int)(unit / s.q.blocks);
-  s.m = (int)(unit - (long)s.h * s.q.blocks);
-  seg_unit(p, s, G);
+  s.k0 = w.k0;
+  s.nch = (int)min((long)(s.q.nch - s.k0), w.left);
   return s;
 }
 
-// On to the next segment; false at the range's end.
-__device__ __forceinline__ bool seg_next(const AttendParams &p, Seg &s,
-                                         int G) {
-  s.left -= s.nch();
-  if (s.left <= 0) return false;
-  s.k0 = 0;
-  if (++s.m == s.q.blocks) {
-    s.m = 0;
-    if (++s.h == p.n_kv) {
-      s.h = 0;
-      do {
-        s.q = seq_at(p, ++s.b, G);
-      } while (seq_chunks(p, s.q) == 0);
-    }
+// On to the segment after `s`; false at the range's end.
+__device__ __forceinline__ bool walk_on(const AttendParams &p, Walk &w,
+                                        const Seg &s, int G, const Seq *near,
+                                        int b0) {
+  w.left -= s.nch;
+  if (w.left <= 0) return false;
+  w.k0 = 0;
+  if (++w.unit == p.n_kv * s.q.blocks) {
+    w.unit = 0;
+    do ++w.b;
+    while (seq_near(p, w.b, G, near, b0).nch == 0);
   }
-  seg_unit(p, s, G);
   return true;
 }
 
@@ -333,50 +375,14 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
   int *s_b = flags + 1;
   long *s_off = reinterpret_cast<long *>(flags + 2);
 
+  Seq *near = reinterpret_cast<Seq *>(smem + C::SEQ_OFF);
+
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.n_h / p.n_kv;
 
-  pdl_wait();
-  pdl_trigger();  // after the wait: the merge launch never overlaps this
-                  // launch's predecessor
-  // ---- this CTA's share ------------------------------------------------
-  long lo, hi;
-  {
-    long before, total;
-    int end;
-    scan_work(p, G, reinterpret_cast<long *>(smem), blockIdx.x == 0, before,
-              total, end);
-    // rows that see nothing
-    for (int b = blockIdx.x; b < end; b += gridDim.x) {
-      const Seq q = seq_at(p, b, G);
-      if (q.n == 0 || q.nch > 0) continue;
-      for (long i = tid; i < (long)q.n * p.n_h * (D / 8); i += C::THREADS)
-        reinterpret_cast<uint4 *>(p.out + (long)q.r0 * p.n_h * D)[i] =
-            make_uint4(0, 0, 0, 0);
-      if (p.lse)
-        for (long i = tid; i < (long)q.n * p.n_h; i += C::THREADS)
-          p.lse[(long)q.r0 * p.n_h + i] = -INFINITY;
-    }
-    const int P = (int)min((long)gridDim.x, total);
-    const int c = blockIdx.x;
-    if (c >= P) return;
-    lo = share_lo(c, total, P);
-    hi = share_lo(c + 1, total, P);
-    const int per = (p.batch + C::THREADS - 1) / C::THREADS;
-    for (int b = tid * per; b < min(tid * per + per, end); ++b) {
-      const long n = seq_chunks(p, seq_at(p, b, G));
-      if (lo >= before && lo < before + n) {
-        *s_b = b;
-        *s_off = lo - before;
-      }
-      before += n;
-    }
-  }
+  // ---- what needs nothing of the launch before --------------------------
   // the swizzled tiles assume 1 KB atoms (every CTA sees the same layout)
-  if ((smem_u32(smem) & 1023u) != 0) {
-    if (tid == 0) report(p.err, DEVERR_TIMEOUT);
-    return;
-  }
+  const bool placed = (smem_u32(smem) & 1023u) == 0;
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], WIDEN ? 4 : 1);
@@ -390,11 +396,11 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
     for (int i = 0; i < QS; ++i) {
       mbar_init(&qfull[i], 4);
       // a commit of either MMA warp (and the softmax warps have the scales)
-      mbar_init(&qempty[i], WIDEN ? 10 : 2);
+      mbar_init(&qempty[i], WIDEN ? 18 : 2);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[i], 8);
     }
     mbar_init(&pvdone[0], 1);
     mbar_init(&pvdone[1], 1);
@@ -411,7 +417,77 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *s_tmem;
-  Seg sg = seg_first(p, *s_b, *s_off, hi - lo, G);
+  pdl_wait();
+  pdl_trigger();  // after the wait: the merge launch never overlaps this
+                  // launch's predecessor
+  // ---- this CTA's share ------------------------------------------------
+  long lo = 0, hi = 0;
+  {
+    constexpr int SPT = (kMaxDecodeBatch + C::THREADS - 1) / C::THREADS;
+    Seq q[SPT];
+    long before, total;
+    int end;
+    scan_work(p, G, reinterpret_cast<long *>(smem), q, before, total, end);
+    const int P = (int)min((long)gridDim.x, total), c = blockIdx.x;
+    if (c < P) {
+      lo = share_lo(c, total, P);
+      hi = share_lo(c + 1, total, P);
+    }
+    const int per = (p.batch + C::THREADS - 1) / C::THREADS, b0 = tid * per;
+    bool zeros = false;  // rows that see nothing, of sequences of this CTA
+#pragma unroll
+    for (int j = 0; j < SPT; ++j) {
+      const int b = b0 + j;
+      if (j >= per || b >= p.batch) continue;
+      const long n = seq_chunks(p, q[j]);
+      if (lo < hi && lo >= before && lo < before + n) {
+        *s_b = b;
+        *s_off = lo - before;
+      }
+      before += n;
+      zeros |= q[j].n > 0 && q[j].nch == 0 && b % gridDim.x == c;
+      if (c == 0) {
+        const bool rows = p.row_start && p.row_start[b] != p.row_start[b + 1];
+        if ((rows && q[j].n == 0) || p.seq_lens[b] > p.max_seq_len)
+          report(p.err, DEVERR_LEN);
+      }
+    }
+    if (__syncthreads_or(zeros)) {
+      for (int b = c; b < end; b += gridDim.x) {
+        const Seq s = seq_at(p, b, G);
+        if (s.n == 0 || s.nch > 0) continue;
+        for (long i = tid; i < (long)s.n * p.n_h * (D / 8); i += C::THREADS)
+          reinterpret_cast<uint4 *>(p.out + (long)s.r0 * p.n_h * D)[i] =
+              make_uint4(0, 0, 0, 0);
+        if (p.lse)
+          for (long i = tid; i < (long)s.n * p.n_h; i += C::THREADS)
+            p.lse[(long)s.r0 * p.n_h + i] = -INFINITY;
+      }
+    }
+    if (lo < hi) {
+#pragma unroll
+      for (int j = 0; j < SPT; ++j) {
+        const int i = b0 + j - *s_b;
+        if (j < per && b0 + j < p.batch && i >= 0 && i < kSeqs) near[i] = q[j];
+      }
+    }
+    __syncthreads();
+  }
+  if (!placed && tid == 0) report(p.err, DEVERR_TIMEOUT);
+  if (lo >= hi || !placed) {
+    if (warp == C::kMma) tmem_dealloc(tbase, 512);
+    return;
+  }
+  const int b_near = *s_b;
+  Walk wk;
+  wk.b = b_near;
+  wk.unit = (int)(*s_off / near[0].nch);
+  wk.k0 = (int)(*s_off % near[0].nch);
+  wk.left = hi - lo;
+  auto here = [&]() { return seg_at(p, wk, G, near, b_near); };
+  auto next = [&](const Seg &s) {
+    return walk_on(p, wk, s, G, near, b_near);
+  };
   // Every wait is bounded. A role whose wait runs out goes on without waiting
   // and without touching what it waited for; the others follow when their own
   // waits run out.
@@ -443,11 +519,14 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                                  sw128(r & 63, c & 7)) = w;
     };
     if constexpr (!WIDEN) {
-      uint4 x[D / 8];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) x[c] = at(c);
+      for (int c0 = 0; c0 < D / 8; c0 += 8) {
+        uint4 x[8];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) put(c, x[c]);
+        for (int c = 0; c < 8; ++c) x[c] = at(c0 + c);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) put(c0 + c, x[c]);
+      }
     } else {
       // twice over the row, with few registers: its largest magnitude first
       uint32_t m = 0;
@@ -490,39 +569,46 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
     if (lane == 0) mbar_arrive(&qfull[q_slot(use)]);
   };
 
-  if (warp < 8) {
+  if (warp < 16) {
     // ======================= softmax ======================================
-    if constexpr (WIDEN) reg_inc<128>();
-    const int t = warp >> 2;
+    // Two threads a pair and step, of 32 columns each.
+    const int t = (warp >> 2) & 1, hf = warp >> 3;
     const int r = (warp & 3) * 32 + lane;  // pair of the tile
+    const int pairbar = 1 + 4 * t + (warp & 3);
     const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     int use = 0;              // query slots used so far
-    int gv = 0, units = 0;    // steps and units of this tile so far
+    int gv = 0, units = 0;    // steps (pairs of them) and units so far
     bool ok = true;
     while (true) {
-      const bool two = sg.two;
-      const int ri = two ? t * kM + r : r;  // pair of the unit
-      const bool live = ri < sg.np;
-      const int f = sg.f0 + ri;
-      const int row = live ? sg.q.r0 + f / G : 0;
+      // ---- what the steps need -------------------------------------------
       // what the pair sees (one that does not exist: everything, so that its
       // warp masks nothing for it; its query is 0 and nothing of it is stored)
-      int vlo = 0, vctx = INT_MAX;
-      const uint32_t *mask = nullptr;
-      if (live) {
-        vlo = p.win_start ? max(p.win_start[sg.b], 0) : 0;
-        vctx = sg.q.ctx;
-        if (p.masks) {
-          mask = p.masks + (long)row * p.words;
-          if (p.window > 0)
-            vlo = max(vlo, max(p.positions[row], vctx) - (p.window - 1));
+      int vlo = 0, vctx = INT_MAX, row = -1;
+      int nv, first, nodes;
+      bool two, live;
+      {
+        const Seg sg = here();
+        two = sg.two;
+        nv = sg.steps(t);
+        first = sg.c0() * kN + 32 * hf;
+        nodes = sg.q.n;
+        const int ri = two ? t * kM + r : r;  // pair of the unit
+        live = ri < sg.np;
+        if (live) {
+          vlo = p.win_start ? max(p.win_start[wk.b], 0) : 0;
+          vctx = sg.q.ctx;
+          if (p.masks) {
+            row = sg.q.r0 + (sg.f0 + ri) / G;
+            if (p.window > 0)
+              vlo = max(vlo, max(p.positions[row], vctx) - (p.window - 1));
+          }
         }
       }
       const bool warp_live = __any_sync(0xffffffffu, live);
       float sl = p.scale_log2;
       if constexpr (WIDEN) {
         // (the other tile's slot is released here too)
-        for (int i = 0; i < sg.tiles(); ++i) {
+        for (int i = 0; i <= (int)two; ++i) {
           if (ok && !wait_all(&qfull[q_slot(use + i)], q_par(use + i))) {
             give_up();
             ok = false;
@@ -536,100 +622,98 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           if (two) mbar_arrive(&qempty[q_slot(use + 1)]);
         }
       }
-      use += sg.tiles();
+      use += two ? 2 : 1;
       float ref = -INFINITY, l = 0.f;
-      const uint64_t sl2 = pack_f32x2(sl, sl);
-      const int nv = sg.steps(t);
-      for (int v = 0; ok && v < nv; ++v) {
-        const int buf = v & 1, g = gv + v;
-        const int pos0 =
-            (sg.q.c0 + sg.k0 + chunk_of(sg, t, v)) * kN + buf * kS;
-        if (!wait_all(&sfull[2 * t + buf], (g >> 1) & 1)) {
+      for (int v = 0; v < nv; ++v) {
+        const int buf = v & 1;
+        const int p0 = first + chunk_of(two, t, v) * kN + buf * kS;
+        if (ok && !wait_all(&sfull[2 * t + buf], (gv + (v >> 1)) & 1)) {
           give_up();
           ok = false;
-          break;
         }
         tc_fence_after();
         if (warp_live) {
-          uint32_t x[2][32];
-          const uint32_t ts = tl + kColS + 128 * t + kS * buf;
+          uint32_t x[32];
+          const uint32_t ts = tl + kColS + 128 * t + kS * buf + 32 * hf;
+          tmem_ld32(ts, x);
+          tmem_wait_ld(x);
+          // columns that some pair of the warp does not see
+          if (__any_sync(0xffffffffu, p0 < vlo || p0 > vctx - 32)) {
+            const uint32_t *mask =
+                row >= 0 ? p.masks + (long)row * p.words : nullptr;
+            const uint32_t bits =
+                live ? seen_bits(p0, vlo, vctx, nodes, mask, p.words)
+                     : 0xffffffffu;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, x[i]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) tmem_wait_ld(x[i]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int p0 = pos0 + 32 * i;
-            // 32 columns that some pair of the warp sees in part
-            if (__any_sync(0xffffffffu, p0 < vlo || p0 > vctx - 32)) {
-              const uint32_t bits =
-                  live ? seen_bits(p0, vlo, vctx, sg.q.n, mask, p.words)
-                       : 0xffffffffu;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(bits >> j & 1)) x[i][j] = 0xff800000u;  // -inf
-            }
+            for (int j = 0; j < 32; ++j)
+              if (!(bits >> j & 1)) x[j] = 0xff800000u;  // -inf
           }
           float mx[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t *y = &x[i >> 1][16 * (i & 1)];
+            const uint32_t *y = &x[8 * i];
             mx[i] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 #pragma unroll
-            for (int j = 2; j < 16; j += 2)
+            for (int j = 2; j < 8; j += 2)
               mx[i] = max3(mx[i], __uint_as_float(y[j]),
                            __uint_as_float(y[j + 1]));
           }
-          const float top =
-              fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl - kHead;
-          const bool grow = top > ref + kSlack;  // from -inf: any score
-          if (__any_sync(0xffffffffu, grow)) {
+          float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl - kHead;
+          // from -inf: any score
+          if (named_any(pairbar, 64, top > ref + kSlack)) {
+            // the larger of the two threads' maxima (a NaN stays out)
+            if (hf == 1) fs[t * kM + r] = top;
+            named_sync(pairbar, 64);
+            if (hf == 0) {
+              top = fmaxf(top, fs[t * kM + r]);
+              fs[t * kM + r] = top;
+            }
+            named_sync(pairbar, 64);
+            if (hf == 1) top = fs[t * kM + r];
+            const bool grow = top > ref + kSlack;
             const float al = grow ? ex2(ref - top) : 1.f;
             if (grow) ref = top;
             l *= al;
             if (v > 0) {
               // the tile's last product into O has to be over (this step's
-              // scores followed the one before it)
-              if (!wait_all(&pvdone[t], (g - 1) & 1)) {
+              // scores followed the one before it); half of its columns each
+              if (ok && !wait_all(&pvdone[t], (v - 1) & 1)) {
                 give_up();
                 ok = false;
-                break;
               }
               tc_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int i = 0; i < D / 16; ++i) {
-                uint32_t o[16];
-                const uint32_t to = tl + kColO + D * t + 16 * i;
-                tmem_ld16(to, o);
-                tmem_wait_ld16(o);
+                uint32_t o[8];
+                const uint32_t to =
+                    tl + kColO + D * t + hf * (D / 2) + 8 * i;
+                tmem_ld8(to, o);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 8; ++j)
                   o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
-                tmem_st16(to, o);
+                tmem_st8(to, o);
               }
             }
           }
           const float mu = ref == -INFINITY ? 0.f : ref;
           const uint64_t mu2 = pack_f32x2(-mu, -mu);
+          const uint64_t sl2 = pack_f32x2(sl, sl);
           uint64_t ls[2] = {0, 0};
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float e0, e1;
-              unpack_f32x2(
-                  fma_f32x2(pack_f32x2(__uint_as_float(x[i][2 * j]),
-                                       __uint_as_float(x[i][2 * j + 1])),
-                            sl2, mu2),
-                  e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              ls[j & 1] = add_f32x2(ls[j & 1], pack_f32x2(e0, e1));
-              pk[j] = WIDEN ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
-            }
-            tmem_st16(ts + 16 * i, pk);
+          for (int j = 0; j < 16; ++j) {
+            float e0, e1;
+            unpack_f32x2(
+                fma_f32x2(pack_f32x2(__uint_as_float(x[2 * j]),
+                                     __uint_as_float(x[2 * j + 1])),
+                          sl2, mu2),
+                e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            ls[j & 1] = add_f32x2(ls[j & 1], pack_f32x2(e0, e1));
+            pk[j] = WIDEN ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
           }
+          tmem_st16(ts, pk);  // over this thread's own scores
           {
             float a0, a1;
             unpack_f32x2(add_f32x2(ls[0], ls[1]), a0, a1);
@@ -642,7 +726,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         if (lane == 0) mbar_arrive(&pfull[2 * t + buf]);
       }
       // ---- epilogue ------------------------------------------------------
-      gv += nv;
+      gv += nv >> 1;
       if (nv > 0) {
         if (ok && !wait_all(&odone[t], units & 1)) {
           give_up();
@@ -651,58 +735,68 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         ++units;
       }
       tc_fence_after();
+      // (looked up again: see Walk)
+      asm volatile("" : "+r"(wk.b), "+r"(wk.unit), "+r"(wk.k0));
+      const Seg sg = here();
+      const int ri = two ? t * kM + r : r, f = sg.f0 + ri;
+      // the sums of a pair's two threads
+      if (hf == 1) fs[t * kM + r] = l;
+      named_sync(pairbar, 64);
+      if (hf == 0) l += fs[t * kM + r];
       // the outputs' factors (of the tile's sums, and of tile 1's in one-tile
       // units) and the log-sum-exp
-      float w0, w1 = 0.f, lse;
+      float w0, w1 = 0.f, lse = 0.f;
       auto finish = [&](float M, float L) {
         lse = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
         return L == 0.f ? 0.f : DT == DT_FP8 ? p.v_scale[sg.h] / L : 1.f / L;
       };
       if (two) {
-        w0 = finish(ref, l);
+        if (hf == 0) fs[t * kM + r] = w0 = finish(ref, l);
+        named_sync(pairbar, 64);
+        if (hf == 1) w0 = fs[t * kM + r];
       } else {
-        // the halves' states of pair r, joined by tile 0's thread
-        if (t == 1) fs[r] = ref, fs[kM + r] = l;
+        // the two tiles' states of pair r, joined by tile 0's first thread
         tc_fence_before();
-        named_sync(kSoftBar, 2 * kM);
+        named_sync(kSoftBar, 512);
         tc_fence_after();
-        if (t == 0) {
+        if (t == 1 && hf == 0) fs[r] = ref, fs[kM + r] = l;
+        named_sync(kSoftBar, 512);
+        if (t == 0 && hf == 0) {
           const float rb = fs[r], M = fmaxf(ref, rb);
           const float mu = M == -INFINITY ? 0.f : M;
           w0 = ex2(ref - mu);
           w1 = ex2(rb - mu);
           const float inv = finish(M, l * w0 + fs[kM + r] * w1);
-          w0 *= inv, w1 *= inv;
-          fs[r] = w0, fs[kM + r] = w1;
+          fs[r] = w0 * inv, fs[kM + r] = w1 * inv;
         }
-        named_sync(kSoftBar, 2 * kM);
-        if (t == 1) w0 = fs[r], w1 = fs[kM + r];
+        named_sync(kSoftBar, 512);
+        w0 = fs[r], w1 = fs[kM + r];
       }
-      // two tiles: all columns of the tile's pair; one: the halves write half
-      // of them each
-      const int ncol = two ? D : D / 2;
-      const int col0 = two ? 0 : t * (D / 2);
+      // two tiles: a thread has half of the columns of its tile's pair; one: a
+      // quarter
+      const int ncol = two ? D / 2 : D / 4;
+      const int col0 = (two ? hf : 2 * t + hf) * ncol;
       const uint32_t ta = tl + kColO + (two ? D * t : 0) + col0;
-      const bool second = !two && sg.nch() > 1;
+      const bool second = !two && sg.nch > 1;
       const bool whole = sg.whole();
-      const long at = (long)row * p.n_h + (long)sg.h * G + f % G;
+      const long at =
+          ((long)sg.q.r0 + f / G) * p.n_h + (long)sg.h * G + f % G;
       const long part = ((long)blockIdx.x * 2 + (sg.k0 > 0 ? 0 : 1)) *
                             p.block_rows + ri;
       if (warp_live && ok) {
 #pragma unroll 1
-        for (int g = 0; g < ncol; g += 32) {
-          uint32_t o[32];
-          tmem_ld32(ta + g, o);
-          tmem_wait_ld(o);
-          float y[32];
+        for (int g = 0; g < ncol; g += 16) {
+          uint32_t o[16];
+          tmem_ld16(ta + g, o);
+          tmem_wait_ld16(o);
+          float y[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            y[i] = __uint_as_float(o[i]) * w0;
+          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]) * w0;
           if (second) {
-            tmem_ld32(ta + D + g, o);
-            tmem_wait_ld(o);
+            tmem_ld16(ta + D + g, o);
+            tmem_wait_ld16(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 16; ++i)
               y[i] = fmaf(__uint_as_float(o[i]), w1, y[i]);
           }
           if (live) {
@@ -710,22 +804,19 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
               uint4 *dst =
                   reinterpret_cast<uint4 *>(p.out + at * D + col0 + g);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 2; ++i)
                 dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]),
                                     pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
                                     pack_bf16x2(y[8 * i + 4], y[8 * i + 5]),
                                     pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
             } else {
-              float4 *dst =
-                  reinterpret_cast<float4 *>(p.ws_o + part * D + col0 + g);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2],
-                                     y[4 * i + 3]);
+              float *dst = p.ws_o + part * D + col0 + g;
+              st_global_v8(dst, y);
+              st_global_v8(dst + 8, y + 8);
             }
           }
         }
-        if (live && (two || t == 0)) {
+        if (live && hf == 0 && (two || t == 0)) {
           if (!whole)
             p.ws_lse[part] = lse;
           else if (p.lse)
@@ -733,22 +824,22 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         }
       }
       tc_fence_before();
-      // (the next unit's products into O and its states wait for both halves'
-      // reads)
-      if (!two) named_sync(kSoftBar, 2 * kM);
-      if (!seg_next(p, sg, G)) break;
+      // (the next unit's products into O and its states wait for all reads)
+      if (!two) named_sync(kSoftBar, 512);
+      if (!next(sg)) break;
     }
-  } else if (WIDEN && warp < 16) {
+  } else if (WIDEN && warp < 24) {
     // ======================= queries, widening ============================
     if constexpr (WIDEN) {
-      reg_dec<72>();
       const int r = tid & 127;  // row of the chunk
-      const bool is_v = warp >= 12;
+      const bool is_v = warp >= 20;
       int use = 0, gc = 0;
       bool ok = true;
       // K rows are raw units 0, 2, 4, ..., V rows 1, 3, 5, ...
       int rs = is_v, rph = 0;
+      Seg sg;
       do {
+        sg = here();
         if (!is_v) {
           for (int t = 0; t < sg.tiles(); ++t, ++use) {
             if (ok && !wait_all(&qempty[q_slot(use)], q_par(use) ^ 1)) {
@@ -758,7 +849,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
             if (ok) load_queries(sg, t, use, r);
           }
         }
-        for (int i = 0; ok && i < sg.nch(); ++i, ++gc) {
+        for (int i = 0; ok && i < sg.nch; ++i, ++gc) {
           if (!wait_all(&rawfull[rs], rph)) {
             give_up();
             ok = false;
@@ -766,7 +857,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           }
           const uint8_t *src =
               smem + C::RAW_OFF + rs * C::RAW + r * row_bytes(D, DT);
-          const int pos = (sg.q.c0 + sg.k0 + i) * kN + r;
+          const int pos = (sg.c0() + i) * kN + r;
           // a row that was not copied, or that no pair sees: zeros, so that 0
           // times it stays 0
           const bool dead = pos < sg.q.lo || pos >= sg.q.T;
@@ -855,13 +946,15 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           if (lane == 0) mbar_arrive(&full[st]);
           if ((rs += 2) >= NR) rs -= NR, rph ^= 1;
         }
-      } while (seg_next(p, sg, G));
+      } while (next(sg));
     }
-  } else if (!WIDEN && warp < 12) {
+  } else if (!WIDEN && warp < 20) {
     // ======================= queries ======================================
     int use = 0;
     bool ok = true;
+    Seg sg;
     do {
+      sg = here();
       for (int t = 0; t < sg.tiles(); ++t, ++use) {
         if (ok && !wait_all(&qempty[q_slot(use)], q_par(use) ^ 1)) {
           give_up();
@@ -869,9 +962,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         }
         if (ok) load_queries(sg, t, use, tid & 127);
       }
-    } while (seg_next(p, sg, G));
+    } while (next(sg));
   } else {
-    if constexpr (WIDEN) reg_dec<72>();
     const int bs = p.block_size;
     auto block_of = [&](int b, int lb) {
       int pb = p.block_table[(long)b * p.max_blocks + lb];
@@ -890,23 +982,26 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       // lane looks further ones up when it issues.
       int L = 1;
       if constexpr (!WIDEN) {
-        L = min(32, kN / tp.box);
+        L = min(32, kN >> (__ffs(tp.box) - 1));
       } else {
         while (L < 32 && L < (bs % kN == 0   ? 1
                               : kN % bs == 0 ? kN / bs
                                              : kN / bs + 2))
           L <<= 1;
       }
-      const int lq = lane & (L - 1), batch = 32 / L;
+      const int shift = __ffs(L) - 1, lq = lane & (L - 1), batch = 32 >> shift;
+      const int mine = lane >> shift, bshift = WIDEN ? 0 : __ffs(tp.box) - 1;
       bool go = true;
       int u = 0;                     // K and V units so far
       uint32_t via = 0, par = 0;     // slots on their way through `land`, and
                                      // its parities, a bit a slot
+      Seg sg;
       do {
-        const int c0 = sg.q.c0 + sg.k0, c1 = sg.q.c0 + sg.k1;
+        sg = here();
+        const int c0 = sg.c0(), c1 = c0 + sg.nch;
         for (int cb = c0; go && cb < c1; cb += batch) {
           // this lane's piece: positions [x0, x1), at row `at` of the cache
-          const int c = cb + lane / L;
+          const int c = cb + mine;
           int t0 = 0, t1 = 0;
           auto piece = [&](int i, int &x0, int &x1) -> long {
             if constexpr (!WIDEN) {
@@ -926,7 +1021,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
               }
             }
             const int lb = x0 / bs;
-            return ((long)block_of(sg.b, lb) * p.n_kv + sg.h) * bs +
+            return ((long)block_of(wk.b, lb) * p.n_kv + sg.h) * bs +
                    (x0 - lb * bs);
           };
           int x0 = 0, x1 = 0;
@@ -959,13 +1054,14 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                 via = (via & ~(1u << s)) | ((uint32_t)ends << s);
                 par ^= (uint32_t)ends << s;
               }
-              if (lane / L == j) {
+              if (mine == j) {
                 if constexpr (!WIDEN) {
                   uint64_t *bar = ends ? &land[s] : &full[s];
-                  const int n = (t1 + tp.box - 1) / tp.box - t0 / tp.box;
+                  const int n =
+                      ((t1 + tp.box - 1) >> bshift) - (t0 >> bshift);
                   if (lq == 0)
                     mbar_arrive_expect_tx(bar,
-                                          (uint32_t)n * tp.box * D * 2);
+                                          (uint32_t)(n << bshift) * D * 2);
                   uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
                   const void *map = q ? &tp.tmv : &tp.tmk;
                   for (int i = lq; i * tp.box < kN; i += L) {
@@ -1008,7 +1104,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
             }
           }
         }
-      } while (seg_next(p, sg, G));
+      } while (next(sg));
       if (!go) {
         give_up();
         // every copy that was issued has landed before this CTA gives its
@@ -1035,9 +1131,11 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       int u = 1;
       uint32_t par = 0;  // parities of `land`, a bit a slot
       bool ok = true;
+      Seg sg;
       do {
-        for (int k = sg.k0; ok && k < sg.k1; ++k, u += 2) {
-          const int pos0 = (sg.q.c0 + k) * kN;
+        sg = here();
+        for (int k = 0; ok && k < sg.nch; ++k, u += 2) {
+          const int pos0 = (sg.c0() + k) * kN;
           const int a = max(sg.q.lo - pos0, 0);
           const int z = min(sg.q.T - pos0, kN);
           if (z - a == kN) continue;
@@ -1064,7 +1162,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[s]);
         }
-      } while (seg_next(p, sg, G));
+      } while (next(sg));
     } else if (warp == C::kMma || warp == C::kMma + 1) {
       // ===================== MMA issue ====================================
       constexpr uint32_t idS = WIDEN ? umma_idesc_f16(kM, kS, false)
@@ -1088,12 +1186,15 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       const int t = warp - C::kMma;
       int use = 0, gc = 0, gv = 0, seen = 0;
       bool ok = true;
+      Seg sg;
       do {
-        const int nv = sg.steps(t), two = sg.two;
+        sg = here();
+        const int nv = sg.steps(t);
+        const bool two = sg.two;
         const int qu = use + (two ? t : 0);
         const uint32_t qa = q0 + q_slot(qu) * C::TILE;
         auto unit_of = [&](int v, int is_v) {
-          return 2 * (gc + chunk_of(sg, t, v)) + is_v;
+          return 2 * (gc + chunk_of(two, t, v)) + is_v;
         };
         // waits for the tiles up to unit u
         auto need = [&](int u) {
@@ -1153,7 +1254,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
 #pragma unroll
           for (int kk = 0; kk < kS / 16; ++kk)
             umma_ts_elect(tbase + kColO + D * t,
-                          tbase + kColS + 128 * t + kS * buf + kk * 8,
+                          tbase + kColS + 128 * t + kS * buf + (kk >> 1) * 32 +
+                              (kk & 1) * 8,
                           bv + (uint64_t)((kk * 2048) >> 4), idO,
                           (v > 0 || kk > 0) ? 1u : 0u);
           umma_commit_elect(&pvdone[t]);
@@ -1169,11 +1271,11 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           for (int i = 0; i < sg.tiles(); ++i)
             umma_commit_elect(&qempty[q_slot(use + i)]);
         // the other tile's last ones too
-        ok = ok && need(2 * (gc + sg.nch()) - 1);
+        ok = ok && need(2 * (gc + sg.nch) - 1);
         use += sg.tiles();
-        gc += sg.nch();
+        gc += sg.nch;
         gv += nv;
-      } while (ok && seg_next(p, sg, G));
+      } while (ok && next(sg));
       if (!ok) give_up();
       // every MMA issued has completed before the dealloc
       umma_commit_elect(drain);
