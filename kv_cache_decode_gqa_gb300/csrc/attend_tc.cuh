@@ -110,6 +110,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+__device__ __forceinline__ int uniform(int x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // named_sync that says whether any of its threads passes `yes`.
 __device__ __forceinline__ bool named_any(int id, int count, bool yes) {
   uint32_t r;
@@ -377,7 +381,10 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
 
   Seq *near = reinterpret_cast<Seq *>(smem + C::SEQ_OFF);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (through a shuffle: the compiler then knows the warp's number, and what
+  // follows from it, to be the same for its lanes, and keeps the operands of
+  // the MMAs in uniform registers)
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int G = p.n_h / p.n_kv;
 
   // ---- what needs nothing of the launch before --------------------------
@@ -1189,8 +1196,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       Seg sg;
       do {
         sg = here();
-        const int nv = sg.steps(t);
-        const bool two = sg.two;
+        const int nv = uniform(sg.steps(t)), nch = uniform(sg.nch);
+        const bool two = uniform(sg.two);
         const int qu = use + (two ? t : 0);
         const uint32_t qa = q0 + q_slot(qu) * C::TILE;
         auto unit_of = [&](int v, int is_v) {
@@ -1226,7 +1233,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           if (buf == 1) umma_commit_elect(&empty[st]);  // the chunk's last step
         };
         // both tiles' query slots are seen and let go of by both warps
-        for (int i = 0; ok && i < sg.tiles(); ++i)
+        for (int i = 0; ok && i <= (int)two; ++i)
           ok = wait_all(&qfull[q_slot(use + i)], q_par(use + i));
         // two steps of scores ahead; then per step the product with V and the
         // scores of the step after next, into the buffer P just left
@@ -1242,7 +1249,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           const int buf = v & 1, u = unit_of(v, 1), st = u % NS;
           if (v == nv - 2) {
             // the unit's scores are all issued: its queries are free
-            for (int i = 0; i < sg.tiles(); ++i)
+            for (int i = 0; i <= (int)two; ++i)
               umma_commit_elect(&qempty[q_slot(use + i)]);
           }
           ok = need(u) &&
@@ -1268,12 +1275,12 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           }
         }
         if (ok && nv == 0)
-          for (int i = 0; i < sg.tiles(); ++i)
+          for (int i = 0; i <= (int)two; ++i)
             umma_commit_elect(&qempty[q_slot(use + i)]);
         // the other tile's last ones too
-        ok = ok && need(2 * (gc + sg.nch) - 1);
-        use += sg.tiles();
-        gc += sg.nch;
+        ok = ok && need(2 * (gc + nch) - 1);
+        use += two ? 2 : 1;
+        gc += nch;
         gv += nv;
       } while (ok && next(sg));
       if (!ok) give_up();
