@@ -6,16 +6,20 @@ namespace kvd {
 namespace {
 
 // Log-sum-exp merge of the units that several CTAs of the launch before share:
-// a lane a float4 of an output row, up to 8 parts' loads in flight. A CTA is
-// small enough to sit beside one of that launch, so that the work is scanned
-// and the rows' parts are found while it still runs (it lets this one start
-// only after its own predecessor has completed).
+// CTA (c - 1, y) looks whether that launch's CTA c is the first to begin inside
+// a unit, and then merges the unit's parts of every gridDim.y-th group of
+// pairs, a lane a float4 of an output row and up to 8 parts' loads in flight.
+// The work is scanned and the unit found while the other launch's last CTAs
+// still run (it lets this one start only after its own predecessor has
+// completed).
 constexpr int kAttendMergeThreads = 256;
 
 template <int D, int NB>
 __global__ void __launch_bounds__(kAttendMergeThreads)
     attend_merge_kernel(const __grid_constant__ AttendParams p) {
-  __shared__ long scratch[33], pre[NB];
+  __shared__ long scratch[33], s_start;
+  __shared__ int s_seq;
+  __shared__ Seq s_q;
   pdl_trigger();
   const int G = p.n_h / p.n_kv, tid = threadIdx.x;
   constexpr int SPT = (NB + kAttendMergeThreads - 1) / kAttendMergeThreads;
@@ -23,63 +27,60 @@ __global__ void __launch_bounds__(kAttendMergeThreads)
   long before, total;
   int end;
   scan_work(p, G, scratch, sq, before, total, end);
+  const int P = (int)min((long)p.n_splits, total), c = blockIdx.x + 1;
+  if (c >= P) return;
+  const long x = share_lo(c, total, P);
   const int per = (p.batch + kAttendMergeThreads - 1) / kAttendMergeThreads;
 #pragma unroll
   for (int j = 0; j < SPT; ++j) {
     if (j >= per || tid * per + j >= p.batch) continue;
-    pre[tid * per + j] = before;
-    before += seq_chunks(p, sq[j]);
+    const long n = seq_chunks(p, sq[j]);
+    if (x >= before && x < before + n) {
+      s_seq = tid * per + j;
+      s_start = before;
+      s_q = sq[j];
+    }
+    before += n;
   }
   __syncthreads();
-  const int P = (int)min((long)p.n_splits, total);
-  constexpr int LANES = D / 4;  // of a row
-  const long at = (long)blockIdx.x * (kAttendMergeThreads / LANES) +
-                  tid / LANES;
-  const int e4 = tid % LANES;
-  int parts = 0, first = 0, ri = 0;
-  if (at < (long)p.rows * p.n_h) {
-    const int row = (int)(at / p.n_h), head = (int)(at - (long)row * p.n_h);
-    int b = 0;
-    Seq q{};
-    for (; b < end; ++b) {
-      const int r0 = p.row_start ? p.row_start[b] : b;
-      const int r1 = p.row_start ? p.row_start[b + 1] : b + 1;
-      if (row >= r0 && row < r1) {
-        q = seq_at(p, b, G);
-        break;
-      }
-    }
-    if (q.n > 0 && q.nch > 0) {
-      const int f = (row - q.r0) * G + head % G, m = f / kUnit;
-      ri = f - m * kUnit;
-      const long u =
-          pre[b] + ((long)(head / G) * q.blocks + m) * q.nch;
-      first = share_of(u, total, P);
-      parts = share_of(u + q.nch - 1, total, P) - first + 1;
-    }
-  }
+  const Seq q = s_q;
+  const int len = q.nch + p.gap;
+  const int unit = (int)((x - s_start) / len);
+  const long u = s_start + (long)unit * len;  // its first chunk
+  // begun by CTA c - 1 and not over when CTA c begins?
+  if (u == x || share_lo(c - 1, total, P) > u || x - u >= q.nch) return;
+  const int parts = share_of(u + q.nch - 1, total, P) - (c - 1) + 1;
+  const int h = unit / q.blocks, f0 = (unit - h * q.blocks) * kUnit;
+  const int np = min(q.n * G - f0, kUnit);
   pdl_wait();
-  if (parts <= 1) return;  // written whole, or no sequence's row
-  float M, W;
-  float4 acc;
-  quad_merge<1>(p.ws_lse, p.ws_o, p.block_rows, D, ri, ri * LANES + e4, parts,
-                [&](int i) { return (long)(first + i) * 2 + (i == 0); }, M, W,
-                acc);
-  const float iw = W == 0.f ? 0.f : 1.f / W;
-  uint2 packed;
-  packed.x = pack_bf16x2(acc.x * iw, acc.y * iw);
-  packed.y = pack_bf16x2(acc.z * iw, acc.w * iw);
-  reinterpret_cast<uint2 *>(p.out + at * D)[e4] = packed;
-  if (e4 == 0 && p.lse) p.lse[at] = W == 0.f ? -INFINITY : M + logf(W);
+  constexpr int LANES = D / 4, ROWS = kAttendMergeThreads / LANES;
+  const int e4 = tid % LANES;
+  for (int ri = blockIdx.y * ROWS + tid / LANES; ri < np;
+       ri += gridDim.y * ROWS) {
+    float M, W;
+    float4 acc;
+    quad_merge<1>(p.ws_lse, p.ws_o, p.block_rows, D, ri, ri * LANES + e4,
+                  parts,
+                  [&](int i) { return (long)(c - 1 + i) * 2 + (i == 0); }, M, W,
+                  acc);
+    const float iw = W == 0.f ? 0.f : 1.f / W;
+    const int f = f0 + ri;
+    const long at = ((long)q.r0 + f / G) * p.n_h + (long)h * G + f % G;
+    uint2 packed;
+    packed.x = pack_bf16x2(acc.x * iw, acc.y * iw);
+    packed.y = pack_bf16x2(acc.z * iw, acc.w * iw);
+    reinterpret_cast<uint2 *>(p.out + at * D)[e4] = packed;
+    if (e4 == 0 && p.lse) p.lse[at] = W == 0.f ? -INFINITY : M + logf(W);
+  }
 }
 
 template <int D>
 cudaError_t launch_merge(const AttendParams &p, cudaStream_t s) {
-  const long rows = (long)p.rows * p.n_h;
-  const long per = kAttendMergeThreads / (D / 4);
-  const dim3 grid((unsigned)((rows + per - 1) / per));
-  return launch_pdl(p.batch <= kMergeSmallBatch
-                        ? attend_merge_kernel<D, kMergeSmallBatch>
+  // a row or two a warp
+  const int rows = 2 * kAttendMergeThreads / (D / 4);
+  const dim3 grid(p.n_splits - 1, (p.block_rows + rows - 1) / rows);
+  return launch_pdl(p.batch <= kAttendMergeThreads
+                        ? attend_merge_kernel<D, kAttendMergeThreads>
                         : attend_merge_kernel<D, kMaxDecodeBatch>,
                     grid, dim3(kAttendMergeThreads), 0, s, 1, p);
 }
@@ -115,6 +116,7 @@ AttendPlan attend_plan(int n_kv, int g, int d, int batch, int rows,
                     kUnit);
   const long chunks = units * (((long)max_seq_len + kN - 1) / kN);
   pl.ctas = (int)std::max(1L, std::min((long)ctas, chunks));
+  if (chunks >= 8L * pl.ctas) pl.gap = kUnitGap;
   if (pl.ctas > 1) {
     const size_t slots = (size_t)pl.ctas * 2 * pl.pairs;
     pl.ws_o_bytes = (slots * d * 4 + 255) / 256 * 256;

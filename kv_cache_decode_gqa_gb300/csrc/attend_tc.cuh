@@ -37,7 +37,7 @@ constexpr int kM = 128;         // pairs per tile
 constexpr int kUnit = 256;      // pairs per unit, at most
 constexpr int kN = 128;         // positions per chunk
 constexpr int kS = 64;          // positions per product (half a chunk)
-constexpr int kSoftBar = 9;     // the softmax warps (1-8: two of them)
+constexpr int kSoftBar = 1;     // named barrier of the softmax warps
 constexpr int kSeqs = 12;       // sequences of a CTA's range kept at hand
 
 // DT, D: the cache's type and head width. QS: slots for tiles of queries (1:
@@ -49,11 +49,12 @@ struct ACfg {
   static constexpr int HALF = TILE / 2;       // 64 positions of a chunk
   static constexpr int COLS = 64 * 128;       // 64 rows x 64 columns
   static constexpr int RAW = kN * row_bytes(D, DT);  // cached rows of a chunk
-  // warps 0-15: softmax; then (WIDEN) 16-19 K and queries, 20-23 V, 24 copies,
-  // 25, 26 MMA issue; or 16-19 queries, 20 copies, 21 the ends of V, 22, 23 MMA
-  static constexpr int kLoad = WIDEN ? 24 : 20;
-  static constexpr int kMma = WIDEN ? 25 : 22;
-  static constexpr int THREADS = WIDEN ? 896 : 768;
+  // warps: 0-7 softmax; then four of queries (WIDEN: and K), (WIDEN) four of V,
+  // copies, (bf16) the ends of V, two of MMA issue
+  static constexpr int SOFT = 8;
+  static constexpr int kLoad = SOFT + (WIDEN ? 8 : 4);
+  static constexpr int kMma = kLoad + (WIDEN ? 1 : 2);
+  static constexpr int THREADS = (SOFT + (WIDEN ? 12 : 8)) * 32;
   // K and V tiles in alternation, then (WIDEN) raw K and V rows
   static constexpr int SCALES = WIDEN ? QS : 0;
   static constexpr int FIXED = (2 + SCALES) * kM * 4 + 896;
@@ -110,22 +111,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ int uniform(int x) {
-  return __shfl_sync(0xffffffffu, x, 0);
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// named_sync that says whether any of its threads passes `yes`.
-__device__ __forceinline__ bool named_any(int id, int count, bool yes) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "bar.red.or.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"((uint32_t)yes)
-      : "memory");
-  return r != 0;
+__device__ __forceinline__ int uniform(int x) {
+  return __shfl_sync(0xffffffffu, x, 0);
 }
 
 // 8 columns of this thread's lane of tensor memory, waited for, and back.
@@ -192,9 +188,11 @@ __device__ __forceinline__ Seq seq_at(const AttendParams &p, int b, int G) {
   return q;
 }
 
+// A unit counts as its chunks and p.gap empty ones behind them, which stand for
+// what a change of units costs the CTA that makes it.
 __device__ __forceinline__ long seq_chunks(const AttendParams &p,
                                            const Seq &q) {
-  return (long)p.n_kv * q.blocks * q.nch;
+  return q.nch == 0 ? 0 : (long)p.n_kv * q.blocks * (q.nch + p.gap);
 }
 
 // Exclusive prefix sums of the sequences' chunks over the block's threads:
@@ -275,7 +273,7 @@ struct Seg {
   Seq q;
   int h;        // kv head
   int f0, np;   // first pair, pairs
-  int k0, nch;  // its chunks, [k0, k0 + nch) of q.nch
+  int k0, nch;  // its chunks, [k0, k0 + nch) of q.nch; none in a gap
   bool two;     // two tiles
   __device__ __forceinline__ int c0() const { return q.c0() + k0; }
   __device__ __forceinline__ bool whole() const { return nch == q.nch; }
@@ -306,7 +304,7 @@ __device__ __forceinline__ Seg seg_at(const AttendParams &p, const Walk &w,
   s.np = min(s.q.n * G - s.f0, kUnit);
   s.two = s.np > kM;
   s.k0 = w.k0;
-  s.nch = (int)min((long)(s.q.nch - s.k0), w.left);
+  s.nch = (int)min((long)max(s.q.nch - s.k0, 0), w.left);
   return s;
 }
 
@@ -314,7 +312,7 @@ __device__ __forceinline__ Seg seg_at(const AttendParams &p, const Walk &w,
 __device__ __forceinline__ bool walk_on(const AttendParams &p, Walk &w,
                                         const Seg &s, int G, const Seq *near,
                                         int b0) {
-  w.left -= s.nch;
+  w.left -= s.q.nch + p.gap - s.k0;
   if (w.left <= 0) return false;
   w.k0 = 0;
   if (++w.unit == p.n_kv * s.q.blocks) {
@@ -401,13 +399,13 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       mbar_init(&rawempty[i], 4);
     }
     for (int i = 0; i < QS; ++i) {
-      mbar_init(&qfull[i], 4);
+      mbar_init(&qfull[i], WIDEN ? 8 : 4);
       // a commit of either MMA warp (and the softmax warps have the scales)
-      mbar_init(&qempty[i], WIDEN ? 18 : 2);
+      mbar_init(&qempty[i], WIDEN ? 2 + C::SOFT : 2);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 8);
+      mbar_init(&pfull[i], 4);
     }
     mbar_init(&pvdone[0], 1);
     mbar_init(&pvdone[1], 1);
@@ -488,13 +486,21 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
   const int b_near = *s_b;
   Walk wk;
   wk.b = b_near;
-  wk.unit = (int)(*s_off / near[0].nch);
-  wk.k0 = (int)(*s_off % near[0].nch);
+  wk.unit = (int)(*s_off / (near[0].nch + p.gap));
+  wk.k0 = (int)(*s_off % (near[0].nch + p.gap));
   wk.left = hi - lo;
   auto here = [&]() { return seg_at(p, wk, G, near, b_near); };
   auto next = [&](const Seg &s) {
     return walk_on(p, wk, s, G, near, b_near);
   };
+  {
+    // a range that begins in a gap; all of it may be one
+    const Seg s = here();
+    if (s.nch == 0 && !next(s)) {
+      if (warp == C::kMma) tmem_dealloc(tbase, 512);
+      return;
+    }
+  }
   // Every wait is bounded. A role whose wait runs out goes on without waiting
   // and without touching what it waited for; the others follow when their own
   // waits run out.
@@ -508,67 +514,58 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
   auto q_slot = [&](int use) { return use % QS; };
   auto q_par = [&](int use) { return (uint32_t)(use / QS & 1); };
 
-  // A tile of queries by 128 threads, a pair each (WIDEN: scaled into f16).
-  auto load_queries = [&](const Seg &s, int t, int use, int r) {
-    const int ri = t * kM + r;
-    const bool live = ri < s.np;
-    const int f = s.f0 + ri;
+  // Rows [r0, r0 + ROWS) of a tile of queries by 128 threads: side by side, so
+  // that the loads are whole lines, several in flight a thread (WIDEN: scaled
+  // into f16).
+  constexpr int ROWS = WIDEN ? 64 : 128;
+  auto load_queries = [&](const Seg &s, int t, int use, int x, int r0) {
+    constexpr int LPR = D / 8, RP = 128 / LPR;  // lanes a row, rows at a time
+    constexpr int NF = WIDEN ? 4 : 8;
+    const int c = x % LPR;
+    int r = r0 + x / LPR;
+    int f = s.f0 + t * kM + r, row = s.q.r0 + f / G, g = f % G;
+    const int dr = RP / G, dg = RP % G;
     uint8_t *qt = smem + C::Q_OFF + q_slot(use) * C::TILE;
-    const uint16_t *src = p.q + (long)(s.q.r0 + f / G) * p.q_rs +
-                          ((long)s.h * G + f % G) * p.q_hs;
-    auto at = [&](int c) {
-      return live ? reinterpret_cast<const uint4 *>(src)[c]
-                  : make_uint4(0, 0, 0, 0);
-    };
-    // 64 rows of 64 columns lie 8 KB apart, columns from 64 on behind all rows
-    auto put = [&](int c, const uint4 &w) {
-      *reinterpret_cast<uint4 *>(qt + ((c >> 3) * 2 + (r >> 6)) * C::COLS +
-                                 sw128(r & 63, c & 7)) = w;
-    };
-    if constexpr (!WIDEN) {
-#pragma unroll
-      for (int c0 = 0; c0 < D / 8; c0 += 8) {
-        uint4 x[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = at(c0 + c);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) put(c0 + c, x[c]);
-      }
-    } else {
-      // twice over the row, with few registers: its largest magnitude first
-      uint32_t m = 0;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D / 8; c0 += 8) {
-        uint4 x[8];
+    for (int i0 = 0; i0 < ROWS / RP; i0 += NF) {
+      uint4 w[NF];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = at(c0 + c);
+      for (int i = 0; i < NF; ++i) {
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (t * kM + r + i * RP < s.np)
+          w[i] = *reinterpret_cast<const uint4 *>(
+              p.q + (long)row * p.q_rs + ((long)s.h * G + g) * p.q_hs + c * 8);
+        row += dr, g += dg;
+        if (g >= G) ++row, g -= G;
+      }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          m = __vmaxu2(m,
-                       __vmaxu2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu));
-          m = __vmaxu2(m,
-                       __vmaxu2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu));
+      for (int i = 0; i < NF; ++i) {
+        if constexpr (WIDEN) {
+          uint32_t m =
+              __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                       __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+          m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+          for (int off = 1; off < LPR; off <<= 1)
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+          const int e = row_exponent(m);
+          const float sc = __uint_as_float((uint32_t)e << 23);
+          if (c == 0)
+            qsl[q_slot(use) * kM + r] =
+                fmaxf(p.scale_log2 * (DT == DT_FP8 ? p.k_scale[s.h] : 1.f) *
+                          exp2f((float)(127 - e)),
+                      1.17549435e-38f);
+          w[i] = make_uint4(
+              pack_f16x2(bf16lo(w[i].x) * sc, bf16hi(w[i].x) * sc),
+              pack_f16x2(bf16lo(w[i].y) * sc, bf16hi(w[i].y) * sc),
+              pack_f16x2(bf16lo(w[i].z) * sc, bf16hi(w[i].z) * sc),
+              pack_f16x2(bf16lo(w[i].w) * sc, bf16hi(w[i].w) * sc));
         }
-      }
-      m = max(m & 0xffffu, m >> 16);
-      const int e = row_exponent(m);
-      const float sc = __uint_as_float((uint32_t)e << 23);
-      const float ks = DT == DT_FP8 ? p.k_scale[s.h] : 1.f;
-      qsl[q_slot(use) * kM + r] = fmaxf(
-          p.scale_log2 * ks * exp2f((float)(127 - e)), 1.17549435e-38f);
-#pragma unroll 1
-      for (int c0 = 0; c0 < D / 8; c0 += 4) {
-        uint4 x[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = at(c0 + c);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          put(c0 + c,
-              make_uint4(pack_f16x2(bf16lo(x[c].x) * sc, bf16hi(x[c].x) * sc),
-                         pack_f16x2(bf16lo(x[c].y) * sc, bf16hi(x[c].y) * sc),
-                         pack_f16x2(bf16lo(x[c].z) * sc, bf16hi(x[c].z) * sc),
-                         pack_f16x2(bf16lo(x[c].w) * sc,
-                                    bf16hi(x[c].w) * sc)));
+        // 64 rows of 64 columns lie 8 KB apart, columns from 64 on behind all
+        // rows
+        *reinterpret_cast<uint4 *>(qt + ((c >> 3) * 2 + (r >> 6)) * C::COLS +
+                                   sw128(r & 63, c & 7)) = w[i];
+        r += RP;
       }
     }
     fence_proxy_async_smem();
@@ -576,12 +573,11 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
     if (lane == 0) mbar_arrive(&qfull[q_slot(use)]);
   };
 
-  if (warp < 16) {
+  if (warp < C::SOFT) {
     // ======================= softmax ======================================
-    // Two threads a pair and step, of 32 columns each.
-    const int t = (warp >> 2) & 1, hf = warp >> 3;
+    if constexpr (WIDEN) reg_inc<128>();
+    const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // pair of the tile
-    const int pairbar = 1 + 4 * t + (warp & 3);
     const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     int use = 0;              // query slots used so far
     int gv = 0, units = 0;    // steps (pairs of them) and units so far
@@ -597,7 +593,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         const Seg sg = here();
         two = sg.two;
         nv = sg.steps(t);
-        first = sg.c0() * kN + 32 * hf;
+        first = sg.c0() * kN;
         nodes = sg.q.n;
         const int ri = two ? t * kM + r : r;  // pair of the unit
         live = ri < sg.np;
@@ -640,60 +636,56 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         }
         tc_fence_after();
         if (warp_live) {
-          uint32_t x[32];
-          const uint32_t ts = tl + kColS + 128 * t + kS * buf + 32 * hf;
-          tmem_ld32(ts, x);
-          tmem_wait_ld(x);
+          uint32_t x[2][32];
+          const uint32_t ts = tl + kColS + 128 * t + kS * buf;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, x[i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) tmem_wait_ld(x[i]);
           // columns that some pair of the warp does not see
-          if (__any_sync(0xffffffffu, p0 < vlo || p0 > vctx - 32)) {
+          if (__any_sync(0xffffffffu, p0 < vlo || p0 > vctx - kS)) {
             const uint32_t *mask =
                 row >= 0 ? p.masks + (long)row * p.words : nullptr;
-            const uint32_t bits =
-                live ? seen_bits(p0, vlo, vctx, nodes, mask, p.words)
-                     : 0xffffffffu;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(bits >> j & 1)) x[j] = 0xff800000u;  // -inf
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t bits =
+                  live ? seen_bits(p0 + 32 * i, vlo, vctx, nodes, mask,
+                                   p.words)
+                       : 0xffffffffu;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(bits >> j & 1)) x[i][j] = 0xff800000u;  // -inf
+            }
           }
           float mx[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t *y = &x[8 * i];
+            const uint32_t *y = &x[i >> 1][16 * (i & 1)];
             mx[i] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 #pragma unroll
-            for (int j = 2; j < 8; j += 2)
+            for (int j = 2; j < 16; j += 2)
               mx[i] = max3(mx[i], __uint_as_float(y[j]),
                            __uint_as_float(y[j + 1]));
           }
-          float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl - kHead;
-          // from -inf: any score
-          if (named_any(pairbar, 64, top > ref + kSlack)) {
-            // the larger of the two threads' maxima (a NaN stays out)
-            if (hf == 1) fs[t * kM + r] = top;
-            named_sync(pairbar, 64);
-            if (hf == 0) {
-              top = fmaxf(top, fs[t * kM + r]);
-              fs[t * kM + r] = top;
-            }
-            named_sync(pairbar, 64);
-            if (hf == 1) top = fs[t * kM + r];
-            const bool grow = top > ref + kSlack;
+          const float top =
+              fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl - kHead;
+          const bool grow = top > ref + kSlack;  // from -inf: any score
+          if (__any_sync(0xffffffffu, grow)) {
             const float al = grow ? ex2(ref - top) : 1.f;
             if (grow) ref = top;
             l *= al;
             if (v > 0) {
               // the tile's last product into O has to be over (this step's
-              // scores followed the one before it); half of its columns each
+              // scores followed the one before it)
               if (ok && !wait_all(&pvdone[t], (v - 1) & 1)) {
                 give_up();
                 ok = false;
               }
               tc_fence_after();
 #pragma unroll 1
-              for (int i = 0; i < D / 16; ++i) {
+              for (int i = 0; i < D / 8; ++i) {
                 uint32_t o[8];
-                const uint32_t to =
-                    tl + kColO + D * t + hf * (D / 2) + 8 * i;
+                const uint32_t to = tl + kColO + D * t + 8 * i;
                 tmem_ld8(to, o);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -706,21 +698,25 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           const uint64_t mu2 = pack_f32x2(-mu, -mu);
           const uint64_t sl2 = pack_f32x2(sl, sl);
           uint64_t ls[2] = {0, 0};
-          uint32_t pk[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float e0, e1;
-            unpack_f32x2(
-                fma_f32x2(pack_f32x2(__uint_as_float(x[2 * j]),
-                                     __uint_as_float(x[2 * j + 1])),
-                          sl2, mu2),
-                e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            ls[j & 1] = add_f32x2(ls[j & 1], pack_f32x2(e0, e1));
-            pk[j] = WIDEN ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float e0, e1;
+              unpack_f32x2(
+                  fma_f32x2(pack_f32x2(__uint_as_float(x[i][2 * j]),
+                                       __uint_as_float(x[i][2 * j + 1])),
+                            sl2, mu2),
+                  e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              ls[j & 1] = add_f32x2(ls[j & 1], pack_f32x2(e0, e1));
+              pk[j] = WIDEN ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+            }
+            // (over the scores of its own pair, which it has read)
+            tmem_st16(ts + 16 * i, pk);
           }
-          tmem_st16(ts, pk);  // over this thread's own scores
           {
             float a0, a1;
             unpack_f32x2(add_f32x2(ls[0], ls[1]), a0, a1);
@@ -746,10 +742,6 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       asm volatile("" : "+r"(wk.b), "+r"(wk.unit), "+r"(wk.k0));
       const Seg sg = here();
       const int ri = two ? t * kM + r : r, f = sg.f0 + ri;
-      // the sums of a pair's two threads
-      if (hf == 1) fs[t * kM + r] = l;
-      named_sync(pairbar, 64);
-      if (hf == 0) l += fs[t * kM + r];
       // the outputs' factors (of the tile's sums, and of tile 1's in one-tile
       // units) and the log-sum-exp
       float w0, w1 = 0.f, lse = 0.f;
@@ -758,72 +750,78 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         return L == 0.f ? 0.f : DT == DT_FP8 ? p.v_scale[sg.h] / L : 1.f / L;
       };
       if (two) {
-        if (hf == 0) fs[t * kM + r] = w0 = finish(ref, l);
-        named_sync(pairbar, 64);
-        if (hf == 1) w0 = fs[t * kM + r];
+        w0 = finish(ref, l);
       } else {
-        // the two tiles' states of pair r, joined by tile 0's first thread
+        // the two tiles' states of pair r, joined by tile 0's thread
+        if (t == 1) fs[r] = ref, fs[kM + r] = l;
         tc_fence_before();
-        named_sync(kSoftBar, 512);
+        named_sync(kSoftBar, 256);
         tc_fence_after();
-        if (t == 1 && hf == 0) fs[r] = ref, fs[kM + r] = l;
-        named_sync(kSoftBar, 512);
-        if (t == 0 && hf == 0) {
+        if (t == 0) {
           const float rb = fs[r], M = fmaxf(ref, rb);
           const float mu = M == -INFINITY ? 0.f : M;
           w0 = ex2(ref - mu);
           w1 = ex2(rb - mu);
           const float inv = finish(M, l * w0 + fs[kM + r] * w1);
-          fs[r] = w0 * inv, fs[kM + r] = w1 * inv;
+          fs[r] = w0 *= inv, fs[kM + r] = w1 *= inv;
         }
-        named_sync(kSoftBar, 512);
+        named_sync(kSoftBar, 256);
         w0 = fs[r], w1 = fs[kM + r];
       }
-      // two tiles: a thread has half of the columns of its tile's pair; one: a
-      // quarter
-      const int ncol = two ? D / 2 : D / 4;
-      const int col0 = (two ? hf : 2 * t + hf) * ncol;
-      const uint32_t ta = tl + kColO + (two ? D * t : 0) + col0;
-      const bool second = !two && sg.nch > 1;
       const bool whole = sg.whole();
       const long at =
           ((long)sg.q.r0 + f / G) * p.n_h + (long)sg.h * G + f % G;
       const long part = ((long)blockIdx.x * 2 + (sg.k0 > 0 ? 0 : 1)) *
                             p.block_rows + ri;
+      // two tiles: all columns of the tile's pair, 64 at a time; one: half of
+      // them by each tile's thread, 32 at a time of either tile's sums
+      const bool second = !two && sg.nch > 1;
+      const int col0 = two ? 0 : t * (D / 2), step = two ? 64 : 32;
+      const uint32_t to = tl + kColO + (two ? D * t : 0);
+      auto emit = [&](int col, const float (&y)[32]) {
+        if (whole) {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]),
+                                pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                pack_bf16x2(y[8 * i + 4], y[8 * i + 5]),
+                                pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st_global_v8(p.ws_o + part * D + col + 8 * i, y + 8 * i);
+        }
+      };
       if (warp_live && ok) {
 #pragma unroll 1
-        for (int g = 0; g < ncol; g += 16) {
-          uint32_t o[16];
-          tmem_ld16(ta + g, o);
-          tmem_wait_ld16(o);
-          float y[16];
+        for (int g = col0; g < (two ? D : col0 + D / 2); g += step) {
+          uint32_t o[2][32];
+          tmem_ld32(to + g, o[0]);
+          if (two)
+            tmem_ld32(to + g + 32, o[1]);
+          else
+            tmem_ld32(to + D + (second ? g : col0), o[1]);
+          tmem_wait_ld(o[0]);
+          tmem_wait_ld(o[1]);
+          float y[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]) * w0;
+          for (int i = 0; i < 32; ++i)
+            y[i] = __uint_as_float(o[0][i]) * w0;
           if (second) {
-            tmem_ld16(ta + D + g, o);
-            tmem_wait_ld16(o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              y[i] = fmaf(__uint_as_float(o[i]), w1, y[i]);
+            for (int i = 0; i < 32; ++i)
+              y[i] = fmaf(__uint_as_float(o[1][i]), w1, y[i]);
           }
-          if (live) {
-            if (whole) {
-              uint4 *dst =
-                  reinterpret_cast<uint4 *>(p.out + at * D + col0 + g);
+          if (live) emit(g, y);
+          if (two) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]),
-                                    pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
-                                    pack_bf16x2(y[8 * i + 4], y[8 * i + 5]),
-                                    pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
-            } else {
-              float *dst = p.ws_o + part * D + col0 + g;
-              st_global_v8(dst, y);
-              st_global_v8(dst + 8, y + 8);
-            }
+            for (int i = 0; i < 32; ++i)
+              y[i] = __uint_as_float(o[1][i]) * w0;
+            if (live) emit(g + 32, y);
           }
         }
-        if (live && hf == 0 && (two || t == 0)) {
+        if (live && (two || t == 0)) {
           if (!whole)
             p.ws_lse[part] = lse;
           else if (p.lse)
@@ -832,14 +830,15 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       }
       tc_fence_before();
       // (the next unit's products into O and its states wait for all reads)
-      if (!two) named_sync(kSoftBar, 512);
+      if (!two) named_sync(kSoftBar, 256);
       if (!next(sg)) break;
     }
-  } else if (WIDEN && warp < 24) {
+  } else if (WIDEN && warp < C::SOFT + 8) {
     // ======================= queries, widening ============================
     if constexpr (WIDEN) {
+      reg_dec<72>();
       const int r = tid & 127;  // row of the chunk
-      const bool is_v = warp >= 20;
+      const bool is_v = warp >= C::SOFT + 4;
       int use = 0, gc = 0;
       bool ok = true;
       // K rows are raw units 0, 2, 4, ..., V rows 1, 3, 5, ...
@@ -847,14 +846,12 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       Seg sg;
       do {
         sg = here();
-        if (!is_v) {
-          for (int t = 0; t < sg.tiles(); ++t, ++use) {
-            if (ok && !wait_all(&qempty[q_slot(use)], q_par(use) ^ 1)) {
-              give_up();
-              ok = false;
-            }
-            if (ok) load_queries(sg, t, use, r);
+        for (int t = 0; t < sg.tiles(); ++t, ++use) {
+          if (ok && !wait_all(&qempty[q_slot(use)], q_par(use) ^ 1)) {
+            give_up();
+            ok = false;
           }
+          if (ok) load_queries(sg, t, use, r, 64 * is_v);
         }
         for (int i = 0; ok && i < sg.nch; ++i, ++gc) {
           if (!wait_all(&rawfull[rs], rph)) {
@@ -955,7 +952,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         }
       } while (next(sg));
     }
-  } else if (!WIDEN && warp < 20) {
+  } else if (!WIDEN && warp < C::SOFT + 4) {
     // ======================= queries ======================================
     int use = 0;
     bool ok = true;
@@ -967,10 +964,11 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           give_up();
           ok = false;
         }
-        if (ok) load_queries(sg, t, use, tid & 127);
+        if (ok) load_queries(sg, t, use, tid & 127, 0);
       }
     } while (next(sg));
   } else {
+    if constexpr (WIDEN) reg_dec<72>();
     const int bs = p.block_size;
     auto block_of = [&](int b, int lb) {
       int pb = p.block_table[(long)b * p.max_blocks + lb];
@@ -1261,8 +1259,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
 #pragma unroll
           for (int kk = 0; kk < kS / 16; ++kk)
             umma_ts_elect(tbase + kColO + D * t,
-                          tbase + kColS + 128 * t + kS * buf + (kk >> 1) * 32 +
-                              (kk & 1) * 8,
+                          tbase + kColS + 128 * t + kS * buf + kk * 8,
                           bv + (uint64_t)((kk * 2048) >> 4), idO,
                           (v > 0 || kk > 0) ? 1u : 0u);
           umma_commit_elect(&pvdone[t]);
