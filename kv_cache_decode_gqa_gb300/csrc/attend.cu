@@ -27,8 +27,13 @@ __global__ void __launch_bounds__(kAttendMergeThreads)
   long before, total;
   int end;
   scan_work(p, G, scratch, sq, before, total, end);
+  // (every CTA waits, also one that has nothing to merge: what follows this
+  // launch on the stream waits for this one only)
   const int P = (int)min((long)p.n_splits, total), c = blockIdx.x + 1;
-  if (c >= P) return;
+  if (c >= P) {
+    pdl_wait();
+    return;
+  }
   const long x = share_lo(c, total, P);
   const int per = (p.batch + kAttendMergeThreads - 1) / kAttendMergeThreads;
 #pragma unroll
@@ -48,11 +53,12 @@ __global__ void __launch_bounds__(kAttendMergeThreads)
   const int unit = (int)((x - s_start) / len);
   const long u = s_start + (long)unit * len;  // its first chunk
   // begun by CTA c - 1 and not over when CTA c begins?
-  if (u == x || share_lo(c - 1, total, P) > u || x - u >= q.nch) return;
+  const bool cut = u < x && share_lo(c - 1, total, P) <= u && x - u < q.nch;
+  pdl_wait();
+  if (!cut) return;
   const int parts = share_of(u + q.nch - 1, total, P) - (c - 1) + 1;
   const int h = unit / q.blocks, f0 = (unit - h * q.blocks) * kUnit;
   const int np = min(q.n * G - f0, kUnit);
-  pdl_wait();
   constexpr int LANES = D / 4, ROWS = kAttendMergeThreads / LANES;
   const int e4 = tid % LANES;
   for (int ri = blockIdx.y * ROWS + tid / LANES; ri < np;
