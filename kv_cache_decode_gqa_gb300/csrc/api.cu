@@ -1574,6 +1574,7 @@ kvd_status attend(const kvd_cache *cache, const kvd_seqs *seqs,
   kvd::AttendParams p{};
   p.n_splits = pl.ctas;
   p.gap = pl.gap;
+  p.whole_units = pl.whole_units;
   p.block_rows = pl.pairs;
   p.ws_o = static_cast<float *>(workspace);
   p.ws_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) +

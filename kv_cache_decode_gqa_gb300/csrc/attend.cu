@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(kAttendMergeThreads)
   }
   __syncthreads();
   const Seq q = s_q;
-  const int len = q.nch + p.gap;
-  const int unit = (int)((x - s_start) / len);
+  const int len = unit_len(p, q);
+  const int unit = (int)div_u(x - s_start, len);
   const long u = s_start + (long)unit * len;  // its first chunk
   // begun by CTA c - 1 and not over when CTA c begins?
   const bool cut = u < x && share_lo(c - 1, total, P) <= u && x - u < q.nch;
@@ -91,27 +91,31 @@ cudaError_t launch_merge(const AttendParams &p, cudaStream_t s) {
                     grid, dim3(kAttendMergeThreads), 0, s, 1, p);
 }
 
-// A bf16 cache as [column half][row][64 columns], in swizzled boxes of `box`
-// rows (of all columns where box is 64).
-bool cache_map(CUtensorMap *map, const uint8_t *data, const AttendParams &p,
-               int box) {
+// A bf16 cache's K and V as [which][column half][row][64 columns], in swizzled
+// boxes of `box` rows (of all columns where box is 64) of one of them.
+bool cache_map(CUtensorMap *map, const AttendParams &p, int box) {
   const auto encode = tensor_map_encoder();
   if (!encode) return false;
+  const uint8_t *lo = std::min(p.k, p.v), *hi = std::max(p.k, p.v);
   const cuuint64_t d = p.dk;
-  const cuuint64_t dims[3] = {
-      64, (cuuint64_t)p.num_blocks * p.n_kv * p.block_size, d / 64};
-  const cuuint64_t strides[2] = {2 * d, 128};
-  const cuuint32_t boxes[3] = {64, (cuuint32_t)box,
-                               (cuuint32_t)(box == 64 ? d / 64 : 1)};
-  const cuuint32_t ones[3] = {1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                const_cast<uint8_t *>(data), dims, strides, boxes, ones,
+  const cuuint64_t dims[4] = {
+      64, (cuuint64_t)p.num_blocks * p.n_kv * p.block_size, d / 64,
+      lo == hi ? 1u : 2u};
+  const cuuint64_t strides[3] = {2 * d, 128,
+                                 lo == hi ? 16 : (cuuint64_t)(hi - lo)};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box,
+                               (cuuint32_t)(box == 64 ? d / 64 : 1), 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                const_cast<uint8_t *>(lo), dims, strides, boxes, ones,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
+
+constexpr long kMergeChunks = 3, kMinChunks = 4;
 
 AttendPlan attend_plan(int n_kv, int g, int d, int batch, int rows,
                        int max_rows, int max_seq_len, int ctas) {
@@ -120,8 +124,21 @@ AttendPlan attend_plan(int n_kv, int g, int d, int batch, int rows,
   const long units =
       (long)n_kv * (((long)rows * g + (long)std::min(batch, rows) * (kUnit - 1)) /
                     kUnit);
-  const long chunks = units * (((long)max_seq_len + kN - 1) / kN);
-  pl.ctas = (int)std::max(1L, std::min((long)ctas, chunks));
+  const long each = ((long)max_seq_len + kN - 1) / kN;
+  const long chunks = units * each;
+  // Not cut where the longest CTA then takes no more than a few chunks longer
+  // than equal shares would, which the merge launch costs.
+  const long waves = (units + ctas - 1) / ctas;
+  if (waves * each <= chunks / ctas + kMergeChunks) {
+    pl.whole_units = 1;
+    pl.ctas = (int)std::max(1L, std::min((long)ctas, units));
+    return pl;
+  }
+  // A CTA takes kMinChunks at least: its partial result of a unit of 128 pairs
+  // has the bytes of a chunk. (16 nodes of 8 heads each over 4,000 positions,
+  // us: 8 CTAs 42, 32 23.3, 64 20.6, 96 23.0, 152 26.8.)
+  pl.ctas = (int)std::max(
+      1L, std::min((long)ctas, std::max(units, chunks / kMinChunks)));
   if (chunks >= 8L * pl.ctas) pl.gap = kUnitGap;
   if (pl.ctas > 1) {
     const size_t slots = (size_t)pl.ctas * 2 * pl.pairs;
@@ -138,15 +155,14 @@ cudaError_t launch_attend(const AttendParams &p, cudaStream_t s) {
   if (p.dtype == DT_BF16) {
     // boxes of rows that lie within a block and within half a chunk
     tp.box = std::min(64, p.block_size & -p.block_size);
-    if (!cache_map(&tp.tmk, p.k, p, tp.box) ||
-        !cache_map(&tp.tmv, p.v, p, tp.box))
-      return cudaErrorNotSupported;
+    if (!cache_map(&tp.map, p, tp.box)) return cudaErrorNotSupported;
+    tp.v_first = p.v < p.k;
     e = p.dk == 128 ? launch_attend_t<DT_BF16, 128, 2>(tp, s)
                     : launch_attend_t<DT_BF16, 64, 2>(tp, s);
   } else {
     e = launch_attend_widen(tp, p.block_rows <= kM, s);
   }
-  if (e != cudaSuccess || p.n_splits <= 1) return e;
+  if (e != cudaSuccess || p.n_splits <= 1 || p.whole_units) return e;
   return p.dk == 128 ? launch_merge<128>(p, s) : launch_merge<64>(p, s);
 }
 

@@ -27,8 +27,11 @@ namespace kvd {
 
 struct TcParams {
   AttendParams p;
-  CUtensorMap tmk, tmv;  // bf16 caches: [column half][row][64 columns]
-  int box;               // rows of their boxes: 1 .. 64, a power of two
+  // bf16 caches: [K, V][column half][row][64 columns], or V first where it lies
+  // first
+  CUtensorMap map;
+  int v_first;
+  int box;  // rows of its boxes: 1 .. 64, a power of two
 };
 
 namespace {
@@ -124,6 +127,17 @@ __device__ __forceinline__ int uniform(int x) {
   return __shfl_sync(0xffffffffu, x, 0);
 }
 
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x,
+                                            int y, int z, int w,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::"
+      "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 8 columns of this thread's lane of tensor memory, waited for, and back.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
@@ -188,11 +202,15 @@ __device__ __forceinline__ Seq seq_at(const AttendParams &p, int b, int G) {
   return q;
 }
 
-// A unit counts as its chunks and p.gap empty ones behind them, which stand for
-// what a change of units costs the CTA that makes it.
+// What a unit counts as in the shares: its chunks and p.gap empty ones behind
+// them, which stand for what a change of units costs the CTA that makes it; or
+// 1, where units are not cut.
+__device__ __forceinline__ int unit_len(const AttendParams &p, const Seq &q) {
+  return p.whole_units ? 1 : q.nch + p.gap;
+}
 __device__ __forceinline__ long seq_chunks(const AttendParams &p,
                                            const Seq &q) {
-  return q.nch == 0 ? 0 : (long)p.n_kv * q.blocks * (q.nch + p.gap);
+  return q.nch == 0 ? 0 : (long)p.n_kv * q.blocks * unit_len(p, q);
 }
 
 // Exclusive prefix sums of the sequences' chunks over the block's threads:
@@ -247,8 +265,14 @@ __device__ __forceinline__ void scan_work(const AttendParams &p, int G,
   __syncthreads();
 }
 
+// a / b of values that are not negative: 32 bits are faster by a few hundred
+// cycles.
+__device__ __forceinline__ long div_u(long a, int b) {
+  return a >> 32 ? a / b : (long)((uint32_t)a / (uint32_t)b);
+}
 __device__ __forceinline__ long share_lo(int c, long total, int P) {
-  return total / P * c + total % P * c / P;
+  const long each = div_u(total, P);
+  return each * c + (total - each * P) * c / P;
 }
 // The CTA whose share holds chunk x.
 __device__ __forceinline__ int share_of(long x, long total, int P) {
@@ -304,7 +328,8 @@ __device__ __forceinline__ Seg seg_at(const AttendParams &p, const Walk &w,
   s.np = min(s.q.n * G - s.f0, kUnit);
   s.two = s.np > kM;
   s.k0 = w.k0;
-  s.nch = (int)min((long)max(s.q.nch - s.k0, 0), w.left);
+  s.nch = p.whole_units ? s.q.nch
+                        : (int)min((long)max(s.q.nch - s.k0, 0), w.left);
   return s;
 }
 
@@ -312,7 +337,7 @@ __device__ __forceinline__ Seg seg_at(const AttendParams &p, const Walk &w,
 __device__ __forceinline__ bool walk_on(const AttendParams &p, Walk &w,
                                         const Seg &s, int G, const Seq *near,
                                         int b0) {
-  w.left -= s.q.nch + p.gap - s.k0;
+  w.left -= unit_len(p, s.q) - s.k0;
   if (w.left <= 0) return false;
   w.k0 = 0;
   if (++w.unit == p.n_kv * s.q.blocks) {
@@ -414,6 +439,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
     mbar_init(drain, 2);
     fence_mbar_init();
   }
+  if (!WIDEN && warp == C::kLoad && lane == 0) prefetch_tmap(&tp.map);
   if (warp == C::kMma) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
@@ -486,8 +512,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
   const int b_near = *s_b;
   Walk wk;
   wk.b = b_near;
-  wk.unit = (int)(*s_off / (near[0].nch + p.gap));
-  wk.k0 = (int)(*s_off % (near[0].nch + p.gap));
+  wk.unit = (int)div_u(*s_off, unit_len(p, near[0]));
+  wk.k0 = (int)(*s_off - (long)wk.unit * unit_len(p, near[0]));
   wk.left = hi - lo;
   auto here = [&]() { return seg_at(p, wk, G, near, b_near); };
   auto next = [&](const Seg &s) {
@@ -1068,7 +1094,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                     mbar_arrive_expect_tx(bar,
                                           (uint32_t)(n << bshift) * D * 2);
                   uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
-                  const void *map = q ? &tp.tmv : &tp.tmk;
+                  const int kv = q ^ tp.v_first;
                   for (int i = lq; i * tp.box < kN; i += L) {
                     int a0 = x0, a1 = x1;
                     long row = at;
@@ -1077,12 +1103,12 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                     const int o = i * tp.box;  // row of the chunk
                     uint8_t *dst = tile + (o >> 6) * C::HALF + (o & 63) * 128;
                     if (tp.box == 64) {
-                      tma_load_3d(dst, map, 0, (int)row, 0, bar);
+                      tma_load_4d(dst, &tp.map, 0, (int)row, 0, kv, bar);
                     } else {
 #pragma unroll
                       for (int z = 0; z < D / 64; ++z)
-                        tma_load_3d(dst + z * C::COLS, map, 0, (int)row, z,
-                                    bar);
+                        tma_load_4d(dst + z * C::COLS, &tp.map, 0, (int)row, z,
+                                    kv, bar);
                     }
                   }
                 } else {

@@ -42,7 +42,7 @@ cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s);
 // The CTAs of a call (at most `ctas`), with equal shares of its chunks, and
 // their partial results: two a CTA, of `pairs` (row, head) pairs each.
 struct AttendPlan {
-  int ctas = 1, pairs = 0, gap = 0;
+  int ctas = 1, pairs = 0, gap = 0, whole_units = 0;
   size_t ws_o_bytes = 0, ws_bytes = 0;
 };
 AttendPlan attend_plan(int n_kv, int g, int d, int batch, int rows,
