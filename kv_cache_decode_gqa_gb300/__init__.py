@@ -734,8 +734,16 @@ def gqa_extend(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
 TREE_NODES = 256     # KVD_TREE_NODES
 
 
-def _words(max_rows):
-    return (max_rows + 31) // 32
+def _on(dev, t, name, dtype, numel):
+    """_need and _one_device in one, for the calls' small arguments: such a
+    call takes 20 to 30 us on the host, most of it here and in allocations."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.device == dev
+            and t.dtype is dtype and t.is_contiguous()
+            and t.numel() == numel):
+        _need(t, name, dtype, numel)
+        raise ValueError(f"{name} is on {t.device}, not {dev}")
+    return t.data_ptr()
 
 
 @_in_context
@@ -750,27 +758,27 @@ def tree_plan(parents, start, row_start, max_rows, window=0, masks=None,
     left out. Rows of new outputs that no sequence owns are not
     initialised."""
     import torch
-    _need(parents, "parents", torch.int32)
-    _need(start, "start", torch.int32)
-    B = start.numel()
-    _need(row_start, "row_start", torch.int32, B + 1)
-    rows, max_rows = parents.numel(), int(max_rows)
-    words = _words(max_rows)
-    if masks is not None:
-        _need(masks, "masks", torch.int32, rows * words)
-    if positions is not None:
-        _need(positions, "positions", torch.int32, rows)
-    dev = _one_device(parents, start, row_start, masks, positions)
+    i32 = torch.int32
+    _need(parents, "parents", i32)
+    rows, B, dev = parents.numel(), start.numel(), parents.device
+    max_rows = int(max_rows)
+    words = (max_rows + 31) // 32
+    sp = _on(dev, start, "start", i32, B)
+    rp = _on(dev, row_start, "row_start", i32, B + 1)
+    mp = masks if masks is None else _on(dev, masks, "masks", i32,
+                                         rows * words)
+    pp = positions if positions is None else _on(dev, positions, "positions",
+                                                 i32, rows)
 
-    def launch(s, masks=masks, positions=positions):
-        if masks is None:
-            masks = torch.empty((rows, words), dtype=torch.int32, device=dev)
-        if positions is None:
-            positions = torch.empty(rows, dtype=torch.int32, device=dev)
-        check(lib().kvd_tree_plan(
-            parents.data_ptr(), start.data_ptr(), row_start.data_ptr(), B,
-            rows, max_rows, int(window), masks.data_ptr(),
-            positions.data_ptr(), s))
+    def launch(s, masks=masks, positions=positions, mp=mp, pp=pp):
+        if mp is None:
+            masks = torch.empty((rows, words), dtype=i32, device=dev)
+            mp = masks.data_ptr()
+        if pp is None:
+            positions = torch.empty(rows, dtype=i32, device=dev)
+            pp = positions.data_ptr()
+        check(lib().kvd_tree_plan(parents.data_ptr(), sp, rp, B, rows,
+                                  max_rows, window, mp, pp, s))
         return masks, positions
     return dev, launch
 
@@ -794,49 +802,77 @@ def attend_workspace_size(cache, block_table, seq_lens, max_seq_len, rows,
     return out.value
 
 
-def _attend(call, extra, cache, seqs, tensors, q, row_start, max_rows, scale,
-            out, lse, workspace, want_lse):
-    """What gqa_tree and gqa_cross share: `call` the name of the function,
-    `extra` its arguments between q and the scale."""
+def _attend(tree, cache, block_table, seq_lens, max_seq_len, q, row_start,
+            max_rows, masks, positions, scale, out, lse, workspace, want_lse,
+            window, window_start):
+    """What gqa_tree and gqa_cross share."""
     import torch
-    d = cache.head_dim
+    i32, d = torch.int32, cache.head_dim
     qs = _rows3(q, "q", width=d)
     c = cache.struct()
-    rows, n_h = qs.rows, qs.heads
+    rows, n_h, dev = qs.rows, qs.heads, q.device
+    _one_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    B = seq_lens.numel()
+    _need(block_table, "block_table", i32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [batch][max_blocks_per_seq]")
+    width = block_table.shape[1]
+    bt = _on(dev, block_table, "block_table", i32, B * width)
+    ws = None
+    if window_start is not None:
+        ws = _on(dev, window_start, "window_start" if tree else "first", i32,
+                 B)
+    seqs = _native.KvdSeqs(bt, _on(dev, seq_lens, "seq_lens", i32, B), B,
+                           width, int(max_seq_len), 0, int(window), ws)
+    rp = mp = pp = None
     if row_start is not None:
-        _need(row_start, "row_start", torch.int32, seqs.batch + 1)
+        rp = _on(dev, row_start, "row_start", i32, B + 1)
+    elif tree:
+        raise ValueError("gqa_tree needs row_start")
+    if max_rows is None:
+        max_rows = 1 if row_start is None else rows
+    max_rows = int(max_rows)
+    if tree:
+        mp = _on(dev, masks, "masks", i32, rows * ((max_rows + 31) // 32))
+        if positions is not None:
+            pp = _on(dev, positions, "positions", i32, rows)
+        elif window:
+            raise ValueError("a window needs positions")
+    op = lp = wp = None
     if out is not None:
-        _need(out, "out", torch.bfloat16, rows * n_h * d)
+        op = _on(dev, out, "out", torch.bfloat16, rows * n_h * d)
     if lse is not None:
-        _need(lse, "lse", torch.float32, rows * n_h)
+        lp = _on(dev, lse, "lse", torch.float32, rows * n_h)
+    nbytes = 0
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8)
-    dev = _one_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale,
-                      row_start, out, lse, workspace, *tensors)
+        nbytes = workspace.numel()
+        wp = _on(dev, workspace, "workspace", torch.uint8, nbytes)
 
-    def launch(s, out=out, lse=lse, workspace=workspace):
+    def launch(s, out=out, lse=lse, op=op, lp=lp, wp=wp, nbytes=nbytes):
         L = lib()
         if out is None:
             out = torch.empty((rows, n_h, d), dtype=torch.bfloat16,
                               device=dev)
+            op = out.data_ptr()
         if lse is None and want_lse:
             lse = torch.empty((rows, n_h), dtype=torch.float32, device=dev)
-        if workspace is not None:
-            nbytes = workspace.numel()
-        else:
+            lp = lse.data_ptr()
+        if wp is None:
             need = ctypes.c_size_t(0)
             check(L.kvd_attend_workspace_size(
-                c, seqs, rows, max_rows, n_h, 0 if row_start is None else 1,
-                need))
+                c, seqs, rows, max_rows, n_h, 0 if rp is None else 1, need))
             nbytes = need.value
             if nbytes:
                 # every partial a call keeps here is written before it is read
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        check(getattr(L, call)(
-            c, seqs, None if row_start is None else row_start.data_ptr(),
-            max_rows, qs, *extra, float(scale or 0.0), out.data_ptr(),
-            None if lse is None else lse.data_ptr(),
-            None if workspace is None else workspace.data_ptr(), nbytes, s))
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+                wp = ws.data_ptr()
+        scl = float(scale or 0.0)
+        if tree:
+            check(L.kvd_gqa_tree(c, seqs, rp, max_rows, qs, mp, pp, scl, op,
+                                 lp, wp, nbytes, s))
+        else:
+            check(L.kvd_gqa_cross(c, seqs, rp, max_rows, qs, scl, op, lp, wp,
+                                  nbytes, s))
         return out, lse
     return dev, launch
 
@@ -855,23 +891,9 @@ def gqa_tree(cache, block_table, seq_lens, max_seq_len, q, row_start,
     ``positions`` (int32 [rows], tree_plan) back, ``window_start`` from the
     front. ``out`` must not overlap q. Rows of new outputs that no sequence owns
     are not initialised."""
-    import torch
-    seqs = _seqs(block_table, seq_lens, max_seq_len, 0, window, window_start)
-    rows, max_rows = q.shape[0], int(max_rows)
-    if row_start is None:
-        raise ValueError("gqa_tree needs row_start")
-    _need(masks, "masks", torch.int32, rows * _words(max_rows))
-    if positions is not None:
-        _need(positions, "positions", torch.int32, rows)
-    elif window:
-        raise ValueError("a window needs positions")
-    return _attend("kvd_gqa_tree",
-                   (masks.data_ptr(),
-                    None if positions is None else positions.data_ptr()),
-                   cache, seqs, (block_table, seq_lens, window_start, masks,
-                                 positions),
-                   q, row_start, max_rows, scale, out, lse, workspace,
-                   want_lse)
+    return _attend(True, cache, block_table, seq_lens, max_seq_len, q,
+                   row_start, max_rows, masks, positions, scale, out, lse,
+                   workspace, want_lse, window, window_start)
 
 
 @_in_context
@@ -884,12 +906,9 @@ def gqa_cross(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
     from 0). Rows row_start[b] .. row_start[b + 1] - 1 belong to sequence b, at
     most ``max_rows`` of them (None: all rows, which fits any list); without
     row_start row b is sequence b's one row."""
-    seqs = _seqs(block_table, seq_lens, max_seq_len, 0, 0, first)
-    if max_rows is None:
-        max_rows = 1 if row_start is None else q.shape[0]
-    return _attend("kvd_gqa_cross", (), cache, seqs,
-                   (block_table, seq_lens, first), q, row_start,
-                   int(max_rows), scale, out, lse, workspace, want_lse)
+    return _attend(False, cache, block_table, seq_lens, max_seq_len, q,
+                   row_start, max_rows, None, None, scale, out, lse,
+                   workspace, want_lse, 0, first)
 
 
 class CacheList:
@@ -920,23 +939,24 @@ def kv_keep(caches, block_table, start, path, n_keep):
     if not isinstance(caches, CacheList):
         caches = CacheList([caches] if isinstance(caches, PagedCache)
                            else caches)
-    _need(block_table, "block_table", torch.int32)
-    _need(path, "path", torch.int32)
+    i32 = torch.int32
+    _need(block_table, "block_table", i32)
+    _need(path, "path", i32)
     if block_table.dim() != 2 or path.dim() != 2:
         raise ValueError("block_table and path must be [batch][...]")
     B, width = path.shape
     if block_table.shape[0] != B:
         raise ValueError(f"block_table and path have {block_table.shape[0]} "
                          f"and {B} sequences")
-    _need(start, "start", torch.int32, B)
-    _need(n_keep, "n_keep", torch.int32, B)
-    dev = _one_device(block_table, start, path, n_keep, caches.caches[0].k)
+    dev, blocks = caches.device, block_table.shape[1]
+    bt = _on(dev, block_table, "block_table", i32, B * blocks)
+    pp = _on(dev, path, "path", i32, B * width)
+    sp = _on(dev, start, "start", i32, B)
+    kp = _on(dev, n_keep, "n_keep", i32, B)
 
     def launch(s):
-        check(lib().kvd_kv_keep(
-            caches.structs, len(caches.structs), block_table.data_ptr(),
-            block_table.shape[1], start.data_ptr(), path.data_ptr(), width,
-            n_keep.data_ptr(), B, s))
+        check(lib().kvd_kv_keep(caches.structs, len(caches.structs), bt,
+                                blocks, sp, pp, width, kp, B, s))
     return dev, launch
 
 

@@ -115,7 +115,7 @@ bool cache_map(CUtensorMap *map, const AttendParams &p, int box) {
 
 }  // namespace
 
-constexpr long kMergeChunks = 3, kMinChunks = 4;
+constexpr long kMergeChunks = 4, kMinChunks = 4;
 
 AttendPlan attend_plan(int n_kv, int g, int d, int batch, int rows,
                        int max_rows, int max_seq_len, int ctas) {
