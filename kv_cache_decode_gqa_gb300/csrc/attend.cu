@@ -126,12 +126,11 @@ AttendPlan attend_plan(int n_kv, int g, int d, int batch, int rows,
                     kUnit);
   const long each = ((long)max_seq_len + kN - 1) / kN;
   const long chunks = units * each;
-  // Not cut where the longest CTA then takes no more than a few chunks longer
-  // than equal shares would, which the merge launch costs.
-  const long waves = (units + ctas - 1) / ctas;
-  if (waves * each <= chunks / ctas + kMergeChunks) {
+  // Not cut where a CTA a unit then takes no more than a few chunks longer than
+  // equal shares would, which the merge launch costs.
+  if (units <= ctas && each <= chunks / ctas + kMergeChunks) {
     pl.whole_units = 1;
-    pl.ctas = (int)std::max(1L, std::min((long)ctas, units));
+    pl.ctas = (int)std::max(1L, units);
     return pl;
   }
   // A CTA takes kMinChunks at least: its partial result of a unit of 128 pairs

@@ -58,12 +58,22 @@ struct ACfg {
   static constexpr int kLoad = SOFT + (WIDEN ? 8 : 4);
   static constexpr int kMma = kLoad + (WIDEN ? 1 : 2);
   static constexpr int THREADS = (SOFT + (WIDEN ? 12 : 8)) * 32;
-  // K and V tiles in alternation, then (WIDEN) raw K and V rows
+  // a ring of K tiles, one of V tiles, then (WIDEN) raw K and V rows
   static constexpr int SCALES = WIDEN ? QS : 0;
   static constexpr int FIXED = (2 + SCALES) * kM * 4 + 896;
   static constexpr int ROOM = 227 * 1024 - FIXED - QS * TILE;
   static constexpr int NS =
       WIDEN ? 4 : (ROOM / TILE > 12 ? 12 : ROOM / TILE);
+  static constexpr int KS = NS / 2, VS = NS - KS;
+  // slots and phases of the tiles of chunk g of a CTA's range
+  __device__ static __forceinline__ int k_slot(int g) { return g % KS; }
+  __device__ static __forceinline__ int v_slot(int g) { return KS + g % VS; }
+  __device__ static __forceinline__ uint32_t k_par(int g) {
+    return g / KS & 1;
+  }
+  __device__ static __forceinline__ uint32_t v_par(int g) {
+    return g / VS & 1;
+  }
   static constexpr int NR_FIT = WIDEN ? (ROOM - NS * TILE) / RAW : 0;
   static constexpr int NR = NR_FIT > 12 ? 12 : NR_FIT & ~1;
   static constexpr int Q_OFF = 0;
@@ -891,7 +901,9 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           // a row that was not copied, or that no pair sees: zeros, so that 0
           // times it stays 0
           const bool dead = pos < sg.q.lo || pos >= sg.q.T;
-          const int u = 2 * gc + is_v, st = u % NS;
+          const int st = is_v ? C::v_slot(gc) : C::k_slot(gc);
+          const uint32_t free_par =
+              (is_v ? C::v_par(gc) : C::k_par(gc)) ^ 1;
           uint8_t *dst = smem + C::KV_OFF + st * C::TILE + (r >> 6) * C::HALF;
           constexpr int PIECES = D / 16;  // of 16 channels
           auto put = [&](int g, const uint32_t (&y)[8]) {
@@ -904,7 +916,15 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                              y[4 * q + 3]);
             }
           };
-          // raw codes to registers, then the slot is free
+          // raw codes to registers, then the slot is free. (The copies into it
+          // are of another proxy: without the fence they overtook loads that
+          // the threads had issued but not received, once in some hundred
+          // calls.)
+          auto raw_free = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rawempty[rs]);
+          };
           if constexpr (DT == DT_MXFP4) {
             uint2 w[PIECES];
             uint32_t sw[PIECES / 4];
@@ -921,9 +941,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
 #pragma unroll
               for (int g = 0; g < PIECES / 4; ++g) sw[g] = 0;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&rawempty[rs]);
-            if (!wait_all(&empty[st], (u / NS & 1) ^ 1)) {
+            raw_free();
+            if (!wait_all(&empty[st], free_par)) {
               give_up();
               ok = false;
               break;
@@ -952,9 +971,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
               w[g] = *reinterpret_cast<const uint4 *>(src + 16 * (g ^ turn));
               if (dead) w[g] = make_uint4(0, 0, 0, 0);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&rawempty[rs]);
-            if (!wait_all(&empty[st], (u / NS & 1) ^ 1)) {
+            raw_free();
+            if (!wait_all(&empty[st], free_par)) {
               give_up();
               ok = false;
               break;
@@ -1023,7 +1041,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       const int shift = __ffs(L) - 1, lq = lane & (L - 1), batch = 32 >> shift;
       const int mine = lane >> shift, bshift = WIDEN ? 0 : __ffs(tp.box) - 1;
       bool go = true;
-      int u = 0;                     // K and V units so far
+      int u = 0;                     // K and V units so far, in turn
       uint32_t via = 0, par = 0;     // slots on their way through `land`, and
                                      // its parities, a bit a slot
       Seg sg;
@@ -1071,10 +1089,16 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           for (int j = 0; go && j < cnt; ++j) {
 #pragma unroll
             for (int q = 0; q < 2; ++q, ++u) {  // K, V
-              constexpr int RING = WIDEN ? NR : NS;
-              const int s = u % RING;
-              uint64_t *eb = WIDEN ? &rawempty[s] : &empty[s];
-              go = go && wait_all(eb, (u / RING & 1) ^ 1);
+              const int gc = u >> 1;
+              int s;
+              if constexpr (WIDEN) {
+                s = u % NR;
+                go = go && wait_all(&rawempty[s], (u / NR & 1) ^ 1);
+              } else {
+                s = q ? C::v_slot(gc) : C::k_slot(gc);
+                go = go && wait_all(&empty[s],
+                                    (q ? C::v_par(gc) : C::k_par(gc)) ^ 1);
+              }
               if (!go) break;
               // a V tile of which some rows are not attended to goes through
               // the warp that fills them with zeros
@@ -1140,17 +1164,19 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         give_up();
         // every copy that was issued has landed before this CTA gives its
         // shared memory back
-        constexpr int RING = WIDEN ? NR : NS;
-        for (int i = 0; i < RING && i < u; ++i) {
-          const int x = u - 1 - i;
+        for (int x = u - 1; x >= 0 && x >= u - (WIDEN ? NR : 2 * NS); --x) {
           if constexpr (WIDEN) {
-            mbar_wait(&rawfull[x % RING], (x / RING) & 1);
+            mbar_wait(&rawfull[x % NR], (x / NR) & 1);
           } else {
-            const int s = x % RING;
+            // (the last use of each slot)
+            const int g = x >> 1;
+            const int s = x & 1 ? C::v_slot(g) : C::k_slot(g);
+            const int ring = x & 1 ? C::VS : C::KS;
+            if (x + 2 * ring < u) continue;
             if (via >> s & 1)
               mbar_wait(&land[s], (par >> s & 1) ^ 1);
             else
-              mbar_wait(&full[s], (x / RING) & 1);
+              mbar_wait(&full[s], x & 1 ? C::v_par(g) : C::k_par(g));
           }
         }
       }
@@ -1159,18 +1185,18 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       // Rows of a chunk that no pair attends to are zeros, so that 0 times
       // them stays 0: the copies left them as they were, or brought in what
       // lies beside the sequence.
-      int u = 1;
+      int gc = 0;
       uint32_t par = 0;  // parities of `land`, a bit a slot
       bool ok = true;
       Seg sg;
       do {
         sg = here();
-        for (int k = 0; ok && k < sg.nch; ++k, u += 2) {
+        for (int k = 0; ok && k < sg.nch; ++k, ++gc) {
           const int pos0 = (sg.c0() + k) * kN;
           const int a = max(sg.q.lo - pos0, 0);
           const int z = min(sg.q.T - pos0, kN);
           if (z - a == kN) continue;
-          const int s = u % NS;
+          const int s = C::v_slot(gc);
           if (!wait_all(&land[s], par >> s & 1)) {
             give_up();
             ok = false;
@@ -1211,11 +1237,11 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         return false;
       };
       // One warp a tile; each touches its own tensor memory only. Both see every
-      // K and V tile arrive, in their order (a barrier's phases must not pass
-      // unseen), and both let go of it: after the products that read it, or at
-      // once where the other tile's do.
+      // K tile arrive and every V tile, in their order (a barrier's phases must
+      // not pass unseen), and both let go of it: after the products that read it,
+      // or at once where the other tile's do.
       const int t = warp - C::kMma;
-      int use = 0, gc = 0, gv = 0, seen = 0;
+      int use = 0, gc = 0, gv = 0, seen_k = 0, seen_v = 0;
       bool ok = true;
       Seg sg;
       do {
@@ -1224,24 +1250,29 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         const bool two = uniform(sg.two);
         const int qu = use + (two ? t : 0);
         const uint32_t qa = q0 + q_slot(qu) * C::TILE;
-        auto unit_of = [&](int v, int is_v) {
-          return 2 * (gc + chunk_of(two, t, v)) + is_v;
-        };
-        // waits for the tiles up to unit u
-        auto need = [&](int u) {
-          for (; seen <= u; ++seen) {
-            const int st = seen % NS;
-            if (!poll(&full[st], seen / NS & 1)) return false;
-            if (!two && (((seen >> 1) - gc) & 1) != t) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&empty[st]);
-            }
+        auto chunk = [&](int v) { return gc + chunk_of(two, t, v); };
+        // wait for the tiles up to chunk g
+        auto see = [&](int g, int st, uint32_t par) {
+          if (!poll(&full[st], par)) return false;
+          if (!two && ((g - gc) & 1) != t) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
           }
+          return true;
+        };
+        auto need_k = [&](int g) {
+          for (; seen_k <= g; ++seen_k)
+            if (!see(seen_k, C::k_slot(seen_k), C::k_par(seen_k))) return false;
+          return true;
+        };
+        auto need_v = [&](int g) {
+          for (; seen_v <= g; ++seen_v)
+            if (!see(seen_v, C::v_slot(seen_v), C::v_par(seen_v))) return false;
           return true;
         };
         // scores of step v, whose K tile is there
         auto issue_s = [&](int v) {
-          const int st = unit_of(v, 0) % NS, buf = v & 1;
+          const int st = C::k_slot(chunk(v)), buf = v & 1;
           const uint64_t a = umma_desc_sw128(qa, 16, 1024);
           const uint64_t bk =
               umma_desc_sw128(kv0 + st * C::TILE + buf * C::HALF, 16, 1024);
@@ -1262,7 +1293,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         // two steps of scores ahead; then per step the product with V and the
         // scores of the step after next, into the buffer P just left
         if (ok && nv > 0) {
-          ok = need(unit_of(0, 0));
+          ok = need_k(chunk(0));
           tc_fence_after();
           if (ok) {
             issue_s(0);
@@ -1270,13 +1301,13 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           }
         }
         for (int v = 0; ok && v < nv; ++v) {
-          const int buf = v & 1, u = unit_of(v, 1), st = u % NS;
+          const int buf = v & 1, st = C::v_slot(chunk(v));
           if (v == nv - 2) {
             // the unit's scores are all issued: its queries are free
             for (int i = 0; i <= (int)two; ++i)
               umma_commit_elect(&qempty[q_slot(use + i)]);
           }
-          ok = need(u) &&
+          ok = need_v(chunk(v)) &&
                wait_all(&pfull[2 * t + buf], ((gv + v) >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
@@ -1292,7 +1323,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           if (buf == 1) umma_commit_elect(&empty[st]);
           if (v == nv - 1) umma_commit_elect(&odone[t]);
           if (v + 2 < nv) {
-            ok = need(unit_of(v + 2, 0));
+            ok = need_k(chunk(v + 2));
             tc_fence_after();
             if (ok) issue_s(v + 2);
           }
@@ -1301,7 +1332,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           for (int i = 0; i <= (int)two; ++i)
             umma_commit_elect(&qempty[q_slot(use + i)]);
         // the other tile's last ones too
-        ok = ok && need(2 * (gc + nch) - 1);
+        ok = ok && need_k(gc + nch - 1) && need_v(gc + nch - 1);
         use += two ? 2 : 1;
         gc += nch;
         gv += nv;

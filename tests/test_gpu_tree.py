@@ -603,6 +603,24 @@ def test_streams_graphs_and_repeats():
     assert K.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "mxfp4"])
+def test_many_calls_give_the_same_bits(dtype):
+    """Short units among long ones, call after call: what one call still
+    reads, the next copy or call must not overwrite."""
+    n, lens, first = [333, 100, 1], [900, 33, 2000], [100, 0, 1999]
+    g = _gen(53)
+    bt, blocks = _table(g, lens, 32)
+    c = _cache(g, blocks, 8, 32, dtype, 128)
+    q = _randn(g, sum(n), 32, 128)
+    args = (c, bt, _i32(lens), 2000, q, _starts(n))
+    fi = _i32(first)
+    want = K.gqa_cross(*args, max(n), first=fi)
+    _check(want, _reference(c, bt, lens, q, n, _cross_sees(n, lens, first)))
+    outs = [K.gqa_cross(*args, max(n), first=fi) for _ in range(600)]
+    assert all(torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
+               for o in outs)
+
+
 def test_workspace_of_the_stated_size():
     case = ("bf16", 128, 16, 2, 64, [20, 33], [3000, 900], 33)
     c, bt, lens, masks, pos, q = _setup(case, 41)
