@@ -155,7 +155,8 @@ cudaError_t launch_attend(const AttendParams &p, cudaStream_t s) {
     // boxes of rows that lie within a block and within half a chunk
     tp.box = std::min(64, p.block_size & -p.block_size);
     if (!cache_map(&tp.map, p, tp.box)) return cudaErrorNotSupported;
-    tp.v_first = p.v < p.k;
+    tp.which[0] = p.v < p.k;
+    tp.which[1] = p.k < p.v;
     e = p.dk == 128 ? launch_attend_t<DT_BF16, 128, 2>(tp, s)
                     : launch_attend_t<DT_BF16, 64, 2>(tp, s);
   } else {

@@ -27,10 +27,10 @@ namespace kvd {
 
 struct TcParams {
   AttendParams p;
-  // bf16 caches: [K, V][column half][row][64 columns], or V first where it lies
-  // first
+  // bf16 caches: [which][column half][row][64 columns], of K and V the one that
+  // lies first first
   CUtensorMap map;
-  int v_first;
+  int which[2];  // K's and V's
   int box;  // rows of its boxes: 1 .. 64, a power of two
 };
 
@@ -1118,7 +1118,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                     mbar_arrive_expect_tx(bar,
                                           (uint32_t)(n << bshift) * D * 2);
                   uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
-                  const int kv = q ^ tp.v_first;
+                  const int kv = tp.which[q];
                   for (int i = lq; i * tp.box < kN; i += L) {
                     int a0 = x0, a1 = x1;
                     long row = at;

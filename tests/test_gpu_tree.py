@@ -540,6 +540,53 @@ def test_bad_blocks_are_flagged():
             assert K.device_error() == K.DEVERR_BLOCK
 
 
+@pytest.mark.parametrize("dtype,d,batch", [("bf16", 128, 1000),
+                                           ("fp8", 128, 1024),
+                                           ("mxfp4", 128, 300),
+                                           ("bf16", 64, 1024)])
+def test_many_sequences(dtype, d, batch):
+    """More sequences than a CTA has threads or keeps at hand: short ones, empty
+    ones and a few long ones."""
+    rng = np.random.default_rng(batch + d)
+    n = rng.integers(0, 4, batch).tolist()
+    lens = rng.integers(0, 60, batch).tolist()
+    for b in (3, batch // 2, batch - 1):
+        n[b], lens[b] = 9, 700
+    n[7], lens[8] = 0, 0
+    g = _gen(batch)
+    bt, blocks = _table(g, lens, 16)
+    c = _cache(g, blocks, 2, 16, dtype, d)
+    q = _randn(g, sum(n), 6, d)
+    got = K.gqa_cross(c, bt, _i32(lens), 700, q, _starts(n), 9)
+    _check(got, _reference(c, bt, lens, q, n, _cross_sees(n, lens, None)))
+    past = [max(x - k, 0) for x, k in zip(lens, n)]
+    lens = [p + k for p, k in zip(past, n)]
+    if max(lens) > 700:
+        return
+    bt, blocks = _table(g, lens, 16)
+    c = _cache(g, blocks, 2, 16, dtype, d)
+    masks, _ = K.tree_plan(_i32([-1] * sum(n)), _i32(past), _starts(n), 9)
+    got = K.gqa_tree(c, bt, _i32(lens), 700, q, _starts(n), 9, masks)
+    _check(got, _reference(c, bt, lens, q, n,
+                           _tree_sees(n, past, masks, 1)))
+    assert K.device_error() == 0
+
+
+def test_keys_and_values_in_one_tensor():
+    """K and V may be the same storage, or V may lie first."""
+    n, lens = [5, 30], [200, 77]
+    g = _gen(59)
+    bt, blocks = _table(g, lens, 64)
+    both = _randn(g, 2, blocks, 2, 64, 128)
+    q = _randn(g, sum(n), 8, 128)
+    for k, v in ((0, 0), (0, 1), (1, 0)):
+        c = K.PagedCache(both[k], both[v], 64, 2, 128)
+        got = K.gqa_cross(c, bt, _i32(lens), 200, q, _starts(n), 30)
+        _check(got, _reference(c, bt, lens, q, n,
+                               _cross_sees(n, lens, None)))
+    assert K.device_error() == 0
+
+
 def test_cache_beyond_32_bit_offsets():
     """Blocks at byte offsets past 2^32 and element offsets past 2^31."""
     bs, n_kv, d, n, past = 64, 8, 128, [5, 12], [200, 70]
