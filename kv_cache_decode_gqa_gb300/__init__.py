@@ -737,13 +737,14 @@ TREE_NODES = 256     # KVD_TREE_NODES
 def _on(dev, t, name, dtype, numel):
     """_need and _one_device in one, for the calls' small arguments: such a
     call takes 20 to 30 us on the host, most of it here and in allocations."""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.device == dev
-            and t.dtype is dtype and t.is_contiguous()
-            and t.numel() == numel):
-        _need(t, name, dtype, numel)
-        raise ValueError(f"{name} is on {t.device}, not {dev}")
-    return t.data_ptr()
+    try:
+        if (t.device == dev and t.dtype is dtype and t.is_contiguous()
+                and (numel is None or t.numel() == numel)):
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    _need(t, name, dtype, numel)
+    raise ValueError(f"{name} is on {t.device}, not {dev}")
 
 
 @_in_context
@@ -812,12 +813,11 @@ def _attend(tree, cache, block_table, seq_lens, max_seq_len, q, row_start,
     c = cache.struct()
     rows, n_h, dev = qs.rows, qs.heads, q.device
     _one_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale)
-    B = seq_lens.numel()
-    _need(block_table, "block_table", i32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    bt = _on(dev, block_table, "block_table", i32, None)
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != seq_lens.numel():
         raise ValueError("block_table must be [batch][max_blocks_per_seq]")
-    width = block_table.shape[1]
-    bt = _on(dev, block_table, "block_table", i32, B * width)
+    B, width = shape
     ws = None
     if window_start is not None:
         ws = _on(dev, window_start, "window_start" if tree else "first", i32,
@@ -851,8 +851,7 @@ def _attend(tree, cache, block_table, seq_lens, max_seq_len, q, row_start,
     def launch(s, out=out, lse=lse, op=op, lp=lp, wp=wp, nbytes=nbytes):
         L = lib()
         if out is None:
-            out = torch.empty((rows, n_h, d), dtype=torch.bfloat16,
-                              device=dev)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
             op = out.data_ptr()
         if lse is None and want_lse:
             lse = torch.empty((rows, n_h), dtype=torch.float32, device=dev)
@@ -860,7 +859,7 @@ def _attend(tree, cache, block_table, seq_lens, max_seq_len, q, row_start,
         if wp is None:
             need = ctypes.c_size_t(0)
             check(L.kvd_attend_workspace_size(
-                c, seqs, rows, max_rows, n_h, 0 if rp is None else 1, need))
+                c, seqs, rows, max_rows, n_h, rp is not None, need))
             nbytes = need.value
             if nbytes:
                 # every partial a call keeps here is written before it is read
