@@ -53,9 +53,10 @@ struct ACfg {
   static constexpr int COLS = 64 * 128;       // 64 rows x 64 columns
   static constexpr int RAW = kN * row_bytes(D, DT);  // cached rows of a chunk
   // warps: 0-7 softmax; then four of queries (WIDEN: and K), (WIDEN) four of V,
-  // copies, (bf16) the ends of V, two of MMA issue
+  // copies of K, (bf16) copies of V, two of MMA issue, (WIDEN) copies of V
   static constexpr int SOFT = 8;
   static constexpr int kLoad = SOFT + (WIDEN ? 8 : 4);
+  static constexpr int kLoadV = kLoad + (WIDEN ? 3 : 1);
   static constexpr int kMma = kLoad + (WIDEN ? 1 : 2);
   static constexpr int THREADS = (SOFT + (WIDEN ? 12 : 8)) * 32;
   // a ring of K tiles, one of V tiles, then (WIDEN) raw K and V rows
@@ -1022,8 +1023,10 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       }
       return pb;
     };
-    if (warp == C::kLoad) {
-      // ===================== copies =======================================
+    if (warp == C::kLoad || warp == C::kLoadV) {
+      // ===================== copies of K, of V ============================
+      // (A warp's copies follow one another at 827 cycles for a swizzled tile
+      // of 16 KB, 540 unswizzled, from L2 too; those of two warps overlap.)
       // Pieces of a chunk: boxes of tp.box rows (bf16), or what it has of a
       // block. Chunks are looked up 32 / L at a time: lane l takes piece l % L
       // of chunk l / L of the batch (L: pieces a chunk may have, a power of
@@ -1041,9 +1044,39 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       const int shift = __ffs(L) - 1, lq = lane & (L - 1), batch = 32 >> shift;
       const int mine = lane >> shift, bshift = WIDEN ? 0 : __ffs(tp.box) - 1;
       bool go = true;
-      int u = 0;                     // K and V units so far, in turn
-      uint32_t via = 0, par = 0;     // slots on their way through `land`, and
-                                     // its parities, a bit a slot
+      const int q = warp == C::kLoadV;
+      int gc = 0;  // chunks so far
+      // bf16: rows of a V tile that no pair attends to are zeros, so that 0 times
+      // them stays 0: the copies left them as they were, or brought in what lies
+      // beside the sequence. Such a tile arrives on a barrier of its own
+      // (`land`); its rows [0, ea) and [ez, 128) are filled behind the copies of
+      // the next one, and before any wait.
+      int ends_slot = -1, ea = 0, ez = 0;
+      uint32_t par = 0;  // parities of `land`, a bit a slot
+      auto fill_ends = [&]() {
+        if (ends_slot < 0) return;
+        const int s = ends_slot;
+        ends_slot = -1;
+        if (!wait_all(&land[s], par >> s & 1)) {
+          go = false;
+          return;
+        }
+        par ^= 1u << s;
+        uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
+        constexpr int PC = D / 8;  // 16-byte pieces of a row
+        const int rows = kN - (ez - ea);
+        for (int i = lane; i < rows * PC; i += 32) {
+          int r = i / PC;
+          const int e = i - r * PC;
+          if (r >= ea) r += ez - ea;
+          *reinterpret_cast<uint4 *>(tile + (r >> 6) * C::HALF +
+                                     (e >> 3) * C::COLS + (r & 63) * 128 +
+                                     (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+      };
       Seg sg;
       do {
         sg = here();
@@ -1086,140 +1119,100 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
             at = piece(lq, x0, x1);
           }
           const int cnt = min(batch, c1 - cb);
-          for (int j = 0; go && j < cnt; ++j) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q, ++u) {  // K, V
-              const int gc = u >> 1;
-              int s;
-              if constexpr (WIDEN) {
-                s = u % NR;
-                go = go && wait_all(&rawempty[s], (u / NR & 1) ^ 1);
-              } else {
-                s = q ? C::v_slot(gc) : C::k_slot(gc);
-                go = go && wait_all(&empty[s],
-                                    (q ? C::v_par(gc) : C::k_par(gc)) ^ 1);
-              }
-              if (!go) break;
-              // a V tile of which some rows are not attended to goes through
-              // the warp that fills them with zeros
-              bool ends = false;
+          for (int j = 0; go && j < cnt; ++j, ++gc) {
+            const int p0 = (cb + j) * kN;
+            const int s = WIDEN ? (2 * gc + q) % NR
+                          : q   ? C::v_slot(gc)
+                                : C::k_slot(gc);
+            uint64_t *free = WIDEN ? &rawempty[s] : &empty[s];
+            const uint32_t free_par = (WIDEN ? (2 * gc + q) / NR & 1
+                                       : q   ? C::v_par(gc)
+                                             : C::k_par(gc)) ^
+                                      1;
+            bool ends = false;
+            if constexpr (!WIDEN) {
+              ends = q == 1 && (p0 < sg.q.lo || p0 > sg.q.T - kN);
+              if (!__all_sync(0xffffffffu, mbar_test_wait(free, free_par)))
+                fill_ends();
+            }
+            go = go && wait_all(free, free_par);
+            if (!go) break;
+            if (mine == j) {
               if constexpr (!WIDEN) {
-                const int p0 = (cb + j) * kN;
-                ends = q == 1 && (p0 < sg.q.lo || p0 > sg.q.T - kN);
-                via = (via & ~(1u << s)) | ((uint32_t)ends << s);
-                par ^= (uint32_t)ends << s;
-              }
-              if (mine == j) {
-                if constexpr (!WIDEN) {
-                  uint64_t *bar = ends ? &land[s] : &full[s];
-                  const int n =
-                      ((t1 + tp.box - 1) >> bshift) - (t0 >> bshift);
-                  if (lq == 0)
-                    mbar_arrive_expect_tx(bar,
-                                          (uint32_t)(n << bshift) * D * 2);
-                  uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
-                  const int kv = tp.which[q];
-                  for (int i = lq; i * tp.box < kN; i += L) {
-                    int a0 = x0, a1 = x1;
-                    long row = at;
-                    if (i > lq) row = piece(i, a0, a1);
-                    if (a0 >= a1) continue;
-                    const int o = i * tp.box;  // row of the chunk
-                    uint8_t *dst = tile + (o >> 6) * C::HALF + (o & 63) * 128;
-                    if (tp.box == 64) {
-                      tma_load_4d(dst, &tp.map, 0, (int)row, 0, kv, bar);
-                    } else {
+                uint64_t *bar = ends ? &land[s] : &full[s];
+                const int n =
+                    ((t1 + tp.box - 1) >> bshift) - (t0 >> bshift);
+                if (lq == 0)
+                  mbar_arrive_expect_tx(bar,
+                                        (uint32_t)(n << bshift) * D * 2);
+                uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
+                const int kv = tp.which[q];
+                for (int i = lq; i * tp.box < kN; i += L) {
+                  int a0 = x0, a1 = x1;
+                  long row = at;
+                  if (i > lq) row = piece(i, a0, a1);
+                  if (a0 >= a1) continue;
+                  const int o = i * tp.box;  // row of the chunk
+                  uint8_t *dst = tile + (o >> 6) * C::HALF + (o & 63) * 128;
+                  if (tp.box == 64) {
+                    tma_load_4d(dst, &tp.map, 0, (int)row, 0, kv, bar);
+                  } else {
 #pragma unroll
-                      for (int z = 0; z < D / 64; ++z)
-                        tma_load_4d(dst + z * C::COLS, &tp.map, 0, (int)row, z,
-                                    kv, bar);
-                    }
-                  }
-                } else {
-                  constexpr int ROW = row_bytes(D, DT);
-                  uint8_t *dst = smem + C::RAW_OFF + s * C::RAW;
-                  const uint8_t *src = q ? p.v : p.k;
-                  // (copies may land before the expectation is set: the phase
-                  // ends with that arrival at the earliest)
-                  if (lq == 0)
-                    mbar_arrive_expect_tx(&rawfull[s],
-                                          (uint32_t)(t1 - t0) * ROW);
-                  for (int i = lq;; i += L) {
-                    int a0 = x0, a1 = x1;
-                    long row = at;
-                    if (i > lq) row = piece(i, a0, a1);
-                    if (a0 < a1)
-                      bulk_g2s(dst + (a0 - c * kN) * ROW, src + row * ROW,
-                               (uint32_t)(a1 - a0) * ROW, &rawfull[s]);
-                    if (L < 32 || (t0 / bs + i + L) * bs >= t1) break;
+                    for (int z = 0; z < D / 64; ++z)
+                      tma_load_4d(dst + z * C::COLS, &tp.map, 0, (int)row, z,
+                                  kv, bar);
                   }
                 }
+              } else {
+                constexpr int ROW = row_bytes(D, DT);
+                uint8_t *dst = smem + C::RAW_OFF + s * C::RAW;
+                const uint8_t *src = q ? p.v : p.k;
+                // (copies may land before the expectation is set: the phase
+                // ends with that arrival at the earliest)
+                if (lq == 0)
+                  mbar_arrive_expect_tx(&rawfull[s],
+                                        (uint32_t)(t1 - t0) * ROW);
+                for (int i = lq;; i += L) {
+                  int a0 = x0, a1 = x1;
+                  long row = at;
+                  if (i > lq) row = piece(i, a0, a1);
+                  if (a0 < a1)
+                    bulk_g2s(dst + (a0 - c * kN) * ROW, src + row * ROW,
+                             (uint32_t)(a1 - a0) * ROW, &rawfull[s]);
+                  if (L < 32 || (t0 / bs + i + L) * bs >= t1) break;
+                }
               }
-              __syncwarp();
+            }
+            __syncwarp();
+            if constexpr (!WIDEN) {
+              fill_ends();
+              if (ends) {
+                ends_slot = s;
+                ea = max(sg.q.lo - p0, 0);
+                ez = min(sg.q.T - p0, kN);
+              }
             }
           }
         }
       } while (next(sg));
+      fill_ends();
       if (!go) {
         give_up();
         // every copy that was issued has landed before this CTA gives its
         // shared memory back
-        for (int x = u - 1; x >= 0 && x >= u - (WIDEN ? NR : 2 * NS); --x) {
+        for (int g = max(gc - NS, 0); g < gc; ++g) {
           if constexpr (WIDEN) {
-            mbar_wait(&rawfull[x % NR], (x / NR) & 1);
-          } else {
-            // (the last use of each slot)
-            const int g = x >> 1;
-            const int s = x & 1 ? C::v_slot(g) : C::k_slot(g);
-            const int ring = x & 1 ? C::VS : C::KS;
-            if (x + 2 * ring < u) continue;
-            if (via >> s & 1)
-              mbar_wait(&land[s], (par >> s & 1) ^ 1);
-            else
-              mbar_wait(&full[s], x & 1 ? C::v_par(g) : C::k_par(g));
+            if (g < gc - NR / 2) continue;
+            mbar_wait(&rawfull[(2 * g + q) % NR], (2 * g + q) / NR & 1);
+          } else if (g >= gc - (q ? C::VS : C::KS)) {
+            const int s = q ? C::v_slot(g) : C::k_slot(g);
+            mbar_wait(s == ends_slot ? &land[s] : &full[s],
+                      s == ends_slot ? par >> s & 1
+                      : q            ? C::v_par(g)
+                                     : C::k_par(g));
           }
         }
       }
-    } else if (!WIDEN && warp == C::kLoad + 1) {
-      // ===================== ends of V ====================================
-      // Rows of a chunk that no pair attends to are zeros, so that 0 times
-      // them stays 0: the copies left them as they were, or brought in what
-      // lies beside the sequence.
-      int gc = 0;
-      uint32_t par = 0;  // parities of `land`, a bit a slot
-      bool ok = true;
-      Seg sg;
-      do {
-        sg = here();
-        for (int k = 0; ok && k < sg.nch; ++k, ++gc) {
-          const int pos0 = (sg.c0() + k) * kN;
-          const int a = max(sg.q.lo - pos0, 0);
-          const int z = min(sg.q.T - pos0, kN);
-          if (z - a == kN) continue;
-          const int s = C::v_slot(gc);
-          if (!wait_all(&land[s], par >> s & 1)) {
-            give_up();
-            ok = false;
-            break;
-          }
-          par ^= 1u << s;
-          uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
-          // 16-byte pieces of the rows [0, a) and [z, 128)
-          constexpr int PC = D / 8;
-          const int rows = kN - (z - a);
-          for (int i = lane; i < rows * PC; i += 32) {
-            int r = i / PC;
-            const int c = i - r * PC;
-            if (r >= a) r += z - a;
-            *reinterpret_cast<uint4 *>(tile + (r >> 6) * C::HALF +
-                                       (c >> 3) * C::COLS + (r & 63) * 128 +
-                                       (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]);
-        }
-      } while (next(sg));
     } else if (warp == C::kMma || warp == C::kMma + 1) {
       // ===================== MMA issue ====================================
       constexpr uint32_t idS = WIDEN ? umma_idesc_f16(kM, kS, false)
