@@ -126,7 +126,8 @@ typedef enum kvd_dtype {
  * scale pointers are unused. Supported: head_dim 128, an even block_size,
  * kv_append and GQA decode with n_h / n_kv of 1, 2 or 4 (dequantised in the
  * CUDA-core decode kernel; there is no fp4 MMA), and the calls of
- * kvd_prompt.h, whose kvd_gqa_extend takes every n_h / n_kv up to 128.
+ * kvd_prompt.h and kvd_tree.h, whose kvd_gqa_extend, kvd_gqa_tree and
+ * kvd_gqa_cross take every n_h / n_kv up to 128.
  */
 typedef struct kvd_cache {
   void *k;
@@ -163,8 +164,9 @@ typedef struct kvd_cache {
  *   window_start  device int32 [batch] replay starts s_b, or NULL (s_b = 0);
  *                 read like seq_lens (KVD_SEQS_STABLE covers it too)
  * window and window_start are honoured by kvd_gqa_decode,
- * kvd_gqa_append_decode, kvd_gqa_decode_noalloc and kvd_gqa_extend
- * (kvd_prompt.h, from each row's own position); the other calls need
+ * kvd_gqa_append_decode, kvd_gqa_decode_noalloc, kvd_gqa_extend
+ * (kvd_prompt.h) and kvd_gqa_tree (kvd_tree.h; both from each row's own
+ * position); kvd_gqa_cross honours window_start alone; the other calls need
  * window == 0 and window_start == NULL (else KVD_ERR_UNSUPPORTED).
  *
  * Kernels of this library may start while the kernel before them on the

@@ -80,10 +80,15 @@ kvd_status kvd_tree_plan(const int32_t *parents, const int32_t *start,
  *   lse        device fp32 [rows][n_h] or NULL
  *   workspace  at least kvd_attend_workspace_size() bytes, 256-byte aligned
  *              (NULL when that is 0); see "Workspace" in kvd.h
- * A sequence with T_b < n_b is skipped and flagged KVD_DEVERR_LEN. Supported:
- * bf16 and fp8 caches with head_dim 64 or 128 and MXFP4 caches, n_h / n_kv of
- * 1 .. 128, at most 1024 sequences a call. seqs->flags must be valid and are
- * ignored.
+ * A sequence with T_b < n_b is skipped and flagged KVD_DEVERR_LEN. positions
+ * below T_b - n_b are taken as that. Scores and sums in fp32; the probabilities
+ * enter the second product as bf16 (bf16 caches) or f16, each rounded by half a
+ * step. What a call does not attend to may hold anything; a value of V that is
+ * not finite, at a position that some row of the sequence sees, may show in
+ * rows that do not see it as well. Supported: bf16 and fp8 caches with head_dim
+ * 64 or 128 and MXFP4 caches, n_h / n_kv of 1 .. 128, at most 1024 sequences a
+ * call, bf16 caches of less than 2^31 rows (blocks x heads x slots), lengths up
+ * to 2^31 - 256. seqs->flags must be valid and are ignored.
  */
 kvd_status kvd_gqa_tree(const kvd_cache *cache, const kvd_seqs *seqs,
                         const int32_t *row_start, int32_t max_rows,
@@ -136,7 +141,7 @@ kvd_status kvd_attend_workspace_size(const kvd_cache *cache,
  * or a bad block id KVD_DEVERR_BLOCK. No block that receives a row may be
  * shared with another sequence of the call. Errors: KVD_ERR_NULL,
  * KVD_ERR_SHAPE (caches that differ), KVD_ERR_UNSUPPORTED (width above
- * KVD_TREE_NODES, rows that are not multiples of 8 bytes).
+ * KVD_TREE_NODES, more than 1024 sequences).
  */
 kvd_status kvd_kv_keep(const kvd_cache *caches, int32_t n_caches,
                        const int32_t *block_table, int32_t max_blocks_per_seq,

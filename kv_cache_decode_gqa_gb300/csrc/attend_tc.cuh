@@ -11,7 +11,51 @@
 // a pair) turns one into P, the tensor core does PV of the other and the
 // scores that follow it. A unit of at most 128 pairs has one tile; then both
 // halves work for it, on even and odd chunks, and their states are merged at
-// its end.
+// its end. The masks of a tree touch the chunks that hold its nodes only: 32
+// columns at a time, a word of bits shifted to the chunk's first position.
+//
+// The work of a call is the list of all its units' chunks. A persistent launch
+// with one CTA per SM takes equal shares of it; units that two shares cut leave
+// partial results, which a second launch merges (attend.cu).
+//
+// bf16 caches feed the MMAs as they are (bf16 products, exact in fp32), rows
+// copied by swizzled TMA boxes; rows of fp8 and MXFP4 caches come raw, by bulk
+// copies, and eight warps widen them to f16 (exact: 4 and 6 significand bits;
+// E4M3's per-head scales go into the scores' and the outputs' factors).
+// Rounded to 16 bits are the probabilities -- to bf16 beside bf16 values, as
+// the MMA wants one type for both operands: half a step, 2^-9 to 2^-8 of each,
+// the size of the bf16 output's own rounding (an error of 0.0023 of the result
+// against 0.0017 for a plain fp32 computation rounded once); to f16 beside f16,
+// 2^-11 -- and, for f16, queries scaled by a power of two a (row, head), which
+// is exact but for elements 2^-29 of the largest. Scores, references and sums
+// are fp32. The reference of a pair moves only when a score passes it by 2^8
+// (f16: from 2^7 below the maximum, so that P stays below 2^15 and drops only
+// what is 2^-32 of the largest); O is then rescaled in tensor memory.
+//
+// What bounds it: with many pairs the products, 512 cycles an M = N = K = 128
+// one (scores of 64 positions take half as long again as they should, 48
+// cycles a step of K = 16 against 32: the operands of both come from shared
+// memory, 6 KB a step), and in practice the chain from a product's end over
+// the softmax to the next product, about 3,100 cycles a chunk of two tiles
+// against 2,576 for its products; with few, HBM, as long as that chain keeps
+// up (1,850 cycles a chunk of one tile, K and V of which take 2,900 at HBM's
+// rate). Measured (us, calls in a graph): 2,011 rows over 20,011 positions, 64
+// heads of 8 kv heads, bf16, 840 (1,570 TFLOP/s, 81% of cuBLAS's rate); trees
+// of 500 nodes in 16 sequences over 9,200 positions (620 MB) 185; of 250 nodes
+// in 32 sequences over 4,600 positions of an fp8 cache (310 MB) 102; of 480
+// nodes in 8 sequences over 18,400 positions of an MXFP4 cache 263; one tree of
+// 16 nodes over 4,000 positions 21.
+//
+// Measured and not kept (the first of these cases, us): two threads a pair and
+// step, of 32 columns each, 1,060 against 1,017 then (more warps to issue for,
+// a barrier a step); V through the load path (cp.async by four warps) 902
+// against 882; pairs of CTAs (cta_group::2, M = 256, half of the tiles each)
+// 1,003, trees of 500 nodes 265, MXFP4 299; two-tile chunks weighted 3 to 2 in
+// the shares 970 (the wider arithmetic slowed every role). What was: MMA
+// operands in uniform registers (1,198 to 1,050), no register spills (what
+// local memory holds comes from L2 beside this much shared memory: 1,810 to
+// 1,198), queries loaded in whole lines and outputs stored 32 bytes at a time
+// (1,017 to 849).
 #pragma once
 
 #include <algorithm>

@@ -10,8 +10,10 @@ constexpr int kPlanThreads = kTreeNodes;
 
 // One CTA a sequence, one thread a node: the thread walks up the parents,
 // which lie in shared memory, and sets a bit of its mask a step. A walk is as
-// long as the node is deep; sums and doubling would save steps in chains of a
-// hundred nodes only.
+// long as the node is deep, some ten steps for a drafted tree and 256 for a
+// chain of that many. Latency bounds it: a launch, two dependent loads, the
+// walk and the stores (2.9 us for one tree of 16 nodes, 5.7 us for 256 trees of
+// 117 on average, in a graph; the bytes would take 0.2).
 __global__ void __launch_bounds__(kPlanThreads)
     tree_plan_kernel(const __grid_constant__ TreePlanParams p) {
   __shared__ int16_t up[kTreeNodes];
@@ -60,14 +62,16 @@ __global__ void __launch_bounds__(kPlanThreads)
     p.positions[row] = (int)((uint32_t)p.start[b] + (uint32_t)(depth - 1));
 }
 
-// Bytes of one access of the move: rows of MXFP4 are multiples of 8.
 constexpr int kKeepThreads = 256;
 
-// A thread moves one piece of 8 bytes of every accepted row of a (cache
-// tensor, sequence, head), eight rows' loads in flight: with an ascending path
-// from 0 up, row j's source path[j] >= j is overwritten by row path[j] at the
-// earliest, so that loads stay ahead of the stores when rows are taken in
-// order.
+// A thread moves one piece of 8 bytes (rows of MXFP4 are multiples of 8) of
+// every accepted row of a (cache tensor, sequence, head), eight rows' loads in
+// flight: with an ascending path from 0 up, row j's source path[j] >= j, so
+// that no store of an earlier row reaches a later row's source when rows are
+// taken in order. All layers go in one launch, for which the launch and three
+// dependent loads (path, block table, rows) take most of the time: 4.2 us for
+// one sequence in 32 layers, 8.5 us for 16 sequences in 80 (21 MB: 2.5 TB/s of
+// scattered rows of 128 bytes), in a graph.
 __global__ void __launch_bounds__(kKeepThreads)
     keep_kernel(const __grid_constant__ KeepParams p) {
   __shared__ long at[kTreeNodes + 1], to[kTreeNodes];
