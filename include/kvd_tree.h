@@ -130,7 +130,8 @@ kvd_status kvd_attend_workspace_size(const kvd_cache *cache,
  * for j < n_keep[b]; nothing else changes (the caller's new length is
  * start[b] + n_keep[b]).
  *   caches     HOST array of n_caches caches (the layers') of one shape and
- *              type, K and V or all K-only; a cache may not be listed twice
+ *              type, K and V or all K-only; neither a cache nor a tensor of
+ *              one may be listed twice (but K and V may be one tensor)
  *   start      device int32 [batch]
  *   path       device int32 [batch][width], a sequence's accepted nodes from
  *              the root on: ascending (a node follows its parent), from 0 up

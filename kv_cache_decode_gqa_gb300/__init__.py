@@ -922,8 +922,11 @@ class CacheList:
         self.structs = (_native.KvdCache * len(self.caches))(
             *[c.struct() for c in self.caches])
         tensors = [t for c in self.caches for t in (c.k, c.v)]
-        if len({c.k.data_ptr() for c in self.caches}) != len(self.caches):
-            raise ValueError("a cache is listed twice")
+        # (one tensor may be both K and V of a cache)
+        at = [{t.data_ptr() for t in (c.k, c.v) if t is not None}
+              for c in self.caches]
+        if len(set().union(*at)) != sum(map(len, at)):
+            raise ValueError("a cache or a tensor is listed twice")
         self.device = _one_device(*tensors)
 
 

@@ -1755,7 +1755,8 @@ kvd_status kvd_kv_keep(const kvd_cache *caches, int32_t n_caches,
     p.tensors = 0;
     for (int32_t j = i; j < std::min(n_caches, i + kvd::kKeepCaches); ++j) {
       p.data[p.tensors++] = static_cast<uint8_t *>(caches[j].k);
-      if (caches[j].v)
+      // (a tensor that holds both K and V is moved once)
+      if (caches[j].v && caches[j].v != caches[j].k)
         p.data[p.tensors++] = static_cast<uint8_t *>(caches[j].v);
     }
     const cudaError_t e =

@@ -725,6 +725,46 @@ def test_kv_keep(dtype, d, layers):
     assert K.device_error() == 0
 
 
+def test_kv_keep_of_keys_and_values_in_one_tensor():
+    """A row is moved once: with two passes over one tensor the second could
+    take rows that the first has replaced."""
+    g = _gen(5)
+    bt, blocks = _table(g, [64, 64], 16)
+    layers = []
+    for _ in range(40):
+        c = _cache(g, blocks, 2, 16, "bf16", 128)
+        layers.append(dataclasses.replace(c, v=c.k))
+    path = [[0] + list(range(2, 40)), list(range(1, 40))]
+    want = [c.k.clone() for c in layers]
+    for t in want:
+        old = t.clone()
+        for b in range(2):
+            for j, x in enumerate(path[b]):
+                x, y = 7 + x, 7 + j
+                t[bt[b, y // 16].item(), :, y % 16] = old[
+                    bt[b, x // 16].item(), :, x % 16]
+    K.kv_keep(layers, bt, _i32([7, 7]), _i32(path), _i32([39, 39]))
+    for c, w in zip(layers, want):
+        assert torch.equal(c.k, w)
+    assert K.device_error() == 0
+
+
+def test_a_tensor_listed_twice_is_refused():
+    g = _gen(6)
+    t = [_cache(g, 2, 2, 16, "bf16", 64) for _ in range(2)]
+    a, b, c, d = t[0].k, t[0].v, t[1].k, t[1].v
+
+    def cache(k, v):
+        return dataclasses.replace(t[0], k=k, v=v)
+    for x, y in ((cache(a, b), cache(a, c)), (cache(a, b), cache(c, b)),
+                 (cache(a, b), cache(c, a)), (cache(a, a), cache(b, a)),
+                 (cache(a, b), cache(a, b)), (cache(a, None), cache(a, None))):
+        with pytest.raises(ValueError, match="twice"):
+            K.CacheList([x, y])
+    assert len(K.CacheList([cache(a, a), cache(b, b)]).caches) == 2
+    assert len(K.CacheList([cache(a, b), cache(c, d)]).caches) == 2
+
+
 def test_kv_keep_long_paths():
     g = _gen(3)
     n = K.TREE_NODES
