@@ -87,8 +87,8 @@ kvd_status kvd_tree_plan(const int32_t *parents, const int32_t *start,
  * not finite, at a position that some row of the sequence sees, may show in
  * rows that do not see it as well. Supported: bf16 and fp8 caches with head_dim
  * 64 or 128 and MXFP4 caches, n_h / n_kv of 1 .. 128, at most 1024 sequences a
- * call, bf16 caches of less than 2^31 rows (blocks x heads x slots), lengths up
- * to 2^31 - 256. seqs->flags must be valid and are ignored.
+ * call, bf16 caches of less than 2^31 rows (blocks x heads x slots) with K and
+ * V less than 2^40 bytes apart, lengths up to 2^31 - 256. seqs->flags must be valid and are ignored.
  */
 kvd_status kvd_gqa_tree(const kvd_cache *cache, const kvd_seqs *seqs,
                         const int32_t *row_start, int32_t max_rows,

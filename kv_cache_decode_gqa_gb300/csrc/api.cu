@@ -1535,6 +1535,14 @@ kvd_status check_attend(const kvd_cache *c, const kvd_seqs *s, int rows,
       (double)c->num_blocks * c->n_kv * c->block_size >= 2147483648.0)
     return fail(KVD_ERR_UNSUPPORTED, "%s: bf16 caches of 2^31 rows (blocks x "
                 "heads x slots) and more", what);
+  if (c->dtype == KVD_BF16) {
+    // one tensor map holds both, the other a stride away
+    const uint64_t k = reinterpret_cast<uint64_t>(c->k);
+    const uint64_t v = reinterpret_cast<uint64_t>(c->v);
+    if ((k < v ? v - k : k - v) >> 40)
+      return fail(KVD_ERR_UNSUPPORTED, "%s: K and V of a bf16 cache must lie "
+                  "less than 2^40 bytes apart", what);
+  }
   return KVD_OK;
 }
 

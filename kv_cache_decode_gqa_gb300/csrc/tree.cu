@@ -74,8 +74,9 @@ constexpr int kKeepThreads = 256;
 // scattered rows of 128 bytes), in a graph.
 __global__ void __launch_bounds__(kKeepThreads)
     keep_kernel(const __grid_constant__ KeepParams p) {
-  __shared__ long at[kTreeNodes + 1], to[kTreeNodes];
-  pdl_trigger();
+  __shared__ long at[kTreeNodes], to[kTreeNodes];
+  // (no early trigger: the next launch starts when the rows are moved, so that
+  // a decode call behind that one may declare its older rows final)
   pdl_wait();
   const int b = blockIdx.y, tid = threadIdx.x;
   const int n = p.n_keep[b];

@@ -129,6 +129,17 @@ def test_tree_and_cross_refusals_of_their_own(lib):
     assert _cross(lib, s=_seqs(batch=6), row_start=None, max_rows=2) == 2
 
 
+@pytest.mark.parametrize("call", [_tree, _cross])
+def test_keys_and_values_far_apart_are_refused(lib, call):
+    for k, v in ((FAKE, FAKE + 2 ** 40), (FAKE + 2 ** 41, FAKE)):
+        assert call(lib, _cache(k=k, v=v)) == 3 and _says(lib, "apart")
+    # (rows = 0: over before anything is read)
+    near = _cache(k=FAKE, v=FAKE + 2 ** 40 - 16)
+    assert call(lib, near, q=_rows(rows=0)) == 0
+    assert call(lib, _cache(v=FAKE + 2 ** 40, dtype=1, k_scale=FAKE,
+                            v_scale=FAKE), q=_rows(rows=0)) == 0
+
+
 def test_workspace_size_validation(lib):
     size = ctypes.c_size_t(0)
     f = lib.kvd_attend_workspace_size
