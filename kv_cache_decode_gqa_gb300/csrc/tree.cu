@@ -92,13 +92,15 @@ __global__ void __launch_bounds__(kKeepThreads)
       bad |= DEVERR_POS;
       return 0L;
     }
-    const int blk =
-        p.block_table[(long)b * p.max_blocks + pos / p.block_size];
+    // (a sum of two int32: below 2^32, and a division of 32 bits)
+    const uint32_t x = (uint32_t)pos, bs = (uint32_t)p.block_size;
+    const uint32_t e = x / bs;
+    const int blk = p.block_table[(long)b * p.max_blocks + e];
     if (blk < 0 || blk >= p.num_blocks) {
       bad |= DEVERR_BLOCK;
       return 0L;
     }
-    return (long)blk * p.n_kv * p.block_size + pos % p.block_size;
+    return (long)blk * p.n_kv * p.block_size + (x - e * bs);
   };
   if (tid < n) {
     const int x = path[tid];
@@ -111,13 +113,18 @@ __global__ void __launch_bounds__(kKeepThreads)
     return;
   }
   const int pieces = p.row / 8;
+  // 32 bits where the values have them: a fraction of the instructions
+  auto div = [](long a, int b) {
+    return a >> 32 ? a / b : (long)((uint32_t)a / (uint32_t)b);
+  };
   const long items = (long)p.tensors * p.n_kv * pieces;
   for (long x = (long)blockIdx.x * kKeepThreads + tid; x < items;
        x += (long)gridDim.x * kKeepThreads) {
-    const int c = (int)(x % pieces);
-    const long th = x / pieces;
-    const long head = th % p.n_kv * p.block_size;
-    uint8_t *base = p.data[th / p.n_kv] + c * 8;
+    const long th = div(x, pieces);
+    const int c = (int)(x - th * pieces);
+    const long t = div(th, p.n_kv);
+    const long head = (th - t * p.n_kv) * p.block_size;
+    uint8_t *base = p.data[t] + c * 8;
     for (int j0 = 0; j0 < n; j0 += 8) {
       uint2 v[8];
 #pragma unroll
