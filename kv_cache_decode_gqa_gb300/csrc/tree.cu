@@ -64,17 +64,19 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 constexpr int kKeepThreads = 256;
 
-// A thread moves one piece of 8 bytes (rows of MXFP4 are multiples of 8) of
-// every accepted row of a (cache tensor, sequence, head), eight rows' loads in
-// flight: with an ascending path from 0 up, row j's source path[j] >= j, so
+// A thread moves one piece of 16 bytes (8 where the rows are multiples of 8
+// only, MXFP4's) of every accepted row of a (cache tensor, sequence, head),
+// eight rows' loads in flight: with an ascending path from 0 up, row j's source path[j] >= j, so
 // that no store of an earlier row reaches a later row's source when rows are
 // taken in order. All layers go in one launch, for which the launch and three
-// dependent loads (path, block table, rows) take most of the time: 4.2 us for
-// one sequence in 32 layers, 8.5 us for 16 sequences in 80 (21 MB: 2.5 TB/s of
-// scattered rows of 128 bytes), in a graph.
+// dependent loads (path, block table, rows) take most of the time: 3.7 us for
+// one sequence in 32 layers, 5.7 us for 16 sequences in 80 (21 MB: 3.7 TB/s of
+// scattered rows of 128 bytes), in a graph. (Pieces of 8 bytes for every type:
+// 7.9 us, and with divisions of 64 bits 8.7.)
+template <class Piece>
 __global__ void __launch_bounds__(kKeepThreads)
     keep_kernel(const __grid_constant__ KeepParams p) {
-  __shared__ long at[kTreeNodes], to[kTreeNodes];
+  __shared__ long at[kTreeNodes], to[kTreeNodes];  // bytes, of head 0
   // (no early trigger: the next launch starts when the rows are moved, so that
   // a decode call behind that one may declare its older rows final)
   pdl_wait();
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kKeepThreads)
       bad |= DEVERR_BLOCK;
       return 0L;
     }
-    return (long)blk * p.n_kv * p.block_size + (x - e * bs);
+    return ((long)blk * p.n_kv * p.block_size + (x - e * bs)) * p.row;
   };
   if (tid < n) {
     const int x = path[tid];
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kKeepThreads)
     if (first && bad) report(p.err, bad);
     return;
   }
-  const int pieces = p.row / 8;
+  const int pieces = p.row / (int)sizeof(Piece);
   // 32 bits where the values have them: a fraction of the instructions
   auto div = [](long a, int b) {
     return a >> 32 ? a / b : (long)((uint32_t)a / (uint32_t)b);
@@ -123,20 +125,18 @@ __global__ void __launch_bounds__(kKeepThreads)
     const long th = div(x, pieces);
     const int c = (int)(x - th * pieces);
     const long t = div(th, p.n_kv);
-    const long head = (th - t * p.n_kv) * p.block_size;
-    uint8_t *base = p.data[t] + c * 8;
+    uint8_t *base = p.data[t] + (th - t * p.n_kv) * p.block_size * p.row +
+                    c * (int)sizeof(Piece);
     for (int j0 = 0; j0 < n; j0 += 8) {
-      uint2 v[8];
+      Piece v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j0 + j < n)
-          v[j] = *reinterpret_cast<const uint2 *>(
-              base + (at[j0 + j] + head) * p.row);
+          v[j] = *reinterpret_cast<const Piece *>(base + at[j0 + j]);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j0 + j < n && at[j0 + j] != to[j0 + j])
-          *reinterpret_cast<uint2 *>(base + (to[j0 + j] + head) * p.row) =
-              v[j];
+          *reinterpret_cast<Piece *>(base + to[j0 + j]) = v[j];
     }
   }
 }
@@ -149,9 +149,10 @@ cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_keep(const KeepParams &p, cudaStream_t s) {
-  const long items = (long)p.tensors * p.n_kv * (p.row / 8);
+  const bool wide = p.row % 16 == 0;
+  const long items = (long)p.tensors * p.n_kv * (p.row / (wide ? 16 : 8));
   const long blocks = (items + kKeepThreads - 1) / kKeepThreads;
-  return launch_pdl(keep_kernel,
+  return launch_pdl(wide ? keep_kernel<uint4> : keep_kernel<uint2>,
                     dim3((unsigned)(blocks < 4096 ? blocks : 4096), p.batch),
                     dim3(kKeepThreads), 0, s, 1, p);
 }
