@@ -83,9 +83,10 @@ kvd_status kvd_tree_plan(const int32_t *parents, const int32_t *start,
  * A sequence with T_b < n_b is skipped and flagged KVD_DEVERR_LEN. positions
  * below T_b - n_b are taken as that. Scores and sums in fp32; the probabilities
  * enter the second product as bf16 (bf16 caches) or f16, each rounded by half a
- * step. What a call does not attend to may hold anything; a value of V that is
+ * step. Positions that no row of a sequence sees (nodes that no mask has,
+ * context before every row's window) may hold anything; a value of V that is
  * not finite, at a position that some row of the sequence sees, may show in
- * rows that do not see it as well. Supported: bf16 and fp8 caches with head_dim
+ * rows that see other positions only (rows that see nothing stay 0). Supported: bf16 and fp8 caches with head_dim
  * 64 or 128 and MXFP4 caches, n_h / n_kv of 1 .. 128, at most 1024 sequences a
  * call, bf16 caches of less than 2^31 rows (blocks x heads x slots) with K and
  * V less than 2^40 bytes apart, lengths up to 2^31 - 256. seqs->flags must be valid and are ignored.

@@ -119,7 +119,7 @@ struct ACfg {
   __device__ static __forceinline__ uint32_t v_par(int g) {
     return g / VS & 1;
   }
-  static constexpr int NR_FIT = WIDEN ? (ROOM - NS * TILE) / RAW : 0;
+  static constexpr int NR_FIT = WIDEN ? (ROOM - NS * TILE) / (RAW + 16) : 0;
   static constexpr int NR = NR_FIT > 12 ? 12 : NR_FIT & ~1;
   static constexpr int Q_OFF = 0;
   static constexpr int KV_OFF = QS * TILE;
@@ -130,7 +130,8 @@ struct ACfg {
   static constexpr int BARS = 3 * NS + 2 * NR + 2 * QS + 13;
   static constexpr int FLAG_OFF = BAR_OFF + BARS * 8;
   static constexpr int SEQ_OFF = FLAG_OFF + 32;  // Seq [kSeqs]
-  static constexpr int SMEM = SEQ_OFF + kSeqs * 32;
+  static constexpr int SEEN_OFF = SEQ_OFF + kSeqs * 32;  // uint32 [NR][4]
+  static constexpr int SMEM = SEEN_OFF + NR * 16;
   static_assert(NS >= 4 && (!WIDEN || NR >= 2) && SMEM <= 227 * 1024,
                 "shared memory");
   static_assert(RAW % 128 == 0 && FLAG_OFF % 8 == 0, "alignment");
@@ -423,6 +424,42 @@ __device__ __forceinline__ uint32_t seen_bits(int p0, int lo, int ctx, int n,
   return bits;
 }
 
+// What no row of a sequence sees may hold anything, but meets a probability of
+// 0 in the product with V, where 0 times NaN would be NaN: such rows of V are
+// zeros there. The next two are called by whole warps.
+//
+// First position of the context that some row of sequence b sees (q.ctx or more:
+// none). q.lo, which the work is shared out by, stands for a row at the tree's
+// first position.
+__device__ __forceinline__ int first_seen(const AttendParams &p, const Seq &q,
+                                          int b, int lane) {
+  if (!p.masks) return q.lo;
+  int lo = p.win_start ? max(p.win_start[b], 0) : 0;
+  if (p.window > 0) {
+    int pos = INT_MAX;
+    for (int i = lane; i < q.n; i += 32)
+      pos = min(pos, p.positions[q.r0 + i]);
+    pos = __reduce_min_sync(0xffffffffu, pos);
+    lo = max(lo, max(pos, q.ctx) - (p.window - 1));
+  }
+  return lo;
+}
+
+// Bits of the 32 positions from p0 on that some row of the sequence sees
+// (`first`: first_seen).
+__device__ __forceinline__ uint32_t seen_by_some(const AttendParams &p,
+                                                 const Seq &q, int first,
+                                                 int p0, int lane) {
+  if (!p.masks || p0 + 32 <= q.ctx)
+    return seen_bits(p0, first, q.ctx, 0, nullptr, 0);
+  uint32_t bits = 0;
+#pragma unroll 4
+  for (int i = lane; i < q.n; i += 32)
+    bits |= seen_bits(p0, first, q.ctx, q.n,
+                      p.masks + (long)(q.r0 + i) * p.words, p.words);
+  return __reduce_or_sync(0xffffffffu, bits);
+}
+
 template <int DT, int D, int QS>
 __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
     attend_tc_kernel(const __grid_constant__ TcParams tp) {
@@ -458,6 +495,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
   long *s_off = reinterpret_cast<long *>(flags + 2);
 
   Seq *near = reinterpret_cast<Seq *>(smem + C::SEQ_OFF);
+  // rows of the raw V slots that some row of the sequence attends to
+  uint32_t *seen_v = reinterpret_cast<uint32_t *>(smem + C::SEEN_OFF);
 
   // (through a shuffle: the compiler then knows the warp's number, and what
   // follows from it, to be the same for its lanes, and keeps the operands of
@@ -859,6 +898,11 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       const bool second = !two && sg.nch > 1;
       const int col0 = two ? 0 : t * (D / 2), step = two ? 64 : 32;
       const uint32_t to = tl + kColO + (two ? D * t : 0);
+      // (a weight of 0 is that of a tile whose pair saw nothing; its sums are
+      // NaN beside values that are not finite)
+      auto times = [](uint32_t o, float w) {
+        return w == 0.f ? 0.f : __uint_as_float(o) * w;
+      };
       auto emit = [&](int col, const float (&y)[32]) {
         if (whole) {
           uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + col);
@@ -888,8 +932,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           float y[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            y[i] = __uint_as_float(o[0][i]) * w0;
-          if (second) {
+            y[i] = times(o[0][i], w0);
+          if (second && w1 != 0.f) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               y[i] = fmaf(__uint_as_float(o[1][i]), w1, y[i]);
@@ -898,7 +942,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           if (two) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              y[i] = __uint_as_float(o[1][i]) * w0;
+              y[i] = times(o[1][i], w0);
             if (live) emit(g + 32, y);
           }
         }
@@ -942,10 +986,10 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
           }
           const uint8_t *src =
               smem + C::RAW_OFF + rs * C::RAW + r * row_bytes(D, DT);
-          const int pos = (sg.c0() + i) * kN + r;
-          // a row that was not copied, or that no pair sees: zeros, so that 0
-          // times it stays 0
-          const bool dead = pos < sg.q.lo || pos >= sg.q.T;
+          // a row of V that was not copied, or that no pair sees: zeros, so
+          // that 0 times it stays 0 (scores of such a row are masked)
+          const bool dead =
+              is_v && !(seen_v[4 * rs + (r >> 5)] >> lane & 1);
           const int st = is_v ? C::v_slot(gc) : C::k_slot(gc);
           const uint32_t free_par =
               (is_v ? C::v_par(gc) : C::k_par(gc)) ^ 1;
@@ -1090,12 +1134,15 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       bool go = true;
       const int q = warp == C::kLoadV;
       int gc = 0;  // chunks so far
-      // bf16: rows of a V tile that no pair attends to are zeros, so that 0 times
-      // them stays 0: the copies left them as they were, or brought in what lies
-      // beside the sequence. Such a tile arrives on a barrier of its own
-      // (`land`); its rows [0, ea) and [ez, 128) are filled behind the copies of
-      // the next one, and before any wait.
-      int ends_slot = -1, ea = 0, ez = 0;
+      // Rows of a V tile that no pair attends to are zeros, so that 0 times
+      // them stays 0. Beside raw rows lie the bits of those attended to, for
+      // the warps that widen them. bf16: the copies left such rows as they were,
+      // or brought in what lies beside the sequence, or nodes that no mask has. A
+      // tile that may have them arrives on a barrier of its own (`land`); rows
+      // whose bits are not in `seen` are filled behind the copies of the next
+      // one, and before any wait.
+      int ends_slot = -1;
+      uint32_t seen[4] = {};
       uint32_t par = 0;  // parities of `land`, a bit a slot
       auto fill_ends = [&]() {
         if (ends_slot < 0) return;
@@ -1107,15 +1154,23 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         }
         par ^= 1u << s;
         uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
-        constexpr int PC = D / 8;  // 16-byte pieces of a row
-        const int rows = kN - (ez - ea);
-        for (int i = lane; i < rows * PC; i += 32) {
-          int r = i / PC;
-          const int e = i - r * PC;
-          if (r >= ea) r += ez - ea;
-          *reinterpret_cast<uint4 *>(tile + (r >> 6) * C::HALF +
-                                     (e >> 3) * C::COLS + (r & 63) * 128 +
-                                     (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+        constexpr int PC = D / 8;  // 16-byte pieces of a row, a lane each
+        const int e = lane % PC;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          for (uint32_t m = ~seen[w]; m != 0;) {
+            int r = -1;  // this lane's row of the next 32 / PC
+#pragma unroll
+            for (int k = 0; k < 32 / PC; ++k) {
+              if (k == lane / PC && m != 0) r = 32 * w + __ffs(m) - 1;
+              m &= m - 1;
+            }
+            if (r >= 0)
+              *reinterpret_cast<uint4 *>(tile + (r >> 6) * C::HALF +
+                                         (e >> 3) * C::COLS + (r & 63) * 128 +
+                                         (e & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1124,6 +1179,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       Seg sg;
       do {
         sg = here();
+        const int first =
+            q == 1 ? first_seen(p, sg.q, wk.b, lane) : sg.q.lo;
         const int c0 = sg.c0(), c1 = c0 + sg.nch;
         for (int cb = c0; go && cb < c1; cb += batch) {
           // this lane's piece: positions [x0, x1), at row `at` of the cache
@@ -1173,9 +1230,9 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                                        : q   ? C::v_par(gc)
                                              : C::k_par(gc)) ^
                                       1;
-            bool ends = false;
+            const bool ends =
+                q == 1 && (p0 < first || p0 > sg.q.ctx - kN);
             if constexpr (!WIDEN) {
-              ends = q == 1 && (p0 < sg.q.lo || p0 > sg.q.T - kN);
               if (!__all_sync(0xffffffffu, mbar_test_wait(free, free_par)))
                 fill_ends();
             }
@@ -1211,11 +1268,6 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                 constexpr int ROW = row_bytes(D, DT);
                 uint8_t *dst = smem + C::RAW_OFF + s * C::RAW;
                 const uint8_t *src = q ? p.v : p.k;
-                // (copies may land before the expectation is set: the phase
-                // ends with that arrival at the earliest)
-                if (lq == 0)
-                  mbar_arrive_expect_tx(&rawfull[s],
-                                        (uint32_t)(t1 - t0) * ROW);
                 for (int i = lq;; i += L) {
                   int a0 = x0, a1 = x1;
                   long row = at;
@@ -1232,9 +1284,27 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
               fill_ends();
               if (ends) {
                 ends_slot = s;
-                ea = max(sg.q.lo - p0, 0);
-                ez = min(sg.q.T - p0, kN);
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                  seen[w] =
+                      seen_by_some(p, sg.q, first, p0 + 32 * w, lane);
               }
+            } else {
+              if (q == 1) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  const uint32_t bits =
+                      ends ? seen_by_some(p, sg.q, first, p0 + 32 * w, lane)
+                           : 0xffffffffu;
+                  if (lane == w) seen_v[4 * s + w] = bits;
+                }
+                __syncwarp();
+              }
+              // (copies may have landed by now: the phase ends with this
+              // arrival at the earliest, which publishes the bits too)
+              if (mine == j && lq == 0)
+                mbar_arrive_expect_tx(
+                    &rawfull[s], (uint32_t)(t1 - t0) * row_bytes(D, DT));
             }
           }
         }

@@ -410,6 +410,102 @@ def test_masked_nodes_with_infinite_keys():
 
 
 # ---------------------------------------------------------------------------
+# what no row sees
+# ---------------------------------------------------------------------------
+def _spoil(c, bt, b, positions):
+    """NaN (infinities beside them) in K and V at these positions."""
+    for i, p in enumerate(positions):
+        blk, slot = bt[b, p // c.block_size].item(), p % c.block_size
+        for t in (c.k, c.v):
+            t[blk, :, slot] = (0x7f if c.dtype != "bf16" else
+                               math.inf if i % 2 else math.nan)
+
+
+UNSEEN = [("bf16", 128, 8, 2, 64), ("bf16", 128, 12, 1, 16),
+          ("bf16", 64, 6, 2, 5), ("fp8", 128, 8, 2, 64), ("fp8", 64, 4, 1, 16),
+          ("mxfp4", 128, 12, 1, 16), ("mxfp4", 128, 4, 2, 64)]
+
+
+@pytest.mark.parametrize("shape", UNSEEN)
+def test_nodes_that_no_row_sees_may_hold_anything(shape):
+    """Spare nodes of a fixed budget, whose bits are clear in every mask: their
+    rows of K and V change nothing, and rows that see nothing stay empty."""
+    dtype, d, n_h, n_kv, bs = shape
+    n, past, bound = [40, 6, 200, 33, 1], [100, 0, 5000, 127, 0], 200
+    case = (dtype, d, n_h, n_kv, bs, n, past, bound)
+    c, bt, lens, masks, pos, q = _setup(case, 61)
+    spare = [[3, 31, 32, 39], [0, 2, 3, 4, 5], list(range(150, 200)) + [7, 64],
+             [32], [0]]
+    rs = _starts(n)
+    for b, nodes in enumerate(spare):
+        for j in nodes:
+            masks[rs[b]:rs[b + 1], j // 32] &= ~(1 << (j % 32)) if (
+                j % 32 != 31) else 0x7fffffff
+    masks[45] = 0                # (no context either: this row sees nothing)
+    args = (bt, _i32(lens), max(lens), q, rs, bound, masks)
+    want = K.gqa_tree(c, *args)
+    _check(want, _reference(c, bt, lens, q, n,
+                            _tree_sees(n, past, masks, 7)))
+    for b, nodes in enumerate(spare):
+        _spoil(c, bt, b, [past[b] + j for j in nodes])
+    got = K.gqa_tree(c, *args)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for row in (45, sum(n) - 1):
+        assert bool((got[0][row] == 0).all())
+        assert bool(torch.isneginf(got[1][row]).all())
+    assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("shape", UNSEEN)
+@pytest.mark.parametrize("window", [1, 30, 200])
+def test_context_before_every_window_may_hold_anything(shape, window):
+    """No node at the tree's first position: the context before the lowest
+    window of a sequence is in no row's, and may hold anything."""
+    dtype, d, n_h, n_kv, bs = shape
+    n, past, bound = [20, 50, 3, 70], [500, 140, 1000, 64], 70
+    case = (dtype, d, n_h, n_kv, bs, n, past, bound)
+    c, bt, lens, masks, _, q = _setup(case, 67)
+    rng = np.random.default_rng(window)
+    up = [[past[b] + int(x) for x in rng.integers(3, 40, k)]
+          for b, k in enumerate(n)]
+    up[2] = [past[2] + 5000] * 3          # past all of the context
+    pos = [x for u in up for x in u]
+    starts = [0, 0, 0, 50]
+    owner = np.repeat(np.arange(4), n)
+    lo = [max(starts[b], p + 1 - window) for b, p in zip(owner, pos)]
+    args = (bt, _i32(lens), max(lens), q, _starts(n), bound, masks)
+    kw = dict(positions=_i32(pos), window=window, window_start=_i32(starts))
+    want = K.gqa_tree(c, *args, **kw)
+    _check(want, _reference(c, bt, lens, q, n,
+                            _tree_sees(n, past, masks, 3, lo)))
+    for b, u in enumerate(up):
+        first = max(starts[b], min(u) + 1 - window)
+        _spoil(c, bt, b, range(max(0, past[b] - window - 3),
+                               min(first, past[b])))
+    got = K.gqa_tree(c, *args, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "mxfp4"])
+def test_rows_that_see_nothing_beside_values_that_are_not_finite(dtype):
+    """A row that sees nothing gives 0 whatever its neighbours see, in units of
+    one tile and of two."""
+    for n_h, n, past in ((8, 6, 0), (64, 9, 0), (8, 200, 0)):
+        case = (dtype, 128, n_h, 1, 64, [n], [past], n)
+        c, bt, lens, masks, _, q = _setup(case, 71)
+        masks[:] = -1
+        masks[::3] = 0
+        _spoil(c, bt, 0, [1, n - 1])
+        out, lse = K.gqa_tree(c, bt, _i32(lens), max(lens), q, _starts([n]),
+                              n, masks)
+        assert bool((out[::3] == 0).all())
+        assert bool(torch.isneginf(lse[::3]).all())
+        assert bool(out[1].isnan().any())
+        assert K.device_error() == 0
+
+
+# ---------------------------------------------------------------------------
 # cross attention
 # ---------------------------------------------------------------------------
 CROSS = [
