@@ -678,6 +678,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int g = 0; g < kGroups / 4; ++g) sw[g] = 0;
       }
+      // the slot is free. (The copies into it are of another proxy: the fence
+      // orders loads that were issued but have not returned before them.)
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&rawempty[rs]);
       if ((rs += 2) >= nraw) rs -= nraw, rph ^= 1;

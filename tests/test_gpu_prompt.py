@@ -1228,3 +1228,24 @@ def test_calls_on_two_streams_at_once():
         assert torch.equal(out, jobs[i][1][0])
         assert torch.equal(lse, jobs[i][1][1])
     assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("counts,lens,n_h", [
+    ([333, 100, 1, 40], [900, 130, 2000, 40], 32),      # single CTAs
+    ([20, 9, 3], [3000, 64, 700], 32),
+    ([300, 200, 70], [1100, 200, 333], 64),             # pairs of CTAs
+])
+def test_extend_many_calls_give_the_same_bits(counts, lens, n_h):
+    """Short units among long ones, call after call: raw rows that a thread
+    still reads must not be overwritten by the next copy."""
+    g = _gen(231)
+    bt, blocks = _table(g, lens, 32)
+    c = _cache(g, blocks, 8, 32, "mxfp4")
+    q = _randn(g, sum(counts), n_h, D)
+    args = (c, bt, _i32(lens), max(lens), q, _starts(counts), max(counts))
+    want = K.gqa_extend(*args)
+    _check(*want, _attend_ref(c, bt, lens, counts, q))
+    outs = [K.gqa_extend(*args) for _ in range(600)]
+    assert all(torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
+               for o in outs)
+    assert K.device_error() == 0
