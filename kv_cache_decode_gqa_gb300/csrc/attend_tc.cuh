@@ -1195,9 +1195,11 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                 return 0;
               }
             } else {
-              const int lb = t0 / bs + i;
-              x0 = max(t0, lb * bs);
-              x1 = min(t1, (lb + 1) * bs);
+              // (64 bits: a block that holds position 2^31 - 257 may end past
+              // 2^31)
+              const long b0 = (long)(t0 / bs + i) * bs;
+              x0 = (int)min(max((long)t0, b0), (long)t1);
+              x1 = (int)min((long)t1, b0 + bs);
               if (x0 >= x1) {
                 x1 = x0;
                 return 0;
@@ -1275,7 +1277,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                   if (a0 < a1)
                     bulk_g2s(dst + (a0 - c * kN) * ROW, src + row * ROW,
                              (uint32_t)(a1 - a0) * ROW, &rawfull[s]);
-                  if (L < 32 || (t0 / bs + i + L) * bs >= t1) break;
+                  if (L < 32 || (long)(t0 / bs + i + L) * bs >= t1) break;
                 }
               }
             }

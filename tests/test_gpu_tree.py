@@ -711,6 +711,44 @@ def test_cache_beyond_32_bit_offsets():
     assert K.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp8", 64), ("fp8", 128),
+                                     ("mxfp4", 128)])
+@pytest.mark.parametrize("bs", [100, 512, 10 ** 6])
+def test_the_longest_lengths(dtype, d, bs):
+    """2^31 - 256 positions, through a table that repeats three blocks, whose
+    last block ends past 2^31; rows see the last few hundred."""
+    T = 2 ** 31 - 256
+    g = _gen(bs + d)
+    c = _cache(g, 3, 1, bs, dtype, d)
+    bt = (torch.arange(-(-T // bs), device="cuda", dtype=torch.int32) % 3)[None]
+    # the same rows as a short sequence, in blocks that divide the long ones
+    u = math.gcd(bs, 64)
+    small = dataclasses.replace(
+        c, block_size=u, **{x: getattr(c, x).view(3 * bs // u, 1, u, -1)
+                            for x in ("k", "v")})
+    first = T - 300
+    base = first // u * u
+    p = torch.arange(base, T, u, device="cuda")
+    st = ((bt[0].long()[p // bs] * bs + p % bs) // u).to(torch.int32)[None]
+    q = _randn(g, 7, 4, d)
+    got = K.gqa_cross(c, bt, _i32([T]), T, q, _starts([7]), 7,
+                      first=_i32([first]))
+    assert K.device_error() == 0
+    _check(got, _reference(small, st, [T - base], q, [7], _cross_sees(
+        [7], [T - base], [first - base])))
+    masks, pos = K.tree_plan(_i32([-1, 0, 0, 1, 2, 2, 4]), _i32([T - 7]),
+                             _starts([7]), 7)
+    for window in (0, 150):
+        got = K.gqa_tree(c, bt, _i32([T]), T, q, _starts([7]), 7, masks,
+                         positions=pos, window=window,
+                         window_start=_i32([first]))
+        assert K.device_error() == 0
+        lo = [max(first, x + 1 - window) if window else first
+              for x in pos.tolist()]
+        _check(got, _reference(small, st, [T - base], q, [7], _tree_sees(
+            [7], [T - base - 7], masks, 1, [x - base for x in lo])))
+
+
 def test_streams_graphs_and_repeats():
     case = ("bf16", 128, 16, 2, 64, [20, 33], [3000, 900], 33)
     c, bt, lens, masks, pos, q = _setup(case, 37)
