@@ -181,7 +181,8 @@ kvd_status kvd_kv_read(const kvd_cache *cache, const int32_t *block_table,
  * finite groups only; where a caller's own bytes hold a NaN scale of V, rows
  * of the same sequence that do not see the position may become NaN as well.
  * Supported: an MXFP4 cache (head_dim 128), n_h / n_kv of 1 .. 128, at most
- * 1024 sequences a call. seqs->flags must be valid and are ignored.
+ * 1024 sequences a call, lengths up to 2^31 - 256 (longer ones are taken as
+ * that and flagged KVD_DEVERR_LEN). seqs->flags must be valid and are ignored.
  */
 kvd_status kvd_gqa_extend(const kvd_cache *cache, const kvd_seqs *seqs,
                           const int32_t *row_start, int32_t max_rows,

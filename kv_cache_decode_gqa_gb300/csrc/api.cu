@@ -1479,7 +1479,8 @@ kvd_status kvd_gqa_extend(const kvd_cache *cache, const kvd_seqs *seqs,
   p.block_size = cache->block_size;
   p.num_blocks = cache->num_blocks;
   p.max_blocks = seqs->max_blocks_per_seq;
-  p.max_seq_len = seqs->max_seq_len;
+  // (the kernels round positions up to whole chunks in 32 bits)
+  p.max_seq_len = std::min(seqs->max_seq_len, INT32_MAX - 255);
   p.window = seqs->window;
   p.win_start = seqs->window_start;
   p.row_start = row_start;

@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(FCfg<HP, CH, RT, W>::THREADS, 1)
           for (int k = q; k < nb; k += L) {
             if (k >= L) pb = block_of(cur.b, b0 + k);
             const int lb = (b0 + k) * bs;
-            const int a0 = max(t0, lb), a1 = min(t1, lb + bs);
+            // (a last block may end past 2^31)
+            const int a0 = max(t0, lb), a1 = (int)min((long)t1, (long)lb + bs);
             const long row = ((long)pb * p.n_kv + cur.h * HP) * bs + (a0 - lb);
             const int off = s * C::STAGE + (a0 - tok) * kRow;
             // whole blocks of a chunk's length hold the unit's heads side by

@@ -752,11 +752,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           t0 = max(c * kN, k.lo) & ~1;
           t1 = (min((c + 1) * kN, k.hi) + 1) & ~1;
           const int lb = t0 / bs + lq;
-          x0 = max(t0, lb * bs);
-          x1 = min(t1, (lb + 1) * bs);
+          const long b0 = (long)lb * bs;  // a last block may end past 2^31
+          x0 = (int)min(max((long)t0, b0), (long)t1);
+          x1 = (int)min((long)t1, b0 + bs);
           if (x0 < x1)
-            at = (((long)block_of(lb) * p.n_kv + h) * bs - (long)lb * bs) *
-                 kRow;
+            at = (((long)block_of(lb) * p.n_kv + h) * bs - b0) * kRow;
         }
         const int cnt = min(batch, c1 - cb);
         for (int j = 0; go && j < cnt; ++j) {
@@ -778,16 +778,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                   long off = at;
                   if (m > lq) {  // blocks of 2 positions: a lane has several
                     const int lb = t0 / bs + m;
-                    a0 = max(u0, lb * bs), a1 = min(u1, (lb + 1) * bs);
+                    const long b0 = (long)lb * bs;
+                    a0 = (int)min(max((long)u0, b0), (long)u1);
+                    a1 = (int)min((long)u1, b0 + bs);
                     if (a0 < a1)
-                      off = (((long)block_of(lb) * p.n_kv + h) * bs -
-                             (long)lb * bs) * kRow;
+                      off = (((long)block_of(lb) * p.n_kv + h) * bs - b0) *
+                            kRow;
                   }
                   if (a0 < a1)
                     bulk_g2s(dst + (a0 - base) * kRow,
                              src + off + (long)a0 * kRow,
                              (uint32_t)(a1 - a0) * kRow, bar);
-                  if (L < 32 || (m + L) * bs + t0 / bs * bs >= t1) break;
+                  if (L < 32 || (long)(t0 / bs + m + L) * bs >= t1) break;
                 }
               };
               if (PAIR && q == 0) {

@@ -1249,3 +1249,43 @@ def test_extend_many_calls_give_the_same_bits(counts, lens, n_h):
     assert all(torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
                for o in outs)
     assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 2, 20, 60])
+@pytest.mark.parametrize("bs", [6, 512, 10 ** 6])
+def test_extend_at_the_longest_lengths(bs, rows):
+    """2^31 - 256 positions, through a table that repeats three blocks, whose
+    last block ends past 2^31; rows see the last few hundred. Longer lengths
+    are flagged."""
+    T = 2 ** 31 - 256
+    g = _gen(bs + rows)
+    kv = []
+    for _ in range(2):
+        codes = torch.randint(0, 256, (3, 1, bs, D // 2), generator=g,
+                              device="cuda", dtype=torch.uint8)
+        sc = 0.05 + 0.5 * torch.rand((3, 1, bs, D // 16), generator=g,
+                                     device="cuda")
+        kv.append(torch.cat([codes, sc.to(torch.float8_e4m3fn).view(
+            torch.uint8)], -1))
+    c = K.PagedCache(*kv, bs, 1, D, "mxfp4")
+    blocks = -(-(2 ** 31 - 1) // bs)
+    bt = (torch.arange(blocks, device="cuda", dtype=torch.int32) % 3)[None]
+    # the same rows as a short sequence, in blocks that divide the long ones
+    u = math.gcd(bs, 64)
+    k, v = (x.view(3 * bs // u, 1, u, -1) for x in (c.k, c.v))
+    small = K.PagedCache(k, v, u, 1, D, "mxfp4")
+    first = T - 300
+    base = first // u * u
+    p = torch.arange(base, T, u, device="cuda")
+    st = ((bt[0].long()[p // bs] * bs + p % bs) // u).to(torch.int32)[None]
+    q = _randn(g, rows, 8, D)
+    for window in (0, 150):
+        args = (q, _starts([rows]), rows)
+        out, lse = K.gqa_extend(c, bt, _i32([T]), 2 ** 31 - 1, *args,
+                                window=window, window_start=_i32([first]))
+        assert K.device_error() == 0
+        _check(out, lse, _attend_ref(small, st, [T - base], [rows], q, window,
+                                     [first - base]))
+        K.gqa_extend(c, bt, _i32([T + 1]), 2 ** 31 - 1, *args, window=window,
+                     window_start=_i32([first]))
+        assert K.device_error() == K.DEVERR_LEN

@@ -713,7 +713,7 @@ def test_cache_beyond_32_bit_offsets():
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp8", 64), ("fp8", 128),
                                      ("mxfp4", 128)])
-@pytest.mark.parametrize("bs", [100, 512, 10 ** 6])
+@pytest.mark.parametrize("bs", [6, 100, 512, 10 ** 6])
 def test_the_longest_lengths(dtype, d, bs):
     """2^31 - 256 positions, through a table that repeats three blocks, whose
     last block ends past 2^31; rows see the last few hundred."""
