@@ -921,7 +921,8 @@ class CacheList:
             raise ValueError("a CacheList needs a cache")
         self.structs = (_native.KvdCache * len(self.caches))(
             *[c.struct() for c in self.caches])
-        tensors = [t for c in self.caches for t in (c.k, c.v)]
+        # (the caches may be given others: the structs point to these)
+        self.tensors = tensors = [t for c in self.caches for t in (c.k, c.v)]
         # (one tensor may be both K and V of a cache)
         at = [{t.data_ptr() for t in (c.k, c.v) if t is not None}
               for c in self.caches]

@@ -2,7 +2,9 @@
 fp64 formulas. Tolerances are sums of the roundings each result goes
 through."""
 import dataclasses
+import gc
 import math
+import weakref
 
 import numpy as np
 import pytest
@@ -897,6 +899,27 @@ def test_a_tensor_listed_twice_is_refused():
             K.CacheList([x, y])
     assert len(K.CacheList([cache(a, a), cache(b, b)]).caches) == 2
     assert len(K.CacheList([cache(a, b), cache(c, d)]).caches) == 2
+
+
+def test_a_cache_list_keeps_the_tensors_it_points_to():
+    """A layer that is given other tensors leaves the list the old ones: their
+    memory is not handed out while the list's calls may write it."""
+    g = _gen(8)
+    bt, blocks = _table(g, [64], 16)
+    c = _cache(g, blocks, 2, 16, "bf16", 64)
+    old = [weakref.ref(c.k), weakref.ref(c.v)]
+    want = [t.clone() for t in (c.k, c.v)]
+    for t in want:
+        t[bt[0, 0].item(), :, 3] = t[bt[0, 1].item(), :, 4]
+    layers = K.CacheList([c])
+    new = [torch.zeros_like(c.k), torch.zeros_like(c.v)]
+    c.k, c.v = new
+    gc.collect()
+    assert all(r() is not None for r in old)
+    K.kv_keep(layers, bt, _i32([3]), _i32([[17]]), _i32([1]))
+    assert all(torch.equal(r(), w) for r, w in zip(old, want))
+    assert not any(bool(t.any()) for t in new)
+    assert K.device_error() == 0
 
 
 def test_kv_keep_long_paths():
