@@ -396,6 +396,50 @@ def test_what_lies_past_the_lengths_is_not_used(dtype):
     assert K.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype,d", [("fp8", 128), ("fp8", 64),
+                                     ("mxfp4", 128)])
+def test_probabilities_beside_f16_values_are_f16(dtype, d):
+    """Few positions, so that their roundings show: over fp8 and MXFP4 caches
+    the probabilities are off by half a step of f16, which bf16's would
+    exceed."""
+    lens, n, n_h, n_kv, bs = [2, 3, 4, 2, 5], [40] * 5, 32, 4, 16
+    g = _gen(79 + d)
+    bt, blocks = _table(g, lens, bs)
+    c = _cache(g, blocks, n_kv, bs, dtype, d)
+    q = _randn(g, sum(n), n_h, d) * 0.2
+    out, lse = K.gqa_cross(c, bt, _i32(lens), max(lens), q, _starts(n), 40)
+    o, l, _, ltol = _reference(c, bt, lens, q, n, _cross_sees(n, lens, None))
+    worst, at = 0.0, 0
+    for b, (k, T) in enumerate(zip(n, lens)):
+        pos = torch.arange(T, device="cuda")
+        blk, slot = bt[b].long()[pos // bs], pos % bs
+        kk, vv = _rows64(c, 0, blk, slot), _rows64(c, 1, blk, slot)
+        x = q[at:at + k].double().view(k, n_kv, n_h // n_kv, d)
+        s = torch.einsum("rhgd,phd->rhgp", x, kk) * d ** -0.5
+        mag = torch.einsum("rhgd,phd->rhgp", x.abs(), kk.abs()).amax(
+            -1) * d ** -0.5
+        p = torch.softmax(s, -1)
+        ov = torch.einsum("rhgp,phd->rhgd", p, vv.abs())
+        # as in _reference, with a probability off by 2^-11, or by 2^-25
+        # below f16's normal range where the largest is 2^7 or more
+        ds = (d + 8) * 2.0 ** -23 * mag + 2.0 ** -22
+        acc = (T + 64) * 2.0 ** -24
+        tol = HALF_BF16 * o[at:at + k].abs() + (
+            (2.0 ** -11 + 2 * ds + 2 * acc)[..., None] * ov +
+            2.0 ** -32 * vv.abs().sum(0)[None, :, None]).reshape(k, n_h, d)
+        err = (out[at:at + k].double() - o[at:at + k]).abs()
+        assert bool((err <= tol).all()), (err / tol).max().item()
+        # the same with the weights relative to the largest in bf16
+        w = p / p.amax(-1, keepdim=True)
+        w = w.to(BF).double() / w.sum(-1, keepdim=True)
+        bad = torch.einsum("rhgp,phd->rhgd", w, vv).reshape(k, n_h, d)
+        worst = max(worst, ((bad - o[at:at + k]).abs() / tol).max().item())
+        at += k
+    assert bool(((lse.double() - l).abs() <= ltol).all())
+    assert worst > 1.5
+    assert K.device_error() == 0
+
+
 def test_masked_nodes_with_infinite_keys():
     """A node's key may be anything where a row's mask leaves it out."""
     case = ("bf16", 128, 8, 1, 64, [6], [130], 6)
@@ -919,6 +963,38 @@ def test_a_cache_list_keeps_the_tensors_it_points_to():
     K.kv_keep(layers, bt, _i32([3]), _i32([[17]]), _i32([1]))
     assert all(torch.equal(r(), w) for r, w in zip(old, want))
     assert not any(bool(t.any()) for t in new)
+    assert K.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("mxfp4", 128)])
+def test_kv_keep_beyond_32_bit_offsets(dtype, d):
+    """Rows move between blocks at byte offsets past 2^32 (and element offsets
+    past 2^31), and nothing else changes in either tensor."""
+    bs, n_kv = 64, 8
+    g = _gen(47)
+    row = 72 if dtype == "mxfp4" else 2 * d
+    blocks = 2 ** 32 // (bs * n_kv * row) * 2 + 40
+    bt = [[blocks - 1, blocks - 3, 7], [blocks - 9, 5, blocks - 2],
+          [3, blocks - 20, 1]]
+    some = _cache(g, 9, n_kv, bs, dtype, d)
+    kv = []
+    for t in (some.k, some.v):
+        x = torch.zeros((blocks, *t.shape[1:]), dtype=t.dtype, device="cuda")
+        for i, b in enumerate(sum(bt, [])):
+            x[b] = t[i]
+        kv.append(x)
+    c = K.PagedCache(*kv, bs, n_kv, d, dtype)
+    start, path = [60, 20, 0], [[1, 6, 70], [0, 90, 120], [64, 65, 127]]
+    want = [x.clone() for x in kv]
+    for w, x in zip(want, kv):
+        for b in range(3):
+            for j, i in enumerate(path[b]):
+                p, t = start[b] + i, start[b] + j
+                w[bt[b][t // bs], :, t % bs] = x[bt[b][p // bs], :, p % bs]
+    K.kv_keep([c], _i32(bt), _i32(start), _i32(path), _i32([3, 3, 3]))
+    for x, w, t in zip(kv, want, (some.k, some.v)):
+        assert torch.equal(x, w)
+        assert not torch.equal(x[blocks - 1], t[0])
     assert K.device_error() == 0
 
 
