@@ -1142,7 +1142,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
       // whose bits are not in `seen` are filled behind the copies of the next
       // one, and before any wait.
       int ends_slot = -1;
-      uint32_t seen[4] = {};
+      uint32_t seen = 0;  // lane w: of rows [32 w, 32 w + 32)
       uint32_t par = 0;  // parities of `land`, a bit a slot
       auto fill_ends = [&]() {
         if (ends_slot < 0) return;
@@ -1154,23 +1154,19 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         }
         par ^= 1u << s;
         uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
-        constexpr int PC = D / 8;  // 16-byte pieces of a row, a lane each
-        const int e = lane % PC;
-#pragma unroll
+        // a lane a 16-byte piece of a row, AT rows at a time
+        constexpr int PC = D / 8, AT = 32 / PC;
+        const int r0 = lane / PC, e = lane % PC;
+        uint8_t *piece = tile + (e >> 3) * C::COLS + r0 * 128 + (e & 7) * 16;
+#pragma unroll 1
         for (int w = 0; w < 4; ++w) {
-          for (uint32_t m = ~seen[w]; m != 0;) {
-            int r = -1;  // this lane's row of the next 32 / PC
+          const uint32_t m = ~__shfl_sync(0xffffffffu, seen, w);
+          if (m == 0) continue;
+          uint8_t *at = piece + (w >> 1) * C::HALF + (w & 1) * 32 * 128;
 #pragma unroll
-            for (int k = 0; k < 32 / PC; ++k) {
-              if (k == lane / PC && m != 0) r = 32 * w + __ffs(m) - 1;
-              m &= m - 1;
-            }
-            if (r >= 0)
-              *reinterpret_cast<uint4 *>(tile + (r >> 6) * C::HALF +
-                                         (e >> 3) * C::COLS + (r & 63) * 128 +
-                                         (e & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-          }
+          for (int k = 0; k < 32; k += AT)
+            if (m >> r0 >> k & 1)
+              *reinterpret_cast<uint4 *>(at + k * 128) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1282,24 +1278,23 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
               }
             }
             __syncwarp();
+            auto look = [&]() {
+              uint32_t bits = 0;
+#pragma unroll 1
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t x =
+                    seen_by_some(p, sg.q, first, p0 + 32 * w, lane);
+                if (lane == w) bits = x;
+              }
+              return bits;
+            };
             if constexpr (!WIDEN) {
               fill_ends();
-              if (ends) {
-                ends_slot = s;
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                  seen[w] =
-                      seen_by_some(p, sg.q, first, p0 + 32 * w, lane);
-              }
+              if (ends) ends_slot = s, seen = look();
             } else {
               if (q == 1) {
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  const uint32_t bits =
-                      ends ? seen_by_some(p, sg.q, first, p0 + 32 * w, lane)
-                           : 0xffffffffu;
-                  if (lane == w) seen_v[4 * s + w] = bits;
-                }
+                const uint32_t bits = ends ? look() : 0xffffffffu;
+                if (lane < 4) seen_v[4 * s + lane] = bits;
                 __syncwarp();
               }
               // (copies may have landed by now: the phase ends with this
