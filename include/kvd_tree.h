@@ -86,10 +86,12 @@ kvd_status kvd_tree_plan(const int32_t *parents, const int32_t *start,
  * step. Positions that no row of a sequence sees (nodes that no mask has,
  * context before every row's window) may hold anything; a value of V that is
  * not finite, at a position that some row of the sequence sees, may show in
- * rows that see other positions only (rows that see nothing stay 0). Supported: bf16 and fp8 caches with head_dim
- * 64 or 128 and MXFP4 caches, n_h / n_kv of 1 .. 128, at most 1024 sequences a
- * call, bf16 caches of less than 2^31 rows (blocks x heads x slots) with K and
- * V less than 2^40 bytes apart, lengths up to 2^31 - 256. seqs->flags must be valid and are ignored.
+ * rows that see other positions only (rows that see nothing stay 0).
+ * Supported: bf16 and fp8 caches with head_dim 64 or 128 and MXFP4 caches,
+ * n_h / n_kv of 1 .. 128, at most 1024 sequences a call, bf16 caches of less
+ * than 2^31 rows (blocks x heads x slots), lengths up to 2^31 - 256. K and V of a
+ * bf16 cache that lie 2^40 bytes or more apart must both be device memory (else
+ * KVD_ERR_UNSUPPORTED). seqs->flags must be valid and are ignored.
  */
 kvd_status kvd_gqa_tree(const kvd_cache *cache, const kvd_seqs *seqs,
                         const int32_t *row_start, int32_t max_rows,

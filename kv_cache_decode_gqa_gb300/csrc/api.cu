@@ -1502,6 +1502,15 @@ kvd_status kvd_gqa_extend(const kvd_cache *cache, const kvd_seqs *seqs,
 // ===========================================================================
 namespace {
 
+bool device_memory(const void *p) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    (void)cudaGetLastError();  // not left for the next call to report
+    return false;
+  }
+  return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
+}
+
 // What kvd_gqa_tree, kvd_gqa_cross and their workspace sizing check alike.
 kvd_status check_attend(const kvd_cache *c, const kvd_seqs *s, int rows,
                         int max_rows, int n_h, bool lists, const char *what) {
@@ -1537,12 +1546,14 @@ kvd_status check_attend(const kvd_cache *c, const kvd_seqs *s, int rows,
     return fail(KVD_ERR_UNSUPPORTED, "%s: bf16 caches of 2^31 rows (blocks x "
                 "heads x slots) and more", what);
   if (c->dtype == KVD_BF16) {
-    // one tensor map holds both, the other a stride away
+    // Allocations may lie that far apart; a device and a host pointer, passed by
+    // mistake, do as a rule.
     const uint64_t k = reinterpret_cast<uint64_t>(c->k);
     const uint64_t v = reinterpret_cast<uint64_t>(c->v);
-    if ((k < v ? v - k : k - v) >> 40)
-      return fail(KVD_ERR_UNSUPPORTED, "%s: K and V of a bf16 cache must lie "
-                  "less than 2^40 bytes apart", what);
+    if ((k < v ? v - k : k - v) >> 40 &&
+        !(device_memory(c->k) && device_memory(c->v)))
+      return fail(KVD_ERR_UNSUPPORTED, "%s: K and V of a bf16 cache lie 2^40 "
+                  "bytes or more apart and are not both device memory", what);
   }
   return KVD_OK;
 }

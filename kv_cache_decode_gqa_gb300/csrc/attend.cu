@@ -92,12 +92,13 @@ cudaError_t launch_merge(const AttendParams &p, cudaStream_t s) {
                     grid, dim3(kAttendMergeThreads), 0, s, 1, p);
 }
 
-// A bf16 cache's K and V as [which][column half][row][64 columns], in swizzled
-// boxes of `box` rows (of all columns where box is 64) of one of them.
-bool cache_map(CUtensorMap *map, const AttendParams &p, int box) {
+// Two tensors of a bf16 cache (or one, twice) as [which][column half][row][64
+// columns], in swizzled boxes of `box` rows (of all columns where box is 64) of
+// one of them.
+bool cache_map(CUtensorMap *map, const AttendParams &p, const uint8_t *lo,
+               const uint8_t *hi, int box) {
   const auto encode = tensor_map_encoder();
   if (!encode) return false;
-  const uint8_t *lo = std::min(p.k, p.v), *hi = std::max(p.k, p.v);
   const cuuint64_t d = p.dk;
   const cuuint64_t dims[4] = {
       64, (cuuint64_t)p.num_blocks * p.n_kv * p.block_size, d / 64,
@@ -159,9 +160,18 @@ cudaError_t launch_attend(const AttendParams &p, cudaStream_t s) {
   if (p.dtype == DT_BF16) {
     // boxes of rows that lie within a block and within half a chunk
     tp.box = std::min(64, p.block_size & -p.block_size);
-    if (!cache_map(&tp.map, p, tp.box)) return cudaErrorNotSupported;
-    tp.which[0] = p.v < p.k;
-    tp.which[1] = p.k < p.v;
+    const uint8_t *lo = std::min(p.k, p.v), *hi = std::max(p.k, p.v);
+    tp.far = (hi - lo) >> 40 != 0;
+    if (!tp.far) {
+      // (one map: half the encoding, and K and V share its fetch)
+      if (!cache_map(&tp.map[0], p, lo, hi, tp.box))
+        return cudaErrorNotSupported;
+      tp.which[0] = p.v < p.k;
+      tp.which[1] = p.k < p.v;
+    } else if (!cache_map(&tp.map[0], p, p.k, p.k, tp.box) ||
+               !cache_map(&tp.map[1], p, p.v, p.v, tp.box)) {
+      return cudaErrorNotSupported;
+    }
     e = p.dk == 128 ? launch_attend_t<DT_BF16, 128, 2>(tp, s)
                     : launch_attend_t<DT_BF16, 64, 2>(tp, s);
   } else {

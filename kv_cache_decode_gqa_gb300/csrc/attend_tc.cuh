@@ -72,9 +72,11 @@ namespace kvd {
 struct TcParams {
   AttendParams p;
   // bf16 caches: [which][column half][row][64 columns], of K and V the one that
-  // lies first first
-  CUtensorMap map;
+  // lies first first; or one map each where they lie further apart than a map's
+  // strides reach
+  CUtensorMap map[2];
   int which[2];  // K's and V's
+  int far;       // whether V has a map of its own
   int box;  // rows of its boxes: 1 .. 64, a power of two
 };
 
@@ -533,7 +535,8 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
     mbar_init(drain, 2);
     fence_mbar_init();
   }
-  if (!WIDEN && warp == C::kLoad && lane == 0) prefetch_tmap(&tp.map);
+  if (!WIDEN && (warp == C::kLoad || warp == C::kLoadV) && lane == 0)
+    prefetch_tmap(&tp.map[warp == C::kLoadV && tp.far]);
   if (warp == C::kMma) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
@@ -1246,6 +1249,7 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                                         (uint32_t)(n << bshift) * D * 2);
                 uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
                 const int kv = tp.which[q];
+                const CUtensorMap *map = &tp.map[q && tp.far];
                 for (int i = lq; i * tp.box < kN; i += L) {
                   int a0 = x0, a1 = x1;
                   long row = at;
@@ -1254,12 +1258,12 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
                   const int o = i * tp.box;  // row of the chunk
                   uint8_t *dst = tile + (o >> 6) * C::HALF + (o & 63) * 128;
                   if (tp.box == 64) {
-                    tma_load_4d(dst, &tp.map, 0, (int)row, 0, kv, bar);
+                    tma_load_4d(dst, map, 0, (int)row, 0, kv, bar);
                   } else {
 #pragma unroll
                     for (int z = 0; z < D / 64; ++z)
-                      tma_load_4d(dst + z * C::COLS, &tp.map, 0, (int)row, z,
-                                  kv, bar);
+                      tma_load_4d(dst + z * C::COLS, map, 0, (int)row, z, kv,
+                                  bar);
                   }
                 }
               } else {

@@ -729,6 +729,32 @@ def test_keys_and_values_in_one_tensor():
     assert K.device_error() == 0
 
 
+def test_keys_and_values_far_apart():
+    """Allocations may lie anywhere: here those of some tens of MB lie 2^48
+    bytes below larger ones."""
+    torch.cuda.empty_cache()
+    some = [torch.empty(mb << 19, dtype=BF, device="cuda")
+            for mb in [*range(21, 121, 3), 200, 400, 1000, 2000]]
+    at = [t.data_ptr() for t in some]
+    ends = [some[at.index(f(at))] for f in (min, max)]
+    if max(at) - min(at) < 2 ** 40:
+        pytest.skip("no two allocations that far apart")
+    n, past, bound = [20, 40], [3000, 64], 40
+    for d in (64, 128):
+        case = ("bf16", d, 8, 2, 16, n, past, bound)
+        c, bt, lens, masks, _, q = _setup(case, 83)
+        args = (bt, _i32(lens), max(lens), q, _starts(n), bound)
+        want = K.gqa_tree(c, *args, masks), K.gqa_cross(c, *args)
+        low, high = (t[:c.k.numel()].view(c.k.shape) for t in ends)
+        for k, v in ((low, high), (high, low)):
+            k.copy_(c.k), v.copy_(c.v)
+            x = dataclasses.replace(c, k=k, v=v)
+            got = K.gqa_tree(x, *args, masks), K.gqa_cross(x, *args)
+            for a, b in zip(got, want):
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert K.device_error() == 0
+
+
 def test_cache_beyond_32_bit_offsets():
     """Blocks at byte offsets past 2^32 and element offsets past 2^31."""
     bs, n_kv, d, n, past = 64, 8, 128, [5, 12], [200, 70]
