@@ -4,6 +4,9 @@ through."""
 import dataclasses
 import gc
 import math
+import os
+import subprocess
+import sys
 import weakref
 
 import numpy as np
@@ -729,16 +732,15 @@ def test_keys_and_values_in_one_tensor():
     assert K.device_error() == 0
 
 
-def test_keys_and_values_far_apart():
-    """Allocations may lie anywhere: here those of some tens of MB lie 2^48
-    bytes below larger ones."""
-    torch.cuda.empty_cache()
+def _far_apart():
+    """Whether K and V could be placed 2^40 bytes and more apart, and then gave
+    what they give side by side."""
     some = [torch.empty(mb << 19, dtype=BF, device="cuda")
             for mb in [*range(21, 121, 3), 200, 400, 1000, 2000]]
     at = [t.data_ptr() for t in some]
     ends = [some[at.index(f(at))] for f in (min, max)]
     if max(at) - min(at) < 2 ** 40:
-        pytest.skip("no two allocations that far apart")
+        return False
     n, past, bound = [20, 40], [3000, 64], 40
     for d in (64, 128):
         case = ("bf16", d, 8, 2, 16, n, past, bound)
@@ -753,6 +755,20 @@ def test_keys_and_values_far_apart():
             for a, b in zip(got, want):
                 assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert K.device_error() == 0
+    return True
+
+
+def test_keys_and_values_far_apart():
+    """Allocations may lie anywhere: in a process that has made few, those of
+    some tens of MB lie 2^48 bytes below the others here."""
+    r = subprocess.run(
+        [sys.executable, "-c", "import tests.test_gpu_tree as t; "
+         "print('far' if t._far_apart() else 'near')"],
+        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+        capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    if r.stdout.split()[-1] == "near":
+        pytest.skip("no two allocations that far apart")
 
 
 def test_cache_beyond_32_bit_offsets():
