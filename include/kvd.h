@@ -188,7 +188,8 @@ typedef struct kvd_cache {
  * this step), or by kvd_gqa_append_decode itself. That holds in a decode
  * step, where older rows were appended by earlier steps; it does not hold
  * right after kvd_copy_blocks or kvd_kv_keep (kvd_tree.h), which write older
- * rows, nor after a kvd_kv_write (kvd_prompt.h) of more than each sequence's newest position.
+ * rows, nor after a kvd_kv_write (kvd_prompt.h) of more than each sequence's
+ * newest position.
  * kvd_gqa_decode, kvd_gqa_append_decode and kvd_indexer_topk may then start
  * copying those rows while that kernel finishes (the query rows, and
  * everything written, still wait for it); the CUDA-core decode kernel (query

@@ -111,6 +111,14 @@ kvd_status kvd_gqa_tree(const kvd_cache *cache, const kvd_seqs *seqs,
  *   max_rows   host: an upper bound on the rows of a sequence; it sizes the
  *              workspace
  *   other arguments and supported shapes as kvd_gqa_tree
+ * Without row_start this is what kvd_gqa_decode computes with window_start =
+ * s_b, for every group size and width here. For the shapes that both take,
+ * kvd_gqa_decode is faster where there are many kv heads and this call where
+ * there are few with groups of 2 and more (16 sequences of 1,060 states, us, this
+ * / that: 16 heads of 16 kv heads, head_dim 64, bf16 31 / 20, fp8 40 / 19; 32 of
+ * 32, 128, bf16 65 / 49; 32 of 8, 128, bf16 22 / 30, MXFP4 20 / 30; 64 of 8, 128,
+ * bf16 22 / 23); for groups of 1, 2 and 4 kvd_gqa_decode keeps the
+ * probabilities in fp32.
  */
 kvd_status kvd_gqa_cross(const kvd_cache *cache, const kvd_seqs *seqs,
                          const int32_t *row_start, int32_t max_rows,

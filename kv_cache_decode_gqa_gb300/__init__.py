@@ -888,7 +888,8 @@ def gqa_tree(cache, block_table, seq_lens, max_seq_len, q, row_start,
     bits its ``masks`` (int32 [rows][ceil(max_rows / 32)], from tree_plan or
     any other) have set. ``window`` bounds the context from the row's
     ``positions`` (int32 [rows], tree_plan) back, ``window_start`` from the
-    front. ``out`` must not overlap q. Rows of new outputs that no sequence owns
+    front. Positions that no row of a sequence sees may hold anything. ``out``
+    must not overlap q. Rows of new outputs that no sequence owns
     are not initialised."""
     return _attend(True, cache, block_table, seq_lens, max_seq_len, q,
                    row_start, max_rows, masks, positions, scale, out, lse,
@@ -904,7 +905,9 @@ def gqa_cross(cache, block_table, seq_lens, max_seq_len, q, row_start=None,
     cached positions [first[b], seq_lens[b]) (``first``: int32 [batch], None:
     from 0). Rows row_start[b] .. row_start[b + 1] - 1 belong to sequence b, at
     most ``max_rows`` of them (None: all rows, which fits any list); without
-    row_start row b is sequence b's one row."""
+    row_start row b is sequence b's one row, and gqa_decode(window_start=first)
+    computes the same for the shapes it takes (kvd_tree.h says which is faster
+    where)."""
     return _attend(False, cache, block_table, seq_lens, max_seq_len, q,
                    row_start, max_rows, None, None, scale, out, lse,
                    workspace, want_lse, 0, first)
@@ -937,7 +940,9 @@ def kv_keep(caches, block_table, start, path, n_keep):
     PagedCache objects to make one of) behind the context: position start[b] +
     j takes the row of start[b] + path[b][j], j < n_keep[b]. ``path``: int32
     [batch][width], ascending node indexes from the root on; ``start``,
-    ``n_keep``: int32 [batch]. The new lengths are start + n_keep."""
+    ``n_keep``: int32 [batch]. The new lengths are start + n_keep. Caches that
+    are no CacheList are checked in every call (0.13 ms for 32 layers, 0.30 for
+    80, where a call with a CacheList takes 9 us)."""
     import torch
     if not isinstance(caches, CacheList):
         caches = CacheList([caches] if isinstance(caches, PagedCache)

@@ -128,8 +128,13 @@ AttendPlan attend_plan(int n_kv, int g, int d, int batch, int rows,
                     kUnit);
   const long each = ((long)max_seq_len + kN - 1) / kN;
   const long chunks = units * each;
-  // Not cut where a CTA a unit then takes no more than a few chunks longer than
-  // equal shares would, which the merge launch costs.
+  // Not cut where a CTA a unit then takes no more than kMergeChunks chunks longer
+  // than equal shares would: the merge launch, which finds no room beside CTAs of
+  // this one, costs more. (Trees of 16 nodes of 8 heads a kv head, bf16, whole
+  // units against shares, us in a graph: 8 units of 3, 5 and 8 chunks 10.3 / 11.5,
+  // 11.9 / 21.8, 14.1 / 17.4; 64 units of 5, 8 and 14 chunks 12.6 / 28.4, 15.0 /
+  // 31.8, 19.5 / 31.6; 128 units of 18 and 32 chunks 55.2 / 55.5, 73.8 / 73.9; 8
+  // units of 32 chunks 42 / 21. fp8 alike.)
   if (units <= ctas && each <= chunks / ctas + kMergeChunks) {
     pl.whole_units = 1;
     pl.ctas = (int)std::max(1L, units);

@@ -40,11 +40,11 @@
 // against 2,576 for its products; with few, HBM, as long as that chain keeps
 // up (1,850 cycles a chunk of one tile, K and V of which take 2,900 at HBM's
 // rate). Measured (us, calls in a graph): 2,011 rows over 20,011 positions, 64
-// heads of 8 kv heads, bf16, 840 (1,570 TFLOP/s, 81% of cuBLAS's rate); trees
-// of 500 nodes in 16 sequences over 9,200 positions (620 MB) 185; of 250 nodes
-// in 32 sequences over 4,600 positions of an fp8 cache (310 MB) 102; of 480
-// nodes in 8 sequences over 18,400 positions of an MXFP4 cache 263; one tree of
-// 16 nodes over 4,000 positions 21.
+// heads of 8 kv heads, bf16, 840 and 881 on two GPUs (1,570 and 1,497 TFLOP/s, 81
+// and 77% of cuBLAS's rate); trees of 500 nodes in 16 sequences over 9,200
+// positions (620 MB) 185; of 250 nodes in 32 sequences over 4,600 positions of an
+// fp8 cache (310 MB) 102; of 480 nodes in 8 sequences over 18,400 positions of an
+// MXFP4 cache 251; one tree of 16 nodes over 4,000 positions 21.
 //
 // Measured and not kept (the first of these cases, us): two threads a pair and
 // step, of 32 columns each, 1,060 against 1,017 then (more warps to issue for,
@@ -1157,7 +1157,9 @@ __global__ void __launch_bounds__(ACfg<DT, D, QS>::THREADS, 1)
         }
         par ^= 1u << s;
         uint8_t *tile = smem + C::KV_OFF + s * C::TILE;
-        // a lane a 16-byte piece of a row, AT rows at a time
+        // a lane a 16-byte piece of a row, AT rows at a time (a loop over the
+        // set bits instead: one tree 23.6 us against 20.7, a unit's last tile
+        // waits for these stores)
         constexpr int PC = D / 8, AT = 32 / PC;
         const int r0 = lane / PC, e = lane % PC;
         uint8_t *piece = tile + (e >> 3) * C::COLS + r0 * 128 + (e & 7) * 16;
